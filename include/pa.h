@@ -21,6 +21,16 @@
  *                      paged cache, bottom-right-aligned causal mask
  *                      ("Prefill Forward Prefix Caching Explained", Facts 1-2
  *                      and the mask section).
+ * Operators around them, for a decode loop over a bounded cache (the pages have
+ * no counterpart beyond the glossary's sliding-window and sink bullets):
+ *   pa_norm_rope_store per-head RMS norm of q and k, position rotation, and the
+ *                      store of the new K/V rows (quantised for 8-bit caches).
+ *   pa_prefill_window  pa_prefill_varlen over a sliding window plus leading
+ *                      sink keys.
+ *   pa_decode_scored   pa_decode that also adds every key's attention weight to
+ *                      a score kept beside the cache.
+ *   pa_evict           cut sequences to a budget of keys by those scores and
+ *                      move the kept rows to the front.
  *
  * Conventions shared by every call
  *   - Every tensor pointer is a DEVICE pointer owned by the caller. The
@@ -31,7 +41,8 @@
  *     Decode launches may start while the previous launch of this library on
  *     the stream is finishing (programmatic dependent launch): they read
  *     context_lens and block_tables before waiting for it, and everything
- *     else after. No kernel of this library writes those two arrays; a
+ *     else after. No kernel of this library writes those two arrays (except
+ *     pa_evict its new_lens, complete before its last launch begins); a
  *     caller's own kernel that writes them and lets its dependents start
  *     early must not directly precede a decode call.
  *   - Argument errors are returned before anything is launched. A launch
@@ -86,6 +97,7 @@ typedef enum { PA_KV_BF16 = 0, PA_KV_FP8_E4M3 = 1, PA_KV_INT8 = 2 } pa_kv_dtype;
 #define PA_DEVERR_SLOT_RANGE 0x1u   /* store_kv: slot >= num_blocks*block_size, skipped */
 #define PA_DEVERR_WAIT_TIMEOUT 0x2u /* a kernel's bounded wait on a copy gave up */
 #define PA_DEVERR_BLOCK_RANGE 0x4u  /* block table entry outside [0, num_blocks), zero-filled */
+#define PA_DEVERR_POSITION_RANGE 0x8u /* norm_rope_store: position outside the table, skipped */
 
 /* A paged KV cache (one layer). Pointers are device pointers; the struct
  * itself is read on the host during the call and may live on the stack. */
@@ -122,6 +134,55 @@ const char* pa_status_string(pa_status status);
 pa_status pa_store_kv(const void* k, const void* v, const float* k_scale_new,
                       const float* v_scale_new, const int64_t* slot_mapping, int32_t num_tokens,
                       const pa_kv_cache* cache, void* stream);
+
+/* Norm and rotation parameters of pa_norm_rope_store. Pointers are device
+ * pointers; the struct itself is read on the host during the call. */
+typedef struct {
+  const void* q_weight;  /* (head_dim) bf16 norm weight of the query heads; NULL: no norm */
+  const void* k_weight;  /* (head_dim) bf16 norm weight of the key heads; NULL: no norm */
+  const float* cos_sin;  /* (max_positions, rotary_dim) fp32: rotary_dim/2 cosines, then the
+                            sines; may be NULL when rotary_dim is 0 */
+  int32_t max_positions;
+  int32_t rotary_dim;    /* leading dims of a head that are rotated: 0, or a multiple of 16 up
+                            to head_dim */
+  int32_t interleaved;   /* pair i is dims (2i, 2i+1); 0: dims (i, i + rotary_dim/2) */
+  float eps;             /* added to the mean square, >= 0 */
+} pa_norm_rope;
+
+/*
+ * pa_norm_rope_store - what happens to a layer's new q, k and v between the
+ * projection and the attention, in one launch: for every query and key head
+ *   n(x) = x * rsqrt(mean(x^2) + eps) * weight      (where a weight is given)
+ *   (a, b) -> (a cos - b sin, b cos + a sin)        (each pair of rotated dims)
+ * in fp32, q rounded once to bf16 into q_out, k (and v as it is) stored in the
+ * cache as by pa_store_kv.
+ *   q               (num_tokens, num_heads, head_dim) bf16; token t starts
+ *                   t * q_stride elements from q (a view of a fused projection's
+ *                   output), the heads of a token are contiguous.
+ *   k, v            (num_tokens, num_kv_heads, head_dim) bf16, likewise. Strides
+ *                   are multiples of 8 elements and at least one token's heads
+ *                   (PA_ERR_SHAPE).
+ *   positions       (num_tokens) int64: row of cos_sin. A position outside
+ *                   [0, max_positions) skips the token (q_out and cache left as
+ *                   they were) and sets PA_DEVERR_POSITION_RANGE. May be NULL
+ *                   when rotary_dim is 0.
+ *   slot_mapping    (num_tokens) int64 as for pa_store_kv. A negative slot is a
+ *                   padding token: nothing of it is written. A slot beyond the
+ *                   pool is flagged PA_DEVERR_SLOT_RANGE and its K/V skipped.
+ *   cache           bf16, or 8-bit: a row is stored as codes round(x / s) with
+ *                   s = max|x| / 448 (E4M3) or / 127 (INT8), 1 for a row of
+ *                   zeros, from the fp32 row, and s in k_scale / v_scale. A row
+ *                   with a NaN or an infinity reads back as NaN.
+ *   scores          NULL, or the (num_blocks, num_kv_heads, block_size) fp32
+ *                   scores of pa_decode_scored: the stored slots' are set to 0.
+ *   q_out           (num_tokens, num_heads, head_dim) bf16, contiguous. May be q
+ *                   itself when q is contiguous (else it must not overlap it).
+ */
+pa_status pa_norm_rope_store(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                             const void* v, int64_t v_stride, const pa_norm_rope* params,
+                             const int64_t* positions, const int64_t* slot_mapping,
+                             int32_t num_tokens, int32_t num_heads, const pa_kv_cache* cache,
+                             float* scores, void* q_out, void* stream);
 
 /*
  * pa_decode_workspace_size - bytes of device scratch pa_decode needs for this
@@ -183,6 +244,62 @@ pa_status pa_decode_window(const void* q, const pa_kv_cache* cache, const int32_
                            int32_t max_context_len, int32_t batch, int32_t num_heads,
                            float scale, int32_t window, int32_t sinks, void* out, void* workspace,
                            size_t workspace_bytes, void* stream);
+
+/*
+ * pa_decode_scored - pa_decode that also adds every key's softmax weight to a
+ * score: for each sequence, kv head g and key position p < context_len,
+ *   scores[slot(p), g] += sum over the query heads h of g of softmax_h(p)
+ * (fp32). The scores of heavily attended keys grow from step to step; pa_evict
+ * keeps the keys with the largest.
+ *   scores    (num_blocks, num_kv_heads, block_size) fp32, as the 8-bit scales.
+ *             Every visible slot gets one addition per call and sequence: scores
+ *             of sequences that share blocks sum over the sequences (in an order
+ *             that may change from call to call). Slots at or past context_len
+ *             are left as they were. pa_norm_rope_store can set a new slot's
+ *             score to zero.
+ *   workspace at least pa_decode_scored_workspace_size() bytes, contract as for
+ *             pa_decode. It holds the scores of every key: 4 bytes per query
+ *             head and key of the bound batch * max_context_len.
+ *   other arguments as pa_decode; out equals pa_decode's bit for bit. Batches
+ *   above 16384 return PA_ERR_UNSUPPORTED.
+ */
+size_t pa_decode_scored_workspace_size(const pa_kv_cache* cache, int32_t batch, int32_t num_heads,
+                                       int32_t max_blocks_per_seq, int32_t max_context_len);
+pa_status pa_decode_scored(const void* q, const pa_kv_cache* cache, const int32_t* block_tables,
+                           int32_t max_blocks_per_seq, const int32_t* context_lens,
+                           int32_t max_context_len, int32_t batch, int32_t num_heads, float scale,
+                           float* scores, void* out, void* workspace, size_t workspace_bytes,
+                           void* stream);
+
+/*
+ * pa_evict - cut sequences to `budget` keys per kv head. For a sequence of
+ * L = min(context_len, bound) > budget keys (bound: max_context_len or the
+ * block-table capacity), every kv head keeps the keys p < sinks, the keys
+ * p >= L - recent, and of the others the budget - sinks - recent with the
+ * largest scores (equal scores: the lowest p; a NaN counts as the largest).
+ * The kept rows of K, V, their scales and scores move, in order, to positions
+ * 0 .. budget-1 of the sequence's blocks; rows from budget on are left as they
+ * were, and the caller may free the blocks past them. A sequence of at most
+ * budget keys is left as it is.
+ *   scores         (num_blocks, num_kv_heads, block_size) fp32, moved like K.
+ *   budget         >= 1; sinks, recent >= 0, sinks + recent <= budget
+ *                  (else PA_ERR_SHAPE).
+ *   kept           (batch, num_kv_heads, budget) int32 out: the positions the
+ *                  rows came from, ascending; 0 .. L-1 and then -1 for a
+ *                  sequence left as it is.
+ *   new_lens       (batch) int32 out: min(L, budget). Not context_lens itself
+ *                  (PA_ERR_SHAPE): the lengths are read by several CTAs.
+ * Keys carry their rotation, and attention does not depend on the order of the
+ * keys, so decode calls over new_lens attend to exactly the kept keys; a later
+ * token's position (for the rotation) is the caller's to keep counting. The
+ * blocks of a cut sequence must not be shared with another sequence. A physical
+ * block id out of range sets PA_DEVERR_BLOCK_RANGE; scores there count as 0 and
+ * rows there are not moved.
+ */
+pa_status pa_evict(const pa_kv_cache* cache, float* scores, const int32_t* block_tables,
+                   int32_t max_blocks_per_seq, const int32_t* context_lens,
+                   int32_t max_context_len, int32_t batch, int32_t budget, int32_t sinks,
+                   int32_t recent, int32_t* kept, int32_t* new_lens, void* stream);
 
 /*
  * pa_decode_append - one decode step's store and attention in one call: the
@@ -259,6 +376,27 @@ pa_status pa_prefill_varlen(const void* q, const pa_kv_cache* cache, const int32
                             const int32_t* cu_seqlens_k, int32_t batch, int32_t num_heads,
                             int32_t total_q, int32_t max_q_len, float scale, void* out,
                             void* stream);
+
+/*
+ * pa_prefill_window - pa_prefill_varlen over a sliding window with attention
+ * sinks: query row i, at position p = i + (kv_len - q_len), sees the keys
+ * j <= p with j < sinks or j > p - window.
+ *   window   >= 1 (PA_ERR_SHAPE otherwise); a window of kv_len keys or more is
+ *            pa_prefill_varlen's mask.
+ *   sinks    >= 0 (PA_ERR_SHAPE if negative).
+ *   other arguments, support and arithmetic as pa_prefill_varlen, with P as two
+ *   bf16 terms on every tile where window + sinks < 128.
+ * Blocks that hold no key visible to a 128-row query tile pair are not read, nor
+ * their table entries, so the blocks of keys no row of the call sees may have
+ * been freed. K and V there, and in keys of a partly visible block that no row
+ * of the pair sees, may hold anything. V of a key that some row of a pair sees
+ * must be finite: a row that does not see it gives it the weight 0.
+ */
+pa_status pa_prefill_window(const void* q, const pa_kv_cache* cache, const int32_t* block_tables,
+                            int32_t max_blocks_per_seq, const int32_t* cu_seqlens_q,
+                            const int32_t* cu_seqlens_k, int32_t batch, int32_t num_heads,
+                            int32_t total_q, int32_t max_q_len, float scale, int32_t window,
+                            int32_t sinks, void* out, void* stream);
 
 /*
  * pa_decode_noalloc - pa_decode for callers that cannot allocate device memory.

@@ -8,7 +8,9 @@ every call raises (build it with ``python -m paged_kv_cache_186_gb300.build``).
 
 Names follow the C ABI: store_kv, decode, decode_window, decode_append,
 decode_workspace_size, prefill_varlen, decode_noalloc, get_device_error,
-debug_inject_wait_timeout.
+debug_inject_wait_timeout; for a decode loop over a bounded cache:
+norm_rope_store, prefill_window, decode_scored, decode_scored_workspace_size,
+evict.
 """
 from __future__ import annotations
 
@@ -27,6 +29,7 @@ PA_KV_INT8 = 2
 PA_DEVERR_SLOT_RANGE = 0x1
 PA_DEVERR_WAIT_TIMEOUT = 0x2
 PA_DEVERR_BLOCK_RANGE = 0x4
+PA_DEVERR_POSITION_RANGE = 0x8
 
 STATUS = {0: "PA_OK", 1: "PA_ERR_NULL", 2: "PA_ERR_SHAPE", 3: "PA_ERR_DTYPE",
           4: "PA_ERR_UNSUPPORTED", 5: "PA_ERR_CUDA", 6: "PA_ERR_WORKSPACE", 7: "PA_ERR_ALIGN",
@@ -38,7 +41,8 @@ DECODE_NOALLOC_SCRATCH_BYTES = 32 << 20
 # Every symbol include/pa.h declares.
 EXPORTED = ("pa_abi_version", "pa_status_string", "pa_store_kv", "pa_decode_workspace_size",
             "pa_decode", "pa_decode_window", "pa_decode_append", "pa_decode_window_append",
-            "pa_prefill_varlen",
+            "pa_prefill_varlen", "pa_norm_rope_store", "pa_prefill_window", "pa_decode_scored",
+            "pa_decode_scored_workspace_size", "pa_evict",
             "pa_decode_noalloc", "pa_get_device_error", "pa_debug_inject_wait_timeout")
 
 
@@ -55,6 +59,14 @@ class KVCache(ctypes.Structure):
                 ("dtype", ctypes.c_int32), ("k_cache", ctypes.c_void_p),
                 ("v_cache", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
                 ("v_scale", ctypes.c_void_p)]
+
+
+class NormRope(ctypes.Structure):
+    """Mirror of pa_norm_rope."""
+    _fields_ = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p),
+                ("cos_sin", ctypes.c_void_p), ("max_positions", ctypes.c_int32),
+                ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+                ("eps", ctypes.c_float)]
 
 
 _lib = None
@@ -101,7 +113,20 @@ def lib() -> ctypes.CDLL:
     L.pa_get_device_error.argtypes = [ctypes.POINTER(ctypes.c_uint32)]
     L.pa_debug_inject_wait_timeout.restype = ctypes.c_int
     L.pa_debug_inject_wait_timeout.argtypes = [i32, ctypes.c_uint64]
-    del i64
+    cache = ctypes.POINTER(KVCache)
+    L.pa_norm_rope_store.restype = ctypes.c_int
+    L.pa_norm_rope_store.argtypes = [P, i64, P, i64, P, i64, ctypes.POINTER(NormRope), P, P, i32,
+                                     i32, cache, P, P, P]
+    L.pa_prefill_window.restype = ctypes.c_int
+    L.pa_prefill_window.argtypes = [P, cache, P, i32, P, P, i32, i32, i32, i32, ctypes.c_float,
+                                    i32, i32, P, P]
+    L.pa_decode_scored_workspace_size.restype = ctypes.c_size_t
+    L.pa_decode_scored_workspace_size.argtypes = [cache, i32, i32, i32, i32]
+    L.pa_decode_scored.restype = ctypes.c_int
+    L.pa_decode_scored.argtypes = [P, cache, P, i32, P, i32, i32, i32, ctypes.c_float, P, P, P,
+                                   ctypes.c_size_t, P]
+    L.pa_evict.restype = ctypes.c_int
+    L.pa_evict.argtypes = [cache, P, P, i32, P, i32, i32, i32, i32, i32, P, P, P]
     _lib = L
     return L
 
@@ -125,6 +150,45 @@ def _stream():
 def _check(code: int, what: str):
     if code != 0:
         raise PAError(code, what)
+
+
+def _want(t: torch.Tensor, name: str, dtype: torch.dtype, shape, contiguous: bool = True):
+    """Refuse a tensor of another type, shape or layout than a call reads or writes."""
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if contiguous and not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+
+
+def _checked_cache(k_cache, v_cache, k_scale, v_scale, *others) -> KVCache:
+    """make_cache of caches that agree with each other, on one device with `others`."""
+    if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype or k_cache.dim() != 4:
+        raise ValueError("k_cache and v_cache must have the same 4-D shape and dtype")
+    if (k_scale is None) != (v_scale is None):
+        raise ValueError("k_scale and v_scale come together")
+    if k_scale is not None:
+        shape = (k_cache.shape[0], k_cache.shape[2], k_cache.shape[1])
+        _want(k_scale, "k_scale", torch.float32, shape)
+        _want(v_scale, "v_scale", torch.float32, shape)
+    cache = make_cache(k_cache, v_cache, k_scale, v_scale)
+    dev = k_cache.device
+    if dev.type != "cuda":
+        raise ValueError("the tensors must be on a CUDA device")
+    for t in (v_cache, k_scale, v_scale) + others:
+        if t is not None and t.device != dev:
+            raise ValueError(f"all tensors must be on {dev}, got one on {t.device}")
+    return cache
+
+
+def _run(device: torch.device, what: str, fn, *args) -> None:
+    """fn(*args, stream) on the tensors' device and its current stream."""
+    if device.index == torch.cuda.current_device():
+        _check(fn(*args, _stream()), what)
+    else:
+        with torch.cuda.device(device):
+            _check(fn(*args, _stream()), what)
 
 
 def make_cache(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor | None = None,
@@ -283,6 +347,180 @@ def prefill_varlen(q, k_cache, v_cache, block_tables, cu_seqlens_q, cu_seqlens_k
                                    int(max_q_len), float(scale), _ptr(out), _stream()),
            "pa_prefill_varlen")
     return out
+
+
+def _token_rows(t: torch.Tensor, name: str, heads, head_dim: int):
+    """(tensor, element stride between its tokens) of (T, heads, head_dim) bf16 whose tokens'
+    heads are contiguous: a view of a fused projection's output is taken as it is, any other
+    layout is copied."""
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
+    if t.dim() != 3 or t.shape[2] != head_dim or (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name} must have shape (tokens, "
+                         f"{'heads' if heads is None else heads}, {head_dim}), got "
+                         f"{tuple(t.shape)}")
+    T, H, D = t.shape
+    st, sh, sd = t.stride()
+    if T == 1:
+        st = H * D
+    if (sd != 1 or (H > 1 and sh != D) or st < H * D or st % 8 != 0 or t.data_ptr() % 16 != 0):
+        return t.clone(memory_format=torch.contiguous_format), H * D
+    return t, st
+
+
+def norm_rope_store(q, k, v, positions, slot_mapping, k_cache, v_cache, *, q_weight=None,
+                    k_weight=None, eps: float = 1e-6, cos_sin=None, interleaved: bool = False,
+                    q_out=None, k_scale=None, v_scale=None, scores=None) -> torch.Tensor:
+    """pa_norm_rope_store: RMS norm of every head of q (T, H, D) and k (T, Hkv, D) (where its
+    bf16 (D,) weight is given), rotation by the row `positions` (int64 (T,)) of cos_sin
+    (max_positions, rotary_dim: cosines, then sines; None: no rotation), and the store of k and
+    v in their slots (int64 (T,), negative: a padding token, skipped) of the cache, quantised
+    for an 8-bit cache. Returns q_out (T, H, D) bf16 (rows of padding tokens are not written);
+    it may be q itself if q is contiguous. q, k and v may be views of one fused projection's
+    output. scores: set the slots' scores (decode_scored) to 0."""
+    D = k_cache.shape[3]
+    T, H = q.shape[0], q.shape[1] if q.dim() == 3 else 0
+    Hkv = k_cache.shape[2]
+    qc, qs = _token_rows(q, "q", None, D)
+    kc, ks = _token_rows(k, "k", Hkv, D)
+    vc, vs = _token_rows(v, "v", Hkv, D)
+    if k.shape[0] != T or v.shape[0] != T:
+        raise ValueError("q, k and v must have the same number of tokens")
+    _want(slot_mapping, "slot_mapping", torch.int64, (T,))
+    if cos_sin is not None:
+        if cos_sin.dim() != 2:
+            raise ValueError("cos_sin must be (max_positions, rotary_dim)")
+        _want(cos_sin, "cos_sin", torch.float32, cos_sin.shape)
+        if positions is None:
+            raise ValueError("a rotation needs positions")
+    if positions is not None:
+        _want(positions, "positions", torch.int64, (T,))
+    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if w is not None:
+            _want(w, name, torch.bfloat16, (D,))
+    if scores is not None:
+        _want(scores, "scores", torch.float32, (k_cache.shape[0], Hkv, k_cache.shape[1]))
+    if q_out is None:
+        q_out = torch.empty((T, H, D), dtype=torch.bfloat16, device=q.device)
+    else:
+        _want(q_out, "q_out", torch.bfloat16, (T, H, D))
+    cache = _checked_cache(k_cache, v_cache, k_scale, v_scale, q, k, v, positions, slot_mapping,
+                           q_weight, k_weight, cos_sin, q_out, scores)
+    rot = 0 if cos_sin is None else cos_sin.shape[1]
+    params = NormRope(_ptr(q_weight), _ptr(k_weight), _ptr(cos_sin),
+                      0 if cos_sin is None else cos_sin.shape[0], rot, int(bool(interleaved)),
+                      float(eps))
+    _run(q.device, "pa_norm_rope_store", lib().pa_norm_rope_store, qc.data_ptr(), qs,
+         kc.data_ptr(), ks, vc.data_ptr(), vs, ctypes.byref(params), _ptr(positions),
+         slot_mapping.data_ptr(), T, H, ctypes.byref(cache), _ptr(scores), q_out.data_ptr())
+    return q_out
+
+
+def prefill_window(q, k_cache, v_cache, block_tables, cu_seqlens_q, cu_seqlens_k, scale: float,
+                   window: int, sinks: int = 0, *, max_q_len: int = 0,
+                   out=None) -> torch.Tensor:
+    """pa_prefill_window: prefill_varlen where a query sees the last `window` (>= 1) keys up to
+    its own and the first `sinks` keys."""
+    if q.dim() != 3:
+        raise ValueError("q must be (total_q, num_heads, head_dim)")
+    T, H, D = q.shape
+    _want(q, "q", torch.bfloat16, (T, H, k_cache.shape[3]), contiguous=False)
+    n = cu_seqlens_q.numel()
+    _want(cu_seqlens_q, "cu_seqlens_q", torch.int32, (n,))
+    _want(cu_seqlens_k, "cu_seqlens_k", torch.int32, (n,))
+    if n < 1 or block_tables.dim() != 2:
+        raise ValueError("block_tables must be (batch, blocks), cu_seqlens (batch + 1,)")
+    _want(block_tables, "block_tables", torch.int32, (n - 1, block_tables.shape[1]))
+    qc = q.contiguous()
+    if out is None:
+        out = torch.empty((T, H, D), dtype=torch.bfloat16, device=q.device)
+    else:
+        _want(out, "out", torch.bfloat16, (T, H, D))
+    cache = _checked_cache(k_cache, v_cache, None, None, q, block_tables, cu_seqlens_q,
+                           cu_seqlens_k, out)
+    _run(q.device, "pa_prefill_window", lib().pa_prefill_window, qc.data_ptr(),
+         ctypes.byref(cache), block_tables.data_ptr(), block_tables.shape[1],
+         cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), n - 1, H, T, int(max_q_len),
+         float(scale), int(window), int(sinks), out.data_ptr())
+    return out
+
+
+def decode_scored_workspace_size(k_cache, batch: int, num_heads: int, max_blocks_per_seq: int,
+                                 max_context_len: int = 0, v_cache=None, k_scale=None,
+                                 v_scale=None) -> int:
+    """Bytes of the workspace of decode_scored (0: the shape is not supported)."""
+    cache = make_cache(k_cache, k_cache if v_cache is None else v_cache, k_scale, v_scale)
+    return int(lib().pa_decode_scored_workspace_size(ctypes.byref(cache), batch, num_heads,
+                                                     max_blocks_per_seq, max_context_len))
+
+
+def decode_scored(q, k_cache, v_cache, block_tables, context_lens, scores, scale: float, *,
+                  max_context_len: int = 0, out=None, workspace=None, k_scale=None,
+                  v_scale=None) -> torch.Tensor:
+    """pa_decode_scored: decode, and every visible key's softmax weight, summed over the query
+    heads of its kv head, added in place to scores (num_blocks, num_kv_heads, block_size) fp32.
+    A workspace (uint8 tensor of decode_scored_workspace_size bytes) is allocated when none is
+    given."""
+    if q.dim() != 3:
+        raise ValueError("q must be (batch, num_heads, head_dim)")
+    B, H, D = q.shape
+    _want(q, "q", torch.bfloat16, (B, H, k_cache.shape[3]), contiguous=False)
+    _want(context_lens, "context_lens", torch.int32, (B,))
+    if block_tables.dim() != 2:
+        raise ValueError("block_tables must be (batch, blocks)")
+    _want(block_tables, "block_tables", torch.int32, (B, block_tables.shape[1]))
+    _want(scores, "scores", torch.float32, (k_cache.shape[0], k_cache.shape[2], k_cache.shape[1]))
+    qc = q.contiguous()
+    if out is None:
+        out = torch.empty((B, H, D), dtype=torch.bfloat16, device=q.device)
+    else:
+        _want(out, "out", torch.bfloat16, (B, H, D))
+    cache = _checked_cache(k_cache, v_cache, k_scale, v_scale, q, block_tables, context_lens,
+                           scores, out, workspace)
+    if workspace is None:  # a caller-provided workspace is checked by the library
+        need = int(lib().pa_decode_scored_workspace_size(ctypes.byref(cache), B, H,
+                                                         block_tables.shape[1],
+                                                         int(max_context_len)))
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _run(q.device, "pa_decode_scored", lib().pa_decode_scored, qc.data_ptr(), ctypes.byref(cache),
+         block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(),
+         int(max_context_len), B, H, float(scale), scores.data_ptr(), out.data_ptr(),
+         _ptr(workspace), ws_bytes)
+    return out
+
+
+def evict(k_cache, v_cache, scores, block_tables, context_lens, budget: int, *, sinks: int = 0,
+          recent: int = 0, max_context_len: int = 0, kept=None, new_lens=None, k_scale=None,
+          v_scale=None) -> tuple[torch.Tensor, torch.Tensor]:
+    """pa_evict: cut every sequence of more than `budget` keys to, per kv head, its first
+    `sinks`, its last `recent` and the best scores between them, moved in order to the front of
+    its blocks (K, V, scales and scores, in place). Returns (new_lens (B,) int32,
+    kept (B, Hkv, budget) int32: the positions the rows came from)."""
+    B = context_lens.numel()
+    _want(context_lens, "context_lens", torch.int32, (B,))
+    if block_tables.dim() != 2:
+        raise ValueError("block_tables must be (batch, blocks)")
+    _want(block_tables, "block_tables", torch.int32, (B, block_tables.shape[1]))
+    Hkv = k_cache.shape[2]
+    _want(scores, "scores", torch.float32, (k_cache.shape[0], Hkv, k_cache.shape[1]))
+    budget = int(budget)
+    if kept is None:
+        kept = torch.empty((B, Hkv, max(budget, 0)), dtype=torch.int32, device=scores.device)
+    else:
+        _want(kept, "kept", torch.int32, (B, Hkv, budget))
+    if new_lens is None:
+        new_lens = torch.empty((B,), dtype=torch.int32, device=scores.device)
+    else:
+        _want(new_lens, "new_lens", torch.int32, (B,))
+    cache = _checked_cache(k_cache, v_cache, k_scale, v_scale, scores, block_tables,
+                           context_lens, kept, new_lens)
+    _run(scores.device, "pa_evict", lib().pa_evict, ctypes.byref(cache), scores.data_ptr(),
+         block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(),
+         int(max_context_len), B, budget, int(sinks), int(recent), kept.data_ptr(),
+         new_lens.data_ptr())
+    return new_lens, kept
 
 
 def decode_noalloc(q, k_cache, v_cache, block_tables, context_lens, scale: float, *,

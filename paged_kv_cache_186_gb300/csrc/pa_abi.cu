@@ -4,6 +4,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <algorithm>
 #include <cmath>
 #include <cstring>
 #include <atomic>
@@ -11,7 +12,9 @@
 
 #include "pa.h"
 #include "pa_device.cuh"
+#include "pa_evict.h"
 #include "pa_launch.h"
+#include "pa_norm_rope.h"
 #include "pa_prefill.h"
 
 namespace {
@@ -254,6 +257,71 @@ pa_status pa_store_kv(const void* k, const void* v, const float* k_scale_new,
                                                                                   : PA_ERR_CUDA;
 }
 
+pa_status pa_norm_rope_store(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                             const void* v, int64_t v_stride, const pa_norm_rope* params,
+                             const int64_t* positions, const int64_t* slot_mapping,
+                             int32_t num_tokens, int32_t num_heads, const pa_kv_cache* cache,
+                             float* scores, void* q_out, void* stream) {
+  pa_status st = check_cache(cache);
+  if (st != PA_OK) return st;
+  if (params == nullptr) return PA_ERR_NULL;
+  if (num_tokens < 0 || num_heads <= 0) return PA_ERR_SHAPE;
+  const int D = cache->head_dim, rot = params->rotary_dim;
+  if (rot < 0 || rot > D || (rot > 0 && params->max_positions <= 0)) return PA_ERR_SHAPE;
+  if (rot % 16 != 0) return PA_ERR_UNSUPPORTED;
+  if (!(params->eps >= 0.f) || !std::isfinite(params->eps)) return PA_ERR_SHAPE;
+  const int64_t qrow = static_cast<int64_t>(num_heads) * D;
+  const int64_t krow = static_cast<int64_t>(cache->num_kv_heads) * D;
+  if (q_stride < qrow || k_stride < krow || v_stride < krow) return PA_ERR_SHAPE;
+  if (q_stride % 8 != 0 || k_stride % 8 != 0 || v_stride % 8 != 0) return PA_ERR_SHAPE;
+  if (q_out == q && q_stride != qrow) return PA_ERR_SHAPE;
+  if (num_tokens == 0) return PA_OK;
+  if (q == nullptr || k == nullptr || v == nullptr || slot_mapping == nullptr || q_out == nullptr ||
+      (rot > 0 && (positions == nullptr || params->cos_sin == nullptr)))
+    return PA_ERR_NULL;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(q_out) ||
+      !aligned16(params->q_weight) || !aligned16(params->k_weight) || !aligned16(params->cos_sin) ||
+      !aligned16(scores))
+    return PA_ERR_ALIGN;
+  DeviceInfo* dev = nullptr;
+  if ((st = device_info(&dev)) != PA_OK) return st;
+  const bool q8 = cache->dtype != PA_KV_BF16;
+  pa::NormRopeArgs a{};
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.q_weight = params->q_weight;
+  a.k_weight = params->k_weight;
+  a.cos_sin = params->cos_sin;
+  a.positions = positions;
+  a.slot_mapping = slot_mapping;
+  a.q_out = q_out;
+  a.k_cache = cache->k_cache;
+  a.v_cache = cache->v_cache;
+  a.k_scale = q8 ? cache->k_scale : nullptr;
+  a.v_scale = q8 ? cache->v_scale : nullptr;
+  a.scores = scores;
+  a.err = dev->err;
+  a.num_slots = static_cast<long long>(cache->num_blocks) * cache->block_size;
+  a.num_tokens = num_tokens;
+  a.num_heads = num_heads;
+  a.num_kv_heads = cache->num_kv_heads;
+  a.head_dim = D;
+  a.block_size = cache->block_size;
+  a.max_positions = params->max_positions;
+  a.rotary_dim = rot;
+  a.interleaved = params->interleaved != 0;
+  a.kv = static_cast<int>(cache->dtype);
+  a.eps = params->eps;
+  a.num_sms = dev->num_sms;
+  return pa::launch_norm_rope_store(a, static_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? PA_OK
+             : PA_ERR_CUDA;
+}
+
 size_t pa_decode_workspace_size(const pa_kv_cache* cache, int32_t batch, int32_t num_heads,
                                 int32_t max_blocks_per_seq, int32_t max_context_len) {
   if (check_cache(cache) != PA_OK || batch <= 0 || num_heads <= 0 || max_blocks_per_seq <= 0)
@@ -270,13 +338,32 @@ size_t pa_decode_workspace_size(const pa_kv_cache* cache, int32_t batch, int32_t
 
 namespace {
 
-// Shared body of pa_decode and pa_decode_append (k_new == NULL: no append).
+// The workspace of pa_decode_scored: pa_decode's, then (from ml on) the final
+// (max, 1 / sum) of every query head, then the scores of every key.
+struct ScoredWorkspace {
+  size_t ml, raw, bytes;
+};
+ScoredWorkspace scored_workspace(size_t decode_bytes, int32_t batch, int32_t num_heads, int cap,
+                                 int block_size) {
+  auto up = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
+  const size_t heads = static_cast<size_t>(batch) * num_heads;
+  const size_t keys = (static_cast<size_t>(cap) + block_size - 1) / block_size * block_size;
+  ScoredWorkspace w;
+  w.ml = up(decode_bytes);
+  w.raw = up(w.ml + heads * sizeof(float2));
+  w.bytes = w.raw + heads * keys * sizeof(float);
+  return w;
+}
+
+// Shared body of pa_decode and pa_decode_append (k_new == NULL: no append) and
+// pa_decode_scored (scores != NULL).
 pa_status decode_common(const void* q, const pa_kv_cache* cache, const int32_t* block_tables,
                         int32_t max_blocks_per_seq, const int32_t* context_lens,
                         int32_t max_context_len, int32_t batch, int32_t num_heads, float scale,
                         void* out, void* workspace, size_t workspace_bytes, void* stream,
                         const void* k_new, const void* v_new, const float* k_scale_new,
-                        const float* v_scale_new, int32_t window, int32_t sinks) {
+                        const float* v_scale_new, int32_t window, int32_t sinks,
+                        float* scores = nullptr) {
   pa_status st = check_cache(cache);
   if (st != PA_OK) return st;
   if (sinks < 0) return PA_ERR_SHAPE;
@@ -298,8 +385,11 @@ pa_status decode_common(const void* q, const pa_kv_cache* cache, const int32_t* 
                                               cache->head_dim, cache->block_size,
                                               static_cast<int>(cache->dtype), cap,
                                               dev->num_sms);
-  if (plan.workspace_bytes > 0 &&
-      (workspace == nullptr || workspace_bytes < plan.workspace_bytes || !aligned16(workspace)))
+  if (scores != nullptr && plan.persistent_ctas == 0) return PA_ERR_UNSUPPORTED;
+  const ScoredWorkspace sw =
+      scored_workspace(plan.workspace_bytes, batch, num_heads, cap, cache->block_size);
+  const size_t need = scores != nullptr ? sw.bytes : plan.workspace_bytes;
+  if (need > 0 && (workspace == nullptr || workspace_bytes < need || !aligned16(workspace)))
     return PA_ERR_WORKSPACE;
   if (window > 0 && plan.persistent_ctas == 0) return PA_ERR_UNSUPPORTED;
   CUtensorMap kmap, vmap;
@@ -375,7 +465,15 @@ pa_status decode_common(const void* q, const pa_kv_cache* cache, const int32_t* 
   const unsigned long long limit = g_debug_wait_limit_ns.load();
   a.wait_limit_ns = limit > 0 ? limit : pa::kWaitLimitNs;
   a.debug_skip_copy = g_debug_skip_copy.load();
-  return pa::launch_decode(a, kmap, vmap, strm) == cudaSuccess ? PA_OK : PA_ERR_CUDA;
+  if (scores != nullptr) {
+    char* const ws = static_cast<char*>(workspace);
+    a.head_ml = reinterpret_cast<float2*>(ws + sw.ml);
+    a.raw_scores = reinterpret_cast<float*>(ws + sw.raw);
+  }
+  if (pa::launch_decode(a, kmap, vmap, strm) != cudaSuccess) return PA_ERR_CUDA;
+  if (scores != nullptr && pa::launch_add_scores(a, scores, dev->num_sms, strm) != cudaSuccess)
+    return PA_ERR_CUDA;
+  return PA_OK;
 }
 
 }  // namespace
@@ -399,6 +497,72 @@ pa_status pa_decode_window(const void* q, const pa_kv_cache* cache, const int32_
   return decode_common(q, cache, block_tables, max_blocks_per_seq, context_lens, max_context_len,
                        batch, num_heads, scale, out, workspace, workspace_bytes, stream, nullptr,
                        nullptr, nullptr, nullptr, window, sinks);
+}
+
+size_t pa_decode_scored_workspace_size(const pa_kv_cache* cache, int32_t batch, int32_t num_heads,
+                                       int32_t max_blocks_per_seq, int32_t max_context_len) {
+  const size_t decode_bytes =
+      pa_decode_workspace_size(cache, batch, num_heads, max_blocks_per_seq, max_context_len);
+  if (decode_bytes == 0 || batch > pa::kMaxPersistentBatch) return 0;
+  return scored_workspace(decode_bytes, batch, num_heads,
+                          decode_len_cap(cache, max_blocks_per_seq, max_context_len),
+                          cache->block_size)
+      .bytes;
+}
+
+pa_status pa_decode_scored(const void* q, const pa_kv_cache* cache, const int32_t* block_tables,
+                           int32_t max_blocks_per_seq, const int32_t* context_lens,
+                           int32_t max_context_len, int32_t batch, int32_t num_heads, float scale,
+                           float* scores, void* out, void* workspace, size_t workspace_bytes,
+                           void* stream) {
+  if (batch > 0 && scores == nullptr) return PA_ERR_NULL;
+  if (!aligned16(scores)) return PA_ERR_ALIGN;
+  return decode_common(q, cache, block_tables, max_blocks_per_seq, context_lens, max_context_len,
+                       batch, num_heads, scale, out, workspace, workspace_bytes, stream, nullptr,
+                       nullptr, nullptr, nullptr, 0, 0, scores);
+}
+
+pa_status pa_evict(const pa_kv_cache* cache, float* scores, const int32_t* block_tables,
+                   int32_t max_blocks_per_seq, const int32_t* context_lens,
+                   int32_t max_context_len, int32_t batch, int32_t budget, int32_t sinks,
+                   int32_t recent, int32_t* kept, int32_t* new_lens, void* stream) {
+  pa_status st = check_cache(cache);
+  if (st != PA_OK) return st;
+  if (batch < 0 || max_blocks_per_seq <= 0 || budget < 1 || sinks < 0 || recent < 0 ||
+      static_cast<int64_t>(sinks) + recent > budget)
+    return PA_ERR_SHAPE;
+  if (batch == 0) return PA_OK;
+  if (scores == nullptr || block_tables == nullptr || context_lens == nullptr || kept == nullptr ||
+      new_lens == nullptr)
+    return PA_ERR_NULL;
+  if (new_lens < context_lens + batch && context_lens < new_lens + batch) return PA_ERR_SHAPE;
+  if (batch > 65535) return PA_ERR_UNSUPPORTED;
+  if (!aligned16(scores)) return PA_ERR_ALIGN;
+  DeviceInfo* dev = nullptr;
+  if ((st = device_info(&dev)) != PA_OK) return st;
+  pa::EvictArgs a{};
+  a.k_cache = cache->k_cache;
+  a.v_cache = cache->v_cache;
+  a.k_scale = cache->k_scale;
+  a.v_scale = cache->v_scale;
+  a.scores = scores;
+  a.block_tables = block_tables;
+  a.context_lens = context_lens;
+  a.kept = kept;
+  a.new_lens = new_lens;
+  a.err = dev->err;
+  a.batch = batch;
+  a.num_kv_heads = cache->num_kv_heads;
+  a.block_size = cache->block_size;
+  a.num_blocks = cache->num_blocks;
+  a.max_blocks = max_blocks_per_seq;
+  a.len_cap = decode_len_cap(cache, max_blocks_per_seq, max_context_len);
+  a.row_bytes = cache->head_dim * elem_bytes(cache);
+  a.budget = budget;
+  a.sinks = sinks;
+  a.recent = recent;
+  return pa::launch_evict(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? PA_OK
+                                                                               : PA_ERR_CUDA;
 }
 
 pa_status pa_decode_append(const void* q, const void* k_new, const void* v_new,
@@ -431,11 +595,16 @@ pa_status pa_decode_window_append(const void* q, const void* k_new, const void* 
                        v_new, k_scale_new, v_scale_new, window, sinks);
 }
 
-pa_status pa_prefill_varlen(const void* q, const pa_kv_cache* cache, const int32_t* block_tables,
-                            int32_t max_blocks_per_seq, const int32_t* cu_seqlens_q,
-                            const int32_t* cu_seqlens_k, int32_t batch, int32_t num_heads,
-                            int32_t total_q, int32_t max_q_len, float scale, void* out,
-                            void* stream) {
+}  // extern "C"
+
+namespace {
+
+// Shared body of pa_prefill_varlen (window 0) and pa_prefill_window.
+pa_status prefill_common(const void* q, const pa_kv_cache* cache, const int32_t* block_tables,
+                         int32_t max_blocks_per_seq, const int32_t* cu_seqlens_q,
+                         const int32_t* cu_seqlens_k, int32_t batch, int32_t num_heads,
+                         int32_t total_q, int32_t max_q_len, float scale, int32_t window,
+                         int32_t sinks, void* out, void* stream) {
   pa_status st = check_cache(cache);
   if (st != PA_OK) return st;
   if (batch < 0 || num_heads <= 0 || total_q < 0 || max_blocks_per_seq <= 0) return PA_ERR_SHAPE;
@@ -492,9 +661,37 @@ pa_status pa_prefill_varlen(const void* q, const pa_kv_cache* cache, const int32
   a.tokens_per_tile = tpt;
   a.num_qtiles = (qbound + tpt - 1) / tpt;
   a.scale_log2 = scale * 1.4426950408889634f;
+  // (the kernel subtracts the window and a key's offset from a position)
+  a.window = std::min(window, 0x7ffffe00);
+  a.sinks = sinks;
   return pa::launch_prefill(a, qmap, kmap, vmap, static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? PA_OK
              : PA_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+pa_status pa_prefill_varlen(const void* q, const pa_kv_cache* cache, const int32_t* block_tables,
+                            int32_t max_blocks_per_seq, const int32_t* cu_seqlens_q,
+                            const int32_t* cu_seqlens_k, int32_t batch, int32_t num_heads,
+                            int32_t total_q, int32_t max_q_len, float scale, void* out,
+                            void* stream) {
+  return prefill_common(q, cache, block_tables, max_blocks_per_seq, cu_seqlens_q, cu_seqlens_k,
+                        batch, num_heads, total_q, max_q_len, scale, 0, 0, out, stream);
+}
+
+pa_status pa_prefill_window(const void* q, const pa_kv_cache* cache, const int32_t* block_tables,
+                            int32_t max_blocks_per_seq, const int32_t* cu_seqlens_q,
+                            const int32_t* cu_seqlens_k, int32_t batch, int32_t num_heads,
+                            int32_t total_q, int32_t max_q_len, float scale, int32_t window,
+                            int32_t sinks, void* out, void* stream) {
+  const pa_status st = check_cache(cache);
+  if (st != PA_OK) return st;
+  if (window < 1 || sinks < 0) return PA_ERR_SHAPE;
+  return prefill_common(q, cache, block_tables, max_blocks_per_seq, cu_seqlens_q, cu_seqlens_k,
+                        batch, num_heads, total_q, max_q_len, scale, window, sinks, out, stream);
 }
 
 pa_status pa_debug_inject_wait_timeout(int32_t skip_copy, uint64_t wait_limit_ns) {

@@ -32,6 +32,10 @@
 //   * 8-bit KV (E4M3 or INT8 codes, flag Q8): codes are widened exactly to
 //     f16 in registers; the K scale multiplies the score, the V scale the
 //     probability.
+//   * The scored variant (SC) also writes every score, in the block order of
+//     the split, and every head's final (max, 1 / sum), for the launch that
+//     turns them into weights (pa_scored.cu): 4 bytes per key and query head
+//     next to the 2 * head_dim * element size of the key and its value.
 //   * A sliding window with sinks (WIN) walks only the blocks that hold a
 //     visible key and masks the rest inside them.
 //   * Batches above kMaxPersistentBatch use a grid of (kv head, sequence,
@@ -184,13 +188,15 @@ __device__ __forceinline__ void load_q(const DecodeArgs& a, int b, int kvh, int 
 // lane group r; acc = O^T fragments for heads 2q4, 2q4+1). The whole block is
 // one softmax step: S for its BS tokens (BS/8 n-tiles, independent MMA
 // chains), one max/sum update, then P.V per 16-token group.
-template <int D, int BS, int KV, bool HOLE = false>
+// `raw` (SC): where the block's scores go, (group, BS) floats.
+template <int D, int BS, int KV, bool HOLE = false, bool SC = false>
 __device__ __forceinline__ void attend_block(uint32_t kt, uint32_t vt, const uint8_t* base_ptr,
                                              uint32_t base, const float* ksc, const float* vsc,
                                              int tok0, int L, int hole_lo, int hole_hi,
                                              const uint32_t (&qa)[D / 16][2],
                                              float (&acc)[D / 16][4], float& m_run, float& l_run,
-                                             float& vfac, float sl2, int lane) {
+                                             float& vfac, float sl2, int lane,
+                                             float* raw = nullptr, int group = 0) {
   constexpr int NT = BS / 8;  // n-tiles of 8 tokens
   constexpr int NG = BS / 16;  // 16-token groups (k-steps of P.V)
   constexpr bool Q8 = KV != kKvBf16;
@@ -253,6 +259,14 @@ __device__ __forceinline__ void attend_block(uint32_t kt, uint32_t vt, const uin
 #pragma unroll
     for (int j = 0; j < 2 * NT; ++j)
       if (!valid(tok0 + (j >> 1) * 8 + 2 * q4 + (j & 1))) x[j] = -INFINITY;
+  }
+  if constexpr (SC) {
+    if (r < group) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+        *reinterpret_cast<float2*>(raw + r * BS + nt * 8 + 2 * q4) =
+            make_float2(x[2 * nt], x[2 * nt + 1]);
+    }
   }
   float mx = x[0];
 #pragma unroll
@@ -567,7 +581,7 @@ __device__ __forceinline__ void piece_next(Piece& p, const int* prefix, int B, i
 // segment is entirely this warp's, else an fp32 partial (O unnormalised,
 // (max, sum) per head) in `slot`. Lane (r, q4) holds O^T for heads 2q4, 2q4+1
 // and the running max/sum of head r.
-template <int D, bool Q8>
+template <int D, bool Q8, bool SC>
 __device__ __forceinline__ void write_warp_result(const DecodeArgs& a, int b, int kvh,
                                                   bool final_out, long long slot, int lane,
                                                   float m_run, float l_run, float o_scale,
@@ -579,6 +593,11 @@ __device__ __forceinline__ void write_warp_result(const DecodeArgs& a, int b, in
   const float l0 = __shfl_sync(kFull, l_tot, 4 * h0);
   const float l1 = __shfl_sync(kFull, l_tot, 4 * h1);
   if (final_out) {
+    if constexpr (SC) {
+      if (q4 == 0 && r < G)
+        a.head_ml[static_cast<long long>(b) * a.num_heads + kvh * G + r] =
+            make_float2(m_run, l_tot > 0.f ? 1.f / l_tot : 0.f);
+    }
     const float inv0 = l0 > 0.f ? o_scale / l0 : 0.f, inv1 = l1 > 0.f ? o_scale / l1 : 0.f;
     __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out) +
                        (static_cast<long long>(b) * a.num_heads + kvh * G) * D;
@@ -811,7 +830,7 @@ __device__ __forceinline__ bool arrive_last(unsigned long long* counter, uint32_
 // shuffles); then every part costs one round of independent loads (its max
 // and the lane's head_dim slice of O), two parts in flight at a time.
 // Partials are read through L2.
-template <int D, int GP>
+template <int D, int GP, bool SC>
 __device__ __forceinline__ void merge_segment_g(const DecodeArgs& a, const PartList& sp, int b,
                                                 int kvh, bool final_out, int lane) {
   // lanes per head (at least 8 dims each, so a slice is whole 16-byte bf16 stores)
@@ -880,6 +899,10 @@ __device__ __forceinline__ void merge_segment_g(const DecodeArgs& a, const PartL
     return;
   }
   const float inv = L > 0.f ? 1.f / L : 0.f;
+  if constexpr (SC) {
+    if (sub == 0)
+      a.head_ml[static_cast<long long>(b) * a.num_heads + kvh * G + g] = make_float2(M, inv);
+  }
   __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(a.out) +
                        (static_cast<long long>(b) * a.num_heads + kvh * G + g) * D + sub * DL;
 #pragma unroll
@@ -893,20 +916,20 @@ __device__ __forceinline__ void merge_segment_g(const DecodeArgs& a, const PartL
   }
 }
 
-template <int D>
+template <int D, bool SC>
 __device__ __forceinline__ void merge_segment(const DecodeArgs& a, const PartList& sp, int b,
                                               int kvh, bool final_out, int lane) {
-  if (a.group <= 1) merge_segment_g<D, 1>(a, sp, b, kvh, final_out, lane);
-  else if (a.group <= 2) merge_segment_g<D, 2>(a, sp, b, kvh, final_out, lane);
-  else if (a.group <= 4) merge_segment_g<D, 4>(a, sp, b, kvh, final_out, lane);
-  else merge_segment_g<D, 8>(a, sp, b, kvh, final_out, lane);
+  if (a.group <= 1) merge_segment_g<D, 1, SC>(a, sp, b, kvh, final_out, lane);
+  else if (a.group <= 2) merge_segment_g<D, 2, SC>(a, sp, b, kvh, final_out, lane);
+  else if (a.group <= 4) merge_segment_g<D, 4, SC>(a, sp, b, kvh, final_out, lane);
+  else merge_segment_g<D, 8, SC>(a, sp, b, kvh, final_out, lane);
 }
 
 // Arrival of one part of a segment of more than kGroupedAbove parts: this
 // part's group first (the group's last arriver merges it into the slot of the
 // group's first part), then the segment over the group results. Out of line:
 // it is rare and must not add registers to the block loop.
-template <int D>
+template <int D, bool SC>
 __device__ __noinline__ void finish_grouped(const DecodeArgs a, const SegParts sp, int b, int kvh,
                                             long long gw, int lane) {
   const int j = static_cast<int>(gw - sp.w0), g0 = j - j % kMergeGroup;
@@ -916,7 +939,7 @@ __device__ __noinline__ void finish_grouped(const DecodeArgs a, const SegParts s
     last = arrive_last(a.grp_counters + sp.slot(g0), a.epoch, static_cast<uint32_t>(ng), a.err);
   if (!__shfl_sync(kFull, last, 0)) return;
   __threadfence();
-  merge_segment<D>(a, PartList{sp, g0, 1, ng}, b, kvh, false, lane);
+  merge_segment<D, SC>(a, PartList{sp, g0, 1, ng}, b, kvh, false, lane);
   __threadfence();
   __syncwarp();
   const int ngroups = (sp.n + kMergeGroup - 1) / kMergeGroup;
@@ -925,7 +948,7 @@ __device__ __noinline__ void finish_grouped(const DecodeArgs a, const SegParts s
                        static_cast<uint32_t>(ngroups), a.err);
   if (!__shfl_sync(kFull, last, 0)) return;
   __threadfence();
-  merge_segment<D>(a, PartList{sp, 0, kMergeGroup, ngroups}, b, kvh, true, lane);
+  merge_segment<D, SC>(a, PartList{sp, 0, kMergeGroup, ngroups}, b, kvh, true, lane);
 }
 
 template <int D, int BS, int NW, int ST, bool Q8>
@@ -979,7 +1002,7 @@ __device__ __noinline__ void append_row(uint8_t* tile, float* stage_scales, cons
   __syncwarp();
 }
 
-template <int D, int BS, int NW, int ST, int KV, bool WIN>
+template <int D, int BS, int NW, int ST, int KV, bool WIN, bool SC>
 __global__ void __launch_bounds__(NW * 32, 3)
     decode_persistent_kernel(const __grid_constant__ CUtensorMap kmap,
                              const __grid_constant__ CUtensorMap vmap, const DecodeArgs a) {
@@ -1128,6 +1151,10 @@ __global__ void __launch_bounds__(NW * 32, 3)
                                                 static_cast<long long>(b) * a.num_heads * D);
     for (int i = threadIdx.x; i < a.num_heads * (D / 8); i += NW * 32) row[i] = make_uint4(0, 0, 0, 0);
   }
+  if constexpr (SC) {  // the block list of the split, for the launch that reads the scores
+    if (blockIdx.x == 0)
+      for (int i = threadIdx.x; i <= B; i += NW * 32) a.prefix_out[i] = prefix[i];
+  }
   if (!active) return;
 
   long long win_base = 0;
@@ -1216,9 +1243,10 @@ __global__ void __launch_bounds__(NW * 32, 3)
                                const_cast<float*>(scale_ptr) + ((warp * ST + s) * 2) * BS,
                                a.block_tables + static_cast<long long>(cp.b) * a.max_blocks + blk,
                                cp.b * Hkv + cp.kvh, (L - 1) - blk * BS, a, lane);
-      attend_block<D, BS, KV, WIN>(kt, kt + C::kTile, base_ptr, base, ksc, ksc + BS, blk * BS, L,
-                                    sw.hole_lo, sw.hole_hi, qa, acc, m_run, l_run, vfac, sl2p,
-                                    lane);
+      attend_block<D, BS, KV, WIN, SC>(
+          kt, kt + C::kTile, base_ptr, base, ksc, ksc + BS, blk * BS, L, sw.hole_lo, sw.hole_hi, qa,
+          acc, m_run, l_run, vfac, sl2p, lane,
+          SC ? a.raw_scores + (cp.g + (vb - cp.lo)) * (a.group * BS) : nullptr, a.group);
       if (!whole && vb == cp.hi - 1 && lane == 0)
         seen = ld_relaxed_gpu(a.seg_counters + static_cast<long long>(cp.b) * Hkv + cp.kvh);
       ++consumed;
@@ -1230,7 +1258,7 @@ __global__ void __launch_bounds__(NW * 32, 3)
     Piece nx = cp;
     piece_next(nx, prefix, B, Hkv, r1);
     if (nx.valid) fetch_q<D, Q8>(a, nx.b, nx.kvh, lane, qraw);
-    write_warp_result<D, Q8>(a, cp.b, cp.kvh, whole, 2 * gw + (cp.lo == 0 ? 1 : 0), lane, m_run,
+    write_warp_result<D, Q8, SC>(a, cp.b, cp.kvh, whole, 2 * gw + (cp.lo == 0 ? 1 : 0), lane, m_run,
                               l_run, 1.f / vfac, acc);
     if (!whole) {
       const SegParts sp = seg_parts(prefix, B, Hkv, cp.b, cp.kvh, W, cost);
@@ -1247,7 +1275,7 @@ __global__ void __launch_bounds__(NW * 32, 3)
         if (lane == 0) atomicExch(a.seg_counters + static_cast<long long>(cp.b) * Hkv + cp.kvh, 0ull);
         __threadfence();
         __syncwarp();
-        merge_segment<D>(a, PartList{sp, 0, 1, sp.n}, cp.b, cp.kvh, true, lane);
+        merge_segment<D, SC>(a, PartList{sp, 0, 1, sp.n}, cp.b, cp.kvh, true, lane);
         cp = nx;
         continue;
       }
@@ -1255,7 +1283,7 @@ __global__ void __launch_bounds__(NW * 32, 3)
       __threadfence();
       __syncwarp();
       if (sp.n > kGroupedAbove) {
-        finish_grouped<D>(a, sp, cp.b, cp.kvh, gw, lane);
+        finish_grouped<D, SC>(a, sp, cp.b, cp.kvh, gw, lane);
       } else {
         int last = 0;
         if (lane == 0)
@@ -1263,7 +1291,7 @@ __global__ void __launch_bounds__(NW * 32, 3)
                              static_cast<uint32_t>(sp.n), a.err);
         if (__shfl_sync(kFull, last, 0)) {
           __threadfence();
-          merge_segment<D>(a, PartList{sp, 0, 1, sp.n}, cp.b, cp.kvh, true, lane);
+          merge_segment<D, SC>(a, PartList{sp, 0, 1, sp.n}, cp.b, cp.kvh, true, lane);
         }
       }
     }
@@ -1465,16 +1493,20 @@ struct Inst {
     const int bb = bucket_batch(std::min(std::max(batch, 1), kMaxPersistentBatch));
     int& slot = cached[dev][bb / kBucket - 1];
     if (slot > 0) return slot;
-    // both variants (with and without a sliding window) get the attribute;
-    // the grid is sized by the one with fewer resident CTAs
-    auto* k0 = decode_persistent_kernel<D, BS, kWarps, kStages, KV, false>;
-    auto* k1 = decode_persistent_kernel<D, BS, kWarps, kStages, KV, true>;
+    // every variant gets the attribute; the grid is sized by the one of the
+    // two that write no scores (with and without a sliding window) with fewer
+    // resident CTAs
+    auto* k0 = decode_persistent_kernel<D, BS, kWarps, kStages, KV, false, false>;
+    auto* k1 = decode_persistent_kernel<D, BS, kWarps, kStages, KV, true, false>;
+    auto* k2 = decode_persistent_kernel<D, BS, kWarps, kStages, KV, false, true>;
     const int smem_max = PC::smem_bytes(kMaxPersistentBatch);
     const int smem = PC::smem_bytes(bb);
     int n0 = 0, n1 = 0;
     if (cudaFuncSetAttribute(k0, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_max) !=
             cudaSuccess ||
         cudaFuncSetAttribute(k1, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_max) !=
+            cudaSuccess ||
+        cudaFuncSetAttribute(k2, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_max) !=
             cudaSuccess ||
         cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n0, k0, kWarps * 32, smem) != cudaSuccess ||
         cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n1, k1, kWarps * 32, smem) != cudaSuccess)
@@ -1488,8 +1520,10 @@ struct Inst {
     cudaError_t e;
     const long long rows = static_cast<long long>(a.batch) * a.num_heads;
     if (a.persistent_ctas > 0) {
-      auto* k = a.window > 0 ? decode_persistent_kernel<D, BS, kWarps, kStages, KV, true>
-                             : decode_persistent_kernel<D, BS, kWarps, kStages, KV, false>;
+      auto* k = a.raw_scores != nullptr
+                    ? decode_persistent_kernel<D, BS, kWarps, kStages, KV, false, true>
+                : a.window > 0 ? decode_persistent_kernel<D, BS, kWarps, kStages, KV, true, false>
+                               : decode_persistent_kernel<D, BS, kWarps, kStages, KV, false, false>;
       (void)ctas_per_sm(a.batch);  // makes sure the shared-memory attribute is set
       // programmatic dependent launch: the prologue may overlap the kernel
       // before this one on the stream (the kernel waits before reading K/V)

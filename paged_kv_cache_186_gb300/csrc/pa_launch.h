@@ -69,6 +69,11 @@ struct DecodeArgs {
   int batch, num_heads, num_kv_heads, group, head_dim, block_size;
   int max_blocks, num_blocks, len_cap;
   int window, sinks;          // sliding window (> 0) with leading sink keys; 0 = all keys
+  // pa_decode_scored: the scores of every key in base-2 units, by the flattened
+  // block index of the persistent kernel: (blocks, group, block_size), and the
+  // final (max, 1 / sum) of every query head (B, H); NULL otherwise
+  float* raw_scores;
+  float2* head_ml;
   int persistent_ctas;        // > 0: persistent kernel with this many CTAs
   int blocks_per_split, num_splits;  // grid-split path
   int kv;                     // kKvBf16, kKvE4m3 or kKvInt8
@@ -93,6 +98,11 @@ struct DecodePlan {
 
 DecodePlan plan_decode(int batch, int num_heads, int num_kv_heads, int head_dim, int block_size,
                        int kv, int len_cap, int num_sms);
+
+// Second launch of pa_decode_scored: adds the softmax weight of every key,
+// summed over the query heads of its kv head, to scores (NB, Hkv, bs).
+cudaError_t launch_add_scores(const DecodeArgs& a, float* scores, int num_sms,
+                              cudaStream_t stream);
 
 cudaError_t launch_decode(const DecodeArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap,
                           cudaStream_t stream);

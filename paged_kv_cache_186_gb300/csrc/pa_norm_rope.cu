@@ -1,0 +1,282 @@
+// norm_rope_store: per-head RMS norm of q and k, position rotation of both, and
+// the store of the new K and V rows in their cache slots.
+//
+// What is computed, for token t at position p = positions[t], slot s =
+// slot_mapping[t], in fp32 from the bf16 inputs:
+//     n(x)_i = x_i * rsqrt(mean_j x_j^2 + eps) * weight_i      (weight given)
+//     (a, b) -> (a cos - b sin, b cos + a sin)                 (dims < rotary_dim)
+// with (cos, sin) of pair i from row p of the caller's table, and pair i either
+// dims (i, i + rotary_dim/2) or (2i, 2i+1). q rows go to q_out (one rounding to
+// bf16), k and v rows to the cache: bf16, or 8-bit codes c = round(x / sc) with
+// sc = max|x| / 448 (E4M3) or / 127 (INT8) taken from the unrounded row.
+//
+// How: a row of head_dim elements belongs to head_dim/8 lanes with one 16-byte
+// chunk each, so every load and store is a 16-byte vector and a warp holds 2
+// (head_dim 128) or 4 rows at once. A warp's rows are of one kind (q, k or v).
+// The norm is a shuffle sum over the row's lanes. The weight and the table
+// entries are folded once per warp into two factors per element,
+//     y_i = rstd * (x_i * A_i + x_partner(i) * B_i),
+// A_i = w_i cos, B_i = -+ w_partner sin, so a row costs two multiply-adds per
+// element and a half-split partner chunk is fetched from its lane as raw bf16
+// (four shuffles). All of a warp's row loads are issued before the table's.
+#include "pa_device.cuh"
+#include "pa_launch.h"
+#include "pa_norm_rope.h"
+
+namespace pa {
+
+namespace {
+
+constexpr int kNrWarps = 4;
+constexpr unsigned kAll = 0xffffffffu;
+
+__device__ __forceinline__ void unpack8(const uint4& u, float (&x)[8]) {
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    x[2 * i] = __uint_as_float(w[i] << 16);
+    x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+
+__device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
+  return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
+                    pack_bf16x2(x[6], x[7]));
+}
+
+// max that keeps a NaN of either operand
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// Eight fp32 -> eight 8-bit codes of kind KV (in order, low byte first).
+// E4M3: round to nearest even, saturating at 448, NaN stays NaN. INT8: round
+// to nearest even, clamped to +-127 (a NaN gives 0: its row's scale is NaN).
+template <int KV>
+__device__ __forceinline__ uint2 codes8(const float (&x)[8]) {
+  if constexpr (KV == kKvE4m3) {
+    uint16_t c[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(c[i]) : "f"(x[2 * i + 1]), "f"(x[2 * i]));
+    return make_uint2(c[0] | (static_cast<uint32_t>(c[1]) << 16),
+                      c[2] | (static_cast<uint32_t>(c[3]) << 16));
+  } else {
+    uint32_t w[2] = {0u, 0u};
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int c = min(127, max(-127, __float2int_rn(x[i])));
+      w[i >> 2] |= (static_cast<uint32_t>(c) & 0xffu) << (8 * (i & 3));
+    }
+    return make_uint2(w[0], w[1]);
+  }
+}
+
+// One warp: NIT rounds of 256/D rows of one kind of one token.
+template <int D, int KV, bool INTER, int NIT>
+__global__ void __launch_bounds__(kNrWarps * 32) norm_rope_kernel(const NormRopeArgs a) {
+  constexpr int LPR = D / 8;     // lanes per row
+  constexpr int RPW = 32 / LPR;  // rows of a round
+  constexpr int RW = NIT * RPW;  // rows of a warp
+  // launched as a programmatic dependent: everything is read after the wait,
+  // and the next launch may start only then (a decode reads the lengths and
+  // the block tables before its own wait; what wrote them is complete here)
+  grid_dependency_wait();
+  grid_launch_dependents();
+  const int lane = threadIdx.x & 31;
+  const int sub = lane / LPR, c = lane % LPR;
+  const int H = a.num_heads, Hkv = a.num_kv_heads;
+  const int nq = (H + RW - 1) / RW, nk = (Hkv + RW - 1) / RW;
+  const int wpt = nq + 2 * nk;  // warps per token
+  const long long w = static_cast<long long>(blockIdx.x) * kNrWarps + (threadIdx.x >> 5);
+  const long long t = w / wpt;
+  if (t >= a.num_tokens) return;
+  int part = static_cast<int>(w - t * wpt);
+  const int kind = part < nq ? 0 : part < nq + nk ? 1 : 2;  // q, k, v
+  part -= kind == 0 ? 0 : kind == 1 ? nq : nq + nk;
+  const int rows = kind == 0 ? H : Hkv;
+  const int row0 = part * RW + sub;
+
+  const __nv_bfloat16* src =
+      static_cast<const __nv_bfloat16*>(kind == 0 ? a.q : kind == 1 ? a.k : a.v) +
+      t * (kind == 0 ? a.q_stride : kind == 1 ? a.k_stride : a.v_stride) + c * 8;
+  uint4 raw[NIT];
+#pragma unroll
+  for (int i = 0; i < NIT; ++i) {
+    const int r = row0 + i * RPW;
+    raw[i] = make_uint4(0u, 0u, 0u, 0u);
+    if (r < rows) raw[i] = *reinterpret_cast<const uint4*>(src + r * D);
+  }
+  const long long slot = a.slot_mapping[t];
+  if (slot < 0) return;  // padding token
+  const int rot = a.rotary_dim;
+  long long pos = 0;
+  if (rot > 0) {
+    pos = a.positions[t];
+    if (pos < 0 || pos >= a.max_positions) {
+      if (lane == 0) report_error(a.err, PA_DEVERR_POSITION_RANGE);
+      return;
+    }
+  }
+  if (kind != 0 && slot >= a.num_slots) {
+    if (lane == 0) report_error(a.err, PA_DEVERR_SLOT_RANGE);
+    return;
+  }
+
+  // ---- factors of this lane's eight elements: y_i = rstd * (x_i A_i + partner_i B_i)
+  float A[8], B[8];
+  const void* const wt = kind == 0 ? a.q_weight : kind == 1 ? a.k_weight : nullptr;
+  const bool norm = wt != nullptr;
+  int pc = c;  // chunk that holds the partners of a half-split pair
+  if (kind != 2) {
+    float wf[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) wf[i] = 1.f;
+    if (norm) unpack8(__ldg(static_cast<const uint4*>(wt) + c), wf);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      A[i] = wf[i];
+      B[i] = 0.f;
+    }
+    if (c * 8 < rot) {
+      const float* cs = a.cos_sin + pos * rot;
+      if constexpr (INTER) {
+        // pairs (2i, 2i+1): four of them in this chunk
+        const float4 co = __ldg(reinterpret_cast<const float4*>(cs + c * 4));
+        const float4 si = __ldg(reinterpret_cast<const float4*>(cs + rot / 2 + c * 4));
+        const float cv[4] = {co.x, co.y, co.z, co.w}, sv[4] = {si.x, si.y, si.z, si.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          A[2 * i] = wf[2 * i] * cv[i];
+          B[2 * i] = -wf[2 * i + 1] * sv[i];
+          A[2 * i + 1] = wf[2 * i + 1] * cv[i];
+          B[2 * i + 1] = wf[2 * i] * sv[i];
+        }
+      } else {
+        const int hc = rot / 16;  // chunks of half the rotated part
+        const bool second = c >= hc;
+        pc = second ? c - hc : c + hc;
+        float pw[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) pw[i] = 1.f;
+        if (norm) unpack8(__ldg(static_cast<const uint4*>(wt) + pc), pw);
+        const float4* cp = reinterpret_cast<const float4*>(cs + 8 * (second ? pc : c));
+        const float4* sp = reinterpret_cast<const float4*>(cs + rot / 2 + 8 * (second ? pc : c));
+        const float4 c0 = __ldg(cp), c1 = __ldg(cp + 1), s0 = __ldg(sp), s1 = __ldg(sp + 1);
+        const float cv[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+        const float sv[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          A[i] = wf[i] * cv[i];
+          B[i] = second ? pw[i] * sv[i] : -pw[i] * sv[i];
+        }
+      }
+    }
+  }
+  const int plane = (lane - c) + pc;  // lane of the partner chunk
+
+  const long long blk = kind == 0 ? 0 : slot / a.block_size;
+  const int off = kind == 0 ? 0 : static_cast<int>(slot - blk * a.block_size);
+#pragma unroll
+  for (int i = 0; i < NIT; ++i) {
+    const int r = row0 + i * RPW;
+    float x[8];
+    unpack8(raw[i], x);
+    if (kind != 2) {
+      float rstd = 1.f;
+      if (norm) {
+        float ss = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
+#pragma unroll
+        for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(kAll, ss, o);
+        rstd = rsqrtf(ss * (1.f / D) + a.eps);
+      }
+      float y[8];
+      if constexpr (INTER) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] = x[j ^ 1];
+      } else {
+        uint4 pr;
+        pr.x = __shfl_sync(kAll, raw[i].x, plane);
+        pr.y = __shfl_sync(kAll, raw[i].y, plane);
+        pr.z = __shfl_sync(kAll, raw[i].z, plane);
+        pr.w = __shfl_sync(kAll, raw[i].w, plane);
+        unpack8(pr, y);
+      }
+      if (c * 8 < rot) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = rstd * fmaf(x[j], A[j], y[j] * B[j]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = rstd * (x[j] * A[j]);
+      }
+    }
+    if (kind == 0) {
+      if (r < rows)
+        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.q_out) +
+                                  (t * H + r) * D + c * 8) = pack8(x);
+      continue;
+    }
+    void* const cache = kind == 1 ? a.k_cache : a.v_cache;
+    const long long row = slot * Hkv + r;  // (slot, head) row of the cache
+    if constexpr (KV == kKvBf16) {
+      if (r < rows)
+        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(cache) + row * D + c * 8) =
+            kind == 2 ? raw[i] : pack8(x);
+    } else {
+      float amax = 0.f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) amax = max_nan(amax, fabsf(x[j]));
+#pragma unroll
+      for (int o = LPR / 2; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(kAll, amax, o));
+      float sc = amax / (KV == kKvE4m3 ? 448.f : 127.f);
+      if (sc == 0.f) sc = 1.f;  // a row of zeros (or whose scale underflows)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[j] = x[j] / sc;
+      if (r < rows) {
+        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(cache) + row * D + c * 8) = codes8<KV>(x);
+        if (c == 0) (kind == 1 ? a.k_scale : a.v_scale)[(blk * Hkv + r) * a.block_size + off] = sc;
+      }
+    }
+    if (kind == 1 && a.scores != nullptr && c == 0 && r < rows)
+      a.scores[(blk * Hkv + r) * a.block_size + off] = 0.f;
+  }
+}
+
+template <int D, int KV, bool INTER, int NIT>
+cudaError_t launch_inst(const NormRopeArgs& a, cudaStream_t stream) {
+  constexpr int RW = NIT * (256 / D);
+  const long long wpt = (a.num_heads + RW - 1) / RW + 2 * ((a.num_kv_heads + RW - 1) / RW);
+  const long long grid = (a.num_tokens * wpt + kNrWarps - 1) / kNrWarps;
+  if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(grid));
+  cfg.blockDim = dim3(kNrWarps * 32);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, norm_rope_kernel<D, KV, INTER, NIT>, a);
+}
+
+template <int D, int KV>
+cudaError_t launch_kind(const NormRopeArgs& a, cudaStream_t stream) {
+  return a.interleaved ? launch_inst<D, KV, true, 1>(a, stream)
+                       : launch_inst<D, KV, false, 1>(a, stream);
+}
+
+}  // namespace
+
+cudaError_t launch_norm_rope_store(const NormRopeArgs& a, cudaStream_t stream) {
+  if (a.num_tokens <= 0) return cudaSuccess;
+  if (a.kv == kKvE4m3) return launch_kind<128, kKvE4m3>(a, stream);
+  if (a.kv == kKvInt8) return launch_kind<128, kKvInt8>(a, stream);
+  return a.head_dim == 64 ? launch_kind<64, kKvBf16>(a, stream) : launch_kind<128, kKvBf16>(a, stream);
+}
+
+}  // namespace pa

@@ -43,6 +43,15 @@
 //     instead of 8. Tiles of rows with longer prefixes are unchanged; the
 //     code's presence costs ~3 % there (measured 124.2 -> 128.4 us on the
 //     8-sequence benchmark, whose prefixes are all >= 250 tokens).
+//   * A sliding window with sinks (WIN): row p sees keys j <= p with j < sinks
+//     or j > p - window. The CTA walks the 128-key tiles that hold a key some
+//     row of its two query tiles sees: the sink keys' tiles, then tiles from
+//     the first window key's block on (PairKeys). Blocks of a walked tile
+//     without such a key are fetched out of bounds like those past the end
+//     (their table entries are not read), V rows that no row sees are zeroed,
+//     and a row's own bounds are masked on the tiles that cross them. A row
+//     may see nothing of its first tiles: its maximum then stays -inf and its
+//     weights zero until it sees a key.
 //   * TMEM: 512 columns (S0, S1, O0, O1, 128 each); shared memory: Q0, Q1,
 //     two K and two V stages (192 KB).
 #include <algorithm>
@@ -116,7 +125,34 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
   return __all_sync(0xffffffffu, ok);
 }
 
+// The keys a pair of query tiles walks: those below `se` (sinks) and from `lo`
+// on (the first row's window), up to n_keys. Walked tile `it` starts at key
+// base(it): `ns` tiles from key 0, the others from key wb (block-aligned) on.
+// Sinks whose tiles would reach into the window's are walked with it, from
+// key 0.
+struct PairKeys {
+  int se, lo, ns, wb;
+  __device__ __forceinline__ int base(int it) const {
+    return it < ns ? it * kBN : wb + (it - ns) * kBN;
+  }
+  // walked tiles that hold the keys below `end`
+  __device__ __forceinline__ int tiles(int end) const {
+    return ns + (max(end - wb, 0) + kBN - 1) / kBN;
+  }
+};
+
 template <int BS>
+__device__ __forceinline__ PairKeys pair_keys(int first_pos, int window, int sinks) {
+  PairKeys k;
+  k.lo = max(0, first_pos - window + 1);
+  k.se = min(sinks, k.lo);
+  k.ns = (k.se + kBN - 1) / kBN;
+  k.wb = k.lo / BS * BS;
+  if (k.ns * kBN >= k.wb) k.ns = k.wb = 0;
+  return k;
+}
+
+template <int BS, bool WIN>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap qmap,
                    const __grid_constant__ CUtensorMap kmap,
@@ -149,12 +185,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   const bool has1 = t00 + TPT < q_len;
   // K/V tiles each query tile needs (keys its last row can see)
   int Tq[2];
-  Tq[0] = (min(cached + min(t00 + TPT, q_len), kv_len) + kBN - 1) / kBN;
-  Tq[1] = has1 ? (min(cached + min(t00 + 2 * TPT, q_len), kv_len) + kBN - 1) / kBN : 0;
+  PairKeys pk{};
+  if constexpr (WIN) pk = pair_keys<BS>(cached + t00, a.window, a.sinks);
+  auto tiles_to = [&](int end) { return WIN ? pk.tiles(end) : (end + kBN - 1) / kBN; };
+  auto tile_base = [&](int n) { return WIN ? pk.base(n) : n * kBN; };
+  Tq[0] = tiles_to(min(cached + min(t00 + TPT, q_len), kv_len));
+  Tq[1] = has1 ? tiles_to(min(cached + min(t00 + 2 * TPT, q_len), kv_len)) : 0;
   const int T = max(Tq[0], Tq[1]);
   // P.V takes P as two bf16 terms on key tile 0 of a query tile whose first
-  // row sees fewer than kBN keys (every key of such a row lies in tile 0)
-  auto two_term = [&](int i) { return cached + t00 + i * TPT < kBN; };
+  // row sees fewer than kBN keys (every key of such a row lies in tile 0), and
+  // on every tile of a window of fewer than kBN keys
+  const bool narrow = WIN && min(a.window, kBN) + min(a.sinks, kBN) < kBN;
+  auto two_term = [&](int i, int n) {
+    return (n == 0 && cached + t00 + i * TPT < kBN) || narrow;
+  };
   __nv_bfloat16* const out = static_cast<__nv_bfloat16*>(a.out);
   const int H = a.num_heads;
 
@@ -220,9 +264,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     // row of its first key), the next window's table reads in flight while
     // the current one is used.
     auto load_ids = [&](int wb) {
-      const int lb = wb + lane;
+      int lb = wb + lane;
+      bool need = true;
+      if constexpr (WIN) {  // wb + lane counts walked blocks
+        lb = tile_base((wb + lane) / kBlocksPerTile) / BS + (wb + lane) % kBlocksPerTile;
+        need = lb * BS < pk.se || (lb + 1) * BS > pk.lo;
+      }
       int rc = oob;
-      if (lb * BS < n_keys && lb < a.max_blocks) {
+      if (need && lb * BS < n_keys && lb < a.max_blocks) {
         const int phys = a.block_tables[bt_row + lb];
         if (phys >= 0 && phys < a.num_blocks) {
           rc = phys * BS;
@@ -280,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     };
     auto issue_pv = [&](int i, int n) {  // O_i += P_i V(n)
       const int vs = n % kVStages;
-      const int terms = n == 0 && two_term(i) ? 2 : 1;
+      const int terms = two_term(i, n) ? 2 : 1;
       tc::fence_after_sync();
       if (lane == 0) {
 #pragma unroll 1
@@ -306,7 +355,29 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int n = 0; ok && n < T; ++n) {
       const int s = n % kVStages;
       if (!warp_wait(bar(BAR_VF + s), (n / kVStages) & 1, &abort_flag, a.err)) break;
-      const int r0 = kv_len - n * kBN;
+      const int r0 = kv_len - tile_base(n);
+      if constexpr (WIN) {
+        // V rows of keys [se, lo), which no row sees, in the blocks around
+        // the bounds (whole blocks of them were not fetched)
+        uint8_t* vp = base_ptr + (v_s(s) - base);
+        const int kb = tile_base(n);
+        bool wrote = false;
+        auto zero_rows = [&](int k0, int k1) {  // keys k0 .. k1-1, as far as in this tile
+          const int z0 = max(k0 - kb, 0), z1 = min(k1 - kb, kBN);
+          for (int e = lane; e < (z1 - z0) * 16; e += 32) {
+            const int row = z0 + (e >> 4), c = e & 15;
+            *reinterpret_cast<uint4*>(vp + (c >> 3) * kSub + row * 128 + (c & 7) * 16) =
+                make_uint4(0, 0, 0, 0);
+          }
+          wrote |= z1 > z0;
+        };
+        zero_rows(pk.se, min(pk.lo, (pk.se + BS - 1) / BS * BS));
+        zero_rows(max(pk.se, pk.lo / BS * BS), pk.lo);
+        if (wrote) {
+          fence_proxy_async_smem();
+          __syncwarp();
+        }
+      }
       if (r0 > 0 && r0 < kBN && (r0 % BS) != 0) {
         const int r1 = min(kBN, (r0 / BS + 1) * BS);
         uint8_t* vp = base_ptr + (v_s(s) - base);
@@ -370,19 +441,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         break;
       }
       tc::fence_after_sync();
-      const int lim = last_key - n * kBN;  // keys 0..lim of this tile are visible
+      const int lim = last_key - tile_base(n);  // keys 0..lim of this tile are visible
+      // ... and with a window, of those, the ones past wl or before sk
+      const int wl = WIN ? tok + cached - a.window - tile_base(n) : -1;
+      const int sk = WIN ? a.sinks - tile_base(n) : 0;
       // the whole score row in registers: one TMEM round trip
       uint32_t u[4][32];
 #pragma unroll
       for (int c = 0; c < 4; ++c) tc::tmem_ld32(tS(ti) + trow + 32 * c, u[c]);
       tc::tmem_wait_ld();
       // most tiles lie wholly left of every row's diagonal: no mask there
-      if (!__all_sync(0xffffffffu, lim >= kBN - 1)) {
+      if (!__all_sync(0xffffffffu, lim >= kBN - 1 && (!WIN || wl < 0 || sk >= kBN))) {
 #pragma unroll
         for (int c = 0; c < 4; ++c)
 #pragma unroll
           for (int j = 0; j < 32; ++j)
-            if (32 * c + j > lim) u[c][j] = __float_as_uint(-INFINITY);
+            if (32 * c + j > lim || (WIN && 32 * c + j <= wl && 32 * c + j >= sk))
+              u[c][j] = __float_as_uint(-INFINITY);
       }
       float mx = -INFINITY;
 #pragma unroll
@@ -399,7 +474,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc::fence_after_sync();
         const float m_new = fmaxf(m_used, m_tile);
-        const float alpha = fast_exp2(m_used - m_new);
+        // (a windowed row that has seen no key yet: 0 + nothing to rescale)
+        const float alpha = WIN && m_new == -INFINITY ? 1.f : fast_exp2(m_used - m_new);
         uint32_t w[32];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
@@ -416,7 +492,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // P = 2^(s*scale*log2e - m_used) as bf16, keys 64h..64h+63 -> columns 32h..32h+31
       // (masked keys hold -inf: P = 0); pairs of keys share one packed FMA for
       // the exponent argument and one packed add for the row sum
-      const uint64_t sl2x2 = tc::f32x2(sl2, sl2), nmx2 = tc::f32x2(-m_used, -m_used);
+      const float nm = WIN && m_used == -INFINITY ? 0.f : -m_used;
+      const uint64_t sl2x2 = tc::f32x2(sl2, sl2), nmx2 = tc::f32x2(nm, nm);
       uint64_t lsum = tc::f32x2(0.f, 0.f);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -434,7 +511,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc::tmem_st32(tS(ti) + trow + 32 * h, w);
       }
-      if (n == 0 && two_term(ti)) {
+      if (two_term(ti, n)) {
         // second term of P, p - bf16(p) as bf16, into columns 64..127: P is
         // computed again from the scores (the same operations, the same values)
 #pragma unroll
@@ -495,7 +572,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int BS>
+template <int BS, bool WIN>
 cudaError_t launch_bs(const PrefillArgs& a, const CUtensorMap& qmap, const CUtensorMap& kmap,
                       const CUtensorMap& vmap, cudaStream_t stream) {
   static bool attr_set[64] = {};
@@ -504,7 +581,7 @@ cudaError_t launch_bs(const PrefillArgs& a, const CUtensorMap& qmap, const CUten
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!attr_set[dev]) {
-    e = cudaFuncSetAttribute(prefill_kernel<BS>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    e = cudaFuncSetAttribute(prefill_kernel<BS, WIN>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
     if (e != cudaSuccess) return e;
     attr_set[dev] = true;
   }
@@ -519,7 +596,7 @@ cudaError_t launch_bs(const PrefillArgs& a, const CUtensorMap& qmap, const CUten
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, prefill_kernel<BS>, qmap, kmap, vmap, a);
+  return cudaLaunchKernelEx(&cfg, prefill_kernel<BS, WIN>, qmap, kmap, vmap, a);
 }
 
 }  // namespace
@@ -527,8 +604,12 @@ cudaError_t launch_bs(const PrefillArgs& a, const CUtensorMap& qmap, const CUten
 cudaError_t launch_prefill(const PrefillArgs& a, const CUtensorMap& qmap, const CUtensorMap& kmap,
                            const CUtensorMap& vmap, cudaStream_t stream) {
   if (a.head_dim != kD || kBM % a.group != 0) return cudaErrorInvalidValue;
-  if (a.block_size == 16) return launch_bs<16>(a, qmap, kmap, vmap, stream);
-  if (a.block_size == 32) return launch_bs<32>(a, qmap, kmap, vmap, stream);
+  if (a.block_size != 16 && a.block_size != 32) return cudaErrorInvalidValue;
+  if (a.window > 0)
+    return a.block_size == 16 ? launch_bs<16, true>(a, qmap, kmap, vmap, stream)
+                              : launch_bs<32, true>(a, qmap, kmap, vmap, stream);
+  if (a.block_size == 16) return launch_bs<16, false>(a, qmap, kmap, vmap, stream);
+  if (a.block_size == 32) return launch_bs<32, false>(a, qmap, kmap, vmap, stream);
   return cudaErrorInvalidValue;
 }
 

@@ -18,6 +18,7 @@ struct PrefillArgs {
   int tokens_per_tile;  // 128 / group query tokens per 128-row tile
   int num_qtiles;       // tiles per sequence in the grid (from the max q_len bound)
   float scale_log2;
+  int window, sinks;    // sliding window (> 0) with leading sink keys; 0 = all keys
 };
 
 // Query tokens per 128-row tile for a head group of `group` query heads.

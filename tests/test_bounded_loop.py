@@ -1,0 +1,101 @@
+"""The bounded-cache operators together: a prompt (norm_rope_store, prefill_window), then
+decode steps (norm_rope_store, decode_scored) with an evict every few of them, against the
+same loop in plain 64-bit arithmetic on the caches the library wrote."""
+import numpy as np
+import pytest
+import torch
+
+import ops64
+import paged_kv_cache_186_gb300 as pa
+from gpu_util import assert_attention_close
+from test_norm_rope import check_rows, table
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+def test_generation_over_a_bounded_cache(kv):
+    H, Hkv, D, bs, B = 8, 2, 128, 16, 3
+    prompts, budget, sinks, recent, every, steps = [70, 5, 41], 48, 2, 16, 6, 30
+    g = torch.Generator().manual_seed(400)
+    nb, width = 64, 10
+    bt = torch.randperm(nb, generator=g)[:B * width].view(B, width).to(torch.int32).cuda()
+    if kv == "bf16":
+        kc, vc = (torch.full((nb, bs, Hkv, D), float("nan"), dtype=torch.bfloat16).cuda()
+                  for _ in range(2))
+        ks = vs = None
+    else:
+        kc, vc = (torch.full((nb, bs, Hkv, D), 0x7f, dtype=torch.uint8).cuda() for _ in range(2))
+        ks, vs = (torch.full((nb, Hkv, bs), float("nan")).cuda() for _ in range(2))
+    scores = torch.full((nb, Hkv, bs), float("nan")).cuda()
+    cs = torch.from_numpy(table(512, D)).cuda()
+    qw, kw = (1 + 0.2 * torch.randn((2, D), generator=g)).to(torch.bfloat16).cuda()
+    scale = 1 / np.sqrt(D)
+    n64 = lambda t: t.float().cpu().double().numpy()
+
+    def store(n_per_seq, slot_pos, pos):
+        """Project, norm, rotate and store new tokens; slots from cache positions slot_pos."""
+        T = sum(n_per_seq)
+        qkv = torch.randn((T, (H + 2 * Hkv) * D), generator=g).to(torch.bfloat16).cuda()
+        q, k, v = (x.view(T, -1, D) for x in qkv.split([H * D, Hkv * D, Hkv * D], dim=1))
+        rows = bt.cpu().numpy()
+        slots, at = [], 0
+        for b, n in enumerate(n_per_seq):
+            for p in slot_pos[at:at + n]:
+                slots.append(int(rows[b, p // bs]) * bs + p % bs)
+            at += n
+        out = pa.norm_rope_store(q, k, v, torch.tensor(pos).cuda(), torch.tensor(slots).cuda(), kc,
+                                 vc, q_weight=qw, k_weight=kw, cos_sin=cs, k_scale=ks, v_scale=vs,
+                                 scores=scores)
+        want, mag = ops64.norm_rope(n64(q), n64(qw), 1e-6, cs.cpu().numpy(), np.array(pos), False)
+        check_rows(n64(out), want, mag, "q")
+        return out
+
+    def values():
+        return (ops64.cache_values(c.cpu(), None if s is None else s.cpu())
+                for c, s in ((kc, ks), (vc, vs)))
+
+    where = [p for n in prompts for p in range(n)]
+    q = store(prompts, where, where)
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(prompts)]), dtype=torch.int32).cuda()
+    if kv == "bf16":
+        out = pa.prefill_window(q, kc, vc, bt, cu, cu, scale, 32, sinks)
+        K, V = values()
+        want = ops64.prefill_window(n64(q), np.nan_to_num(K), np.nan_to_num(V), bt.cpu().numpy(),
+                                    cu.cpu().numpy(), cu.cpu().numpy(), scale, 32, sinks)
+        assert_attention_close(out, want, "prompt")
+    lens = torch.tensor(prompts, dtype=torch.int32).cuda()
+    position = list(prompts)  # a token's position keeps counting past evictions
+    cut = 0
+    for step in range(steps):
+        host = lens.tolist()
+        q = store([1] * B, host, position)
+        position = [p + 1 for p in position]
+        lens = lens + 1
+        before = n64(scores)
+        out = pa.decode_scored(q, kc, vc, bt, lens, scores, scale, k_scale=ks, v_scale=vs)
+        K, V = values()
+        want, add, mag = ops64.decode_scored(n64(q), np.nan_to_num(K), np.nan_to_num(V),
+                                             bt.cpu().numpy(), lens.tolist(), scale,
+                                             tuple(scores.shape))
+        assert_attention_close(out, want, f"step {step}")
+        live = add > 0
+        tol = mag * 2.0 ** -15 + add * 2.0 ** -19 + np.abs(before) * 2.0 ** -23
+        assert (np.abs(n64(scores) - before - add)[live] <= tol[live]).all()
+        if step % every == every - 1:
+            s = {n: t.cpu() if t is not None else None
+                 for n, t in (("kc", kc), ("vc", vc), ("scores", scores), ("ks", ks), ("vs", vs))}
+            lens, kept = pa.evict(kc, vc, scores, bt, lens, budget, sinks=sinks, recent=recent,
+                                  k_scale=ks, v_scale=vs)
+            host = [n + 1 for n in host]
+            rows, new = ops64.evict_rows(s["scores"].numpy(), bt.cpu().numpy(), host, budget, sinks,
+                                         recent)
+            assert np.array_equal(kept.cpu().numpy(), rows)
+            assert np.array_equal(lens.cpu().numpy(), new)
+            for n, t, by_slot in (("kc", kc, True), ("vc", vc, True), ("scores", scores, False)):
+                moved = ops64.move_rows(s[n], by_slot, rows, bt.cpu().numpy(), host, budget, bs)
+                bits = torch.uint8 if by_slot and kv == "fp8" else torch.int16 if by_slot else torch.int32
+                assert torch.equal(t.cpu().view(bits), moved.view(bits)), n
+            cut += int((np.array(host) > budget).sum())
+    assert pa.get_device_error() == 0
+    assert cut >= 5 and lens.max() <= budget + every

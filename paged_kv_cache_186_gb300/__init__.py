@@ -154,9 +154,9 @@ def _check(code: int, what: str):
 
 def _want(t: torch.Tensor, name: str, dtype: torch.dtype, shape, contiguous: bool = True):
     """Refuse a tensor of another type, shape or layout than a call reads or writes."""
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:  # a torch.Size is a tuple
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if contiguous and not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -164,31 +164,37 @@ def _want(t: torch.Tensor, name: str, dtype: torch.dtype, shape, contiguous: boo
 
 def _checked_cache(k_cache, v_cache, k_scale, v_scale, *others) -> KVCache:
     """make_cache of caches that agree with each other, on one device with `others`."""
-    if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype or k_cache.dim() != 4:
+    shape = k_cache.shape
+    if v_cache.shape != shape or v_cache.dtype is not k_cache.dtype or len(shape) != 4:
         raise ValueError("k_cache and v_cache must have the same 4-D shape and dtype")
     if (k_scale is None) != (v_scale is None):
         raise ValueError("k_scale and v_scale come together")
     if k_scale is not None:
-        shape = (k_cache.shape[0], k_cache.shape[2], k_cache.shape[1])
-        _want(k_scale, "k_scale", torch.float32, shape)
-        _want(v_scale, "v_scale", torch.float32, shape)
+        sshape = (shape[0], shape[2], shape[1])
+        _want(k_scale, "k_scale", torch.float32, sshape)
+        _want(v_scale, "v_scale", torch.float32, sshape)
     cache = make_cache(k_cache, v_cache, k_scale, v_scale)
-    dev = k_cache.device
-    if dev.type != "cuda":
+    dev = k_cache.get_device()  # -1: not a CUDA tensor
+    if dev < 0:
         raise ValueError("the tensors must be on a CUDA device")
     for t in (v_cache, k_scale, v_scale) + others:
-        if t is not None and t.device != dev:
-            raise ValueError(f"all tensors must be on {dev}, got one on {t.device}")
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"all tensors must be on {k_cache.device}, got one on {t.device}")
     return cache
 
 
-def _run(device: torch.device, what: str, fn, *args) -> None:
-    """fn(*args, stream) on the tensors' device and its current stream."""
-    if device.index == torch.cuda.current_device():
-        _check(fn(*args, _stream()), what)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _run(device: int, what: str, fn, *args) -> None:
+    """fn(*args, stream) on device `device` and its current stream."""
+    if device == _current_device():
+        code = fn(*args, _raw_stream(device) if _raw_stream is not None else _stream())
     else:
         with torch.cuda.device(device):
-            _check(fn(*args, _stream()), what)
+            code = fn(*args, _stream())
+    if code != 0:
+        raise PAError(code, what)
 
 
 def make_cache(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor | None = None,
@@ -349,23 +355,24 @@ def prefill_varlen(q, k_cache, v_cache, block_tables, cu_seqlens_q, cu_seqlens_k
     return out
 
 
-def _token_rows(t: torch.Tensor, name: str, heads, head_dim: int):
-    """(tensor, element stride between its tokens) of (T, heads, head_dim) bf16 whose tokens'
-    heads are contiguous: a view of a fused projection's output is taken as it is, any other
-    layout is copied."""
-    if t.dtype != torch.bfloat16:
+def _token_rows(t: torch.Tensor, name: str, shape):
+    """(address, element stride between tokens, tensor) of bf16 `shape` = (T, heads, head_dim)
+    whose tokens' heads are contiguous: a view of a fused projection's output is taken as it
+    is, any other layout is copied."""
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
-    if t.dim() != 3 or t.shape[2] != head_dim or (heads is not None and t.shape[1] != heads):
-        raise ValueError(f"{name} must have shape (tokens, "
-                         f"{'heads' if heads is None else heads}, {head_dim}), got "
-                         f"{tuple(t.shape)}")
-    T, H, D = t.shape
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    T, H, D = shape
+    row = H * D
     st, sh, sd = t.stride()
     if T == 1:
-        st = H * D
-    if (sd != 1 or (H > 1 and sh != D) or st < H * D or st % 8 != 0 or t.data_ptr() % 16 != 0):
-        return t.clone(memory_format=torch.contiguous_format), H * D
-    return t, st
+        st = row
+    p = t.data_ptr()
+    if sd != 1 or (H > 1 and sh != D) or st < row or st % 8 != 0 or p % 16 != 0:
+        t = t.clone(memory_format=torch.contiguous_format)
+        return t.data_ptr(), row, t
+    return p, st, t
 
 
 def norm_rope_store(q, k, v, positions, slot_mapping, k_cache, v_cache, *, q_weight=None,
@@ -378,41 +385,41 @@ def norm_rope_store(q, k, v, positions, slot_mapping, k_cache, v_cache, *, q_wei
     for an 8-bit cache. Returns q_out (T, H, D) bf16 (rows of padding tokens are not written);
     it may be q itself if q is contiguous. q, k and v may be views of one fused projection's
     output. scores: set the slots' scores (decode_scored) to 0."""
-    D = k_cache.shape[3]
-    T, H = q.shape[0], q.shape[1] if q.dim() == 3 else 0
-    Hkv = k_cache.shape[2]
-    qc, qs = _token_rows(q, "q", None, D)
-    kc, ks = _token_rows(k, "k", Hkv, D)
-    vc, vs = _token_rows(v, "v", Hkv, D)
-    if k.shape[0] != T or v.shape[0] != T:
-        raise ValueError("q, k and v must have the same number of tokens")
+    NB, bs, Hkv, D = k_cache.shape
+    if q.dim() != 3:
+        raise ValueError("q must be (tokens, num_heads, head_dim)")
+    T, H, _ = q.shape
+    qp, qs, qc = _token_rows(q, "q", (T, H, D))
+    kp, ks, kc = _token_rows(k, "k", (T, Hkv, D))
+    vp, vs, vc = _token_rows(v, "v", (T, Hkv, D))
     _want(slot_mapping, "slot_mapping", torch.int64, (T,))
+    rows = rot = 0
     if cos_sin is not None:
         if cos_sin.dim() != 2:
             raise ValueError("cos_sin must be (max_positions, rotary_dim)")
-        _want(cos_sin, "cos_sin", torch.float32, cos_sin.shape)
+        rows, rot = cos_sin.shape
+        _want(cos_sin, "cos_sin", torch.float32, (rows, rot))
         if positions is None:
             raise ValueError("a rotation needs positions")
     if positions is not None:
         _want(positions, "positions", torch.int64, (T,))
-    for w, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if w is not None:
-            _want(w, name, torch.bfloat16, (D,))
+    if q_weight is not None:
+        _want(q_weight, "q_weight", torch.bfloat16, (D,))
+    if k_weight is not None:
+        _want(k_weight, "k_weight", torch.bfloat16, (D,))
     if scores is not None:
-        _want(scores, "scores", torch.float32, (k_cache.shape[0], Hkv, k_cache.shape[1]))
+        _want(scores, "scores", torch.float32, (NB, Hkv, bs))
     if q_out is None:
         q_out = torch.empty((T, H, D), dtype=torch.bfloat16, device=q.device)
     else:
         _want(q_out, "q_out", torch.bfloat16, (T, H, D))
     cache = _checked_cache(k_cache, v_cache, k_scale, v_scale, q, k, v, positions, slot_mapping,
                            q_weight, k_weight, cos_sin, q_out, scores)
-    rot = 0 if cos_sin is None else cos_sin.shape[1]
-    params = NormRope(_ptr(q_weight), _ptr(k_weight), _ptr(cos_sin),
-                      0 if cos_sin is None else cos_sin.shape[0], rot, int(bool(interleaved)),
-                      float(eps))
-    _run(q.device, "pa_norm_rope_store", lib().pa_norm_rope_store, qc.data_ptr(), qs,
-         kc.data_ptr(), ks, vc.data_ptr(), vs, ctypes.byref(params), _ptr(positions),
-         slot_mapping.data_ptr(), T, H, ctypes.byref(cache), _ptr(scores), q_out.data_ptr())
+    params = NormRope(_ptr(q_weight), _ptr(k_weight), _ptr(cos_sin), rows, rot,
+                      1 if interleaved else 0, eps)
+    _run(q.get_device(), "pa_norm_rope_store", lib().pa_norm_rope_store, qp, qs, kp, ks, vp, vs,
+         ctypes.byref(params), _ptr(positions), slot_mapping.data_ptr(), T, H,
+         ctypes.byref(cache), _ptr(scores), q_out.data_ptr())
     return q_out
 
 
@@ -438,7 +445,7 @@ def prefill_window(q, k_cache, v_cache, block_tables, cu_seqlens_q, cu_seqlens_k
         _want(out, "out", torch.bfloat16, (T, H, D))
     cache = _checked_cache(k_cache, v_cache, None, None, q, block_tables, cu_seqlens_q,
                            cu_seqlens_k, out)
-    _run(q.device, "pa_prefill_window", lib().pa_prefill_window, qc.data_ptr(),
+    _run(q.get_device(), "pa_prefill_window", lib().pa_prefill_window, qc.data_ptr(),
          ctypes.byref(cache), block_tables.data_ptr(), block_tables.shape[1],
          cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), n - 1, H, T, int(max_q_len),
          float(scale), int(window), int(sinks), out.data_ptr())
@@ -484,7 +491,7 @@ def decode_scored(q, k_cache, v_cache, block_tables, context_lens, scores, scale
         if need:
             workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _run(q.device, "pa_decode_scored", lib().pa_decode_scored, qc.data_ptr(), ctypes.byref(cache),
+    _run(q.get_device(), "pa_decode_scored", lib().pa_decode_scored, qc.data_ptr(), ctypes.byref(cache),
          block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(),
          int(max_context_len), B, H, float(scale), scores.data_ptr(), out.data_ptr(),
          _ptr(workspace), ws_bytes)
@@ -516,7 +523,7 @@ def evict(k_cache, v_cache, scores, block_tables, context_lens, budget: int, *, 
         _want(new_lens, "new_lens", torch.int32, (B,))
     cache = _checked_cache(k_cache, v_cache, k_scale, v_scale, scores, block_tables,
                            context_lens, kept, new_lens)
-    _run(scores.device, "pa_evict", lib().pa_evict, ctypes.byref(cache), scores.data_ptr(),
+    _run(scores.get_device(), "pa_evict", lib().pa_evict, ctypes.byref(cache), scores.data_ptr(),
          block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(),
          int(max_context_len), B, budget, int(sinks), int(recent), kept.data_ptr(),
          new_lens.data_ptr())

@@ -22,6 +22,7 @@
 #include "pa_device.cuh"
 #include "pa_launch.h"
 #include "pa_norm_rope.h"
+#include "pa_tcgen05.cuh"
 
 namespace pa {
 
@@ -37,6 +38,11 @@ __device__ __forceinline__ void unpack8(const uint4& u, float (&x)[8]) {
     x[2 * i] = __uint_as_float(w[i] << 16);
     x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
   }
+}
+
+// Two bf16 (one word) -> a packed pair of fp32.
+__device__ __forceinline__ uint64_t unpack2(uint32_t w) {
+  return tc::f32x2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
 }
 
 __device__ __forceinline__ uint4 pack8(const float (&x)[8]) {
@@ -74,12 +80,14 @@ __device__ __forceinline__ uint2 codes8(const float (&x)[8]) {
   }
 }
 
-// One warp: NIT rounds of 256/D rows of one kind of one token.
+// One warp: rows_per_warp rows of one kind of one token, in batches of NIT
+// rounds of 256/D rows; a batch's rows are read while the one before is worked
+// on.
 template <int D, int KV, bool INTER, int NIT>
-__global__ void __launch_bounds__(kNrWarps * 32) norm_rope_kernel(const NormRopeArgs a) {
+__global__ void __launch_bounds__(kNrWarps * 32, NIT == 2 ? 8 : NIT == 4 ? 6 : 1) norm_rope_kernel(const NormRopeArgs a) {
   constexpr int LPR = D / 8;     // lanes per row
   constexpr int RPW = 32 / LPR;  // rows of a round
-  constexpr int RW = NIT * RPW;  // rows of a warp
+  constexpr int RW = NIT * RPW;  // rows of a batch
   // launched as a programmatic dependent: everything is read after the wait,
   // and the next launch may start only then (a decode reads the lengths and
   // the block tables before its own wait; what wrote them is complete here)
@@ -88,27 +96,31 @@ __global__ void __launch_bounds__(kNrWarps * 32) norm_rope_kernel(const NormRope
   const int lane = threadIdx.x & 31;
   const int sub = lane / LPR, c = lane % LPR;
   const int H = a.num_heads, Hkv = a.num_kv_heads;
-  const int nq = (H + RW - 1) / RW, nk = (Hkv + RW - 1) / RW;
-  const int wpt = nq + 2 * nk;  // warps per token
-  const long long w = static_cast<long long>(blockIdx.x) * kNrWarps + (threadIdx.x >> 5);
+  const int RPT = a.rows_per_warp;
+  const int nq = (H + RPT - 1) / RPT, nk = (Hkv + RPT - 1) / RPT;
+  const unsigned wpt = nq + 2 * nk;  // warps per token
+  const unsigned w = blockIdx.x * kNrWarps + (threadIdx.x >> 5);
   const long long t = w / wpt;
   if (t >= a.num_tokens) return;
-  int part = static_cast<int>(w - t * wpt);
+  int part = static_cast<int>(w % wpt);
   const int kind = part < nq ? 0 : part < nq + nk ? 1 : 2;  // q, k, v
   part -= kind == 0 ? 0 : kind == 1 ? nq : nq + nk;
-  const int rows = kind == 0 ? H : Hkv;
-  const int row0 = part * RW + sub;
+  const int row0 = part * RPT + sub;
+  const int rows = min(kind == 0 ? H : Hkv, part * RPT + RPT);
 
   const __nv_bfloat16* src =
       static_cast<const __nv_bfloat16*>(kind == 0 ? a.q : kind == 1 ? a.k : a.v) +
       t * (kind == 0 ? a.q_stride : kind == 1 ? a.k_stride : a.v_stride) + c * 8;
-  uint4 raw[NIT];
+  uint4 raw[NIT], nxt[NIT];
+  auto load = [&](uint4 (&x)[NIT], int r0) {
 #pragma unroll
-  for (int i = 0; i < NIT; ++i) {
-    const int r = row0 + i * RPW;
-    raw[i] = make_uint4(0u, 0u, 0u, 0u);
-    if (r < rows) raw[i] = *reinterpret_cast<const uint4*>(src + r * D);
-  }
+    for (int i = 0; i < NIT; ++i) {
+      const int r = r0 + i * RPW;
+      x[i] = make_uint4(0u, 0u, 0u, 0u);
+      if (r < rows) x[i] = *reinterpret_cast<const uint4*>(src + r * D);
+    }
+  };
+  load(raw, row0);
   const long long slot = a.slot_mapping[t];
   if (slot < 0) return;  // padding token
   const int rot = a.rotary_dim;
@@ -126,20 +138,21 @@ __global__ void __launch_bounds__(kNrWarps * 32) norm_rope_kernel(const NormRope
   }
 
   // ---- factors of this lane's eight elements: y_i = rstd * (x_i A_i + partner_i B_i)
+  // (a lane that is not rotated adds 0 * -0 = -0: x * A unchanged, zeros too)
   float A[8], B[8];
   const void* const wt = kind == 0 ? a.q_weight : kind == 1 ? a.k_weight : nullptr;
   const bool norm = wt != nullptr;
   int pc = c;  // chunk that holds the partners of a half-split pair
+  float wf[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) wf[i] = 1.f;
+  if (norm) unpack8(__ldg(static_cast<const uint4*>(wt) + c), wf);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    A[i] = wf[i];
+    B[i] = -0.f;
+  }
   if (kind != 2) {
-    float wf[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) wf[i] = 1.f;
-    if (norm) unpack8(__ldg(static_cast<const uint4*>(wt) + c), wf);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      A[i] = wf[i];
-      B[i] = 0.f;
-    }
     if (c * 8 < rot) {
       const float* cs = a.cos_sin + pos * rot;
       if constexpr (INTER) {
@@ -179,79 +192,89 @@ __global__ void __launch_bounds__(kNrWarps * 32) norm_rope_kernel(const NormRope
 
   const long long blk = kind == 0 ? 0 : slot / a.block_size;
   const int off = kind == 0 ? 0 : static_cast<int>(slot - blk * a.block_size);
+  const uint32_t pmask = kind != 2 && c * 8 < rot ? 0xffffffffu : 0u;  // not rotated: no partner
+  uint64_t A2[4], B2[4];
 #pragma unroll
-  for (int i = 0; i < NIT; ++i) {
-    const int r = row0 + i * RPW;
-    float x[8];
-    unpack8(raw[i], x);
-    if (kind != 2) {
-      float rstd = 1.f;
-      if (norm) {
-        float ss = 0.f;
+  for (int j = 0; j < 4; ++j) {
+    A2[j] = tc::f32x2(A[2 * j], A[2 * j + 1]);
+    B2[j] = tc::f32x2(B[2 * j], B[2 * j + 1]);
+  }
+#pragma unroll 1
+  for (int r0 = row0; r0 - sub < rows; r0 += RW) {
+    if (r0 - sub + RW < rows) load(nxt, r0 + RW);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) ss = fmaf(x[j], x[j], ss);
+    for (int i = 0; i < NIT; ++i) {
+      const int r = r0 + i * RPW;
+      float x[8];
+      if (kind != 2) {
+        const uint32_t xw[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+        uint64_t x2[4];
 #pragma unroll
-        for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(kAll, ss, o);
-        rstd = rsqrtf(ss * (1.f / D) + a.eps);
+        for (int j = 0; j < 4; ++j) x2[j] = unpack2(xw[j]);
+        float rstd = 1.f;
+        if (norm) {
+          uint64_t s2 = tc::fma_f32x2(x2[0], x2[0], tc::f32x2(0.f, 0.f));
+#pragma unroll
+          for (int j = 1; j < 4; ++j) s2 = tc::fma_f32x2(x2[j], x2[j], s2);
+          float s0, s1;
+          tc::f32x2_split(s2, s0, s1);
+          float ss = s0 + s1;
+#pragma unroll
+          for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(kAll, ss, o);
+          rstd = rsqrtf(ss * (1.f / D) + a.eps);
+        }
+        const uint64_t r2 = tc::f32x2(rstd, rstd);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t pw = INTER ? prmt(xw[j], 0u, 0x1032u) : __shfl_sync(kAll, xw[j], plane);
+          const uint64_t y2 = tc::mul_f32x2(unpack2(pw & pmask), B2[j]);
+          tc::f32x2_split(tc::mul_f32x2(tc::fma_f32x2(x2[j], A2[j], y2), r2), x[2 * j], x[2 * j + 1]);
+        }
+      } else if (KV != kKvBf16) {
+        unpack8(raw[i], x);
       }
-      float y[8];
-      if constexpr (INTER) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = x[j ^ 1];
+      if (kind == 0) {
+        if (r < rows)
+          *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.q_out) +
+                                    (t * H + r) * D + c * 8) = pack8(x);
+        continue;
+      }
+      void* const cache = kind == 1 ? a.k_cache : a.v_cache;
+      const long long row = slot * Hkv + r;  // (slot, head) row of the cache
+      if constexpr (KV == kKvBf16) {
+        if (r < rows)
+          *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(cache) + row * D + c * 8) =
+              kind == 2 ? raw[i] : pack8(x);
       } else {
-        uint4 pr;
-        pr.x = __shfl_sync(kAll, raw[i].x, plane);
-        pr.y = __shfl_sync(kAll, raw[i].y, plane);
-        pr.z = __shfl_sync(kAll, raw[i].z, plane);
-        pr.w = __shfl_sync(kAll, raw[i].w, plane);
-        unpack8(pr, y);
+        float amax = 0.f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) amax = max_nan(amax, fabsf(x[j]));
+#pragma unroll
+        for (int o = LPR / 2; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(kAll, amax, o));
+        float sc = amax / (KV == kKvE4m3 ? 448.f : 127.f);
+        if (sc == 0.f) sc = 1.f;  // a row of zeros (or whose scale underflows)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = x[j] / sc;
+        if (r < rows) {
+          *reinterpret_cast<uint2*>(static_cast<uint8_t*>(cache) + row * D + c * 8) = codes8<KV>(x);
+          if (c == 0) (kind == 1 ? a.k_scale : a.v_scale)[(blk * Hkv + r) * a.block_size + off] = sc;
+        }
       }
-      if (c * 8 < rot) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = rstd * fmaf(x[j], A[j], y[j] * B[j]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = rstd * (x[j] * A[j]);
-      }
+      if (kind == 1 && a.scores != nullptr && c == 0 && r < rows)
+        a.scores[(blk * Hkv + r) * a.block_size + off] = 0.f;
     }
-    if (kind == 0) {
-      if (r < rows)
-        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.q_out) +
-                                  (t * H + r) * D + c * 8) = pack8(x);
-      continue;
-    }
-    void* const cache = kind == 1 ? a.k_cache : a.v_cache;
-    const long long row = slot * Hkv + r;  // (slot, head) row of the cache
-    if constexpr (KV == kKvBf16) {
-      if (r < rows)
-        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(cache) + row * D + c * 8) =
-            kind == 2 ? raw[i] : pack8(x);
-    } else {
-      float amax = 0.f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) amax = max_nan(amax, fabsf(x[j]));
-#pragma unroll
-      for (int o = LPR / 2; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(kAll, amax, o));
-      float sc = amax / (KV == kKvE4m3 ? 448.f : 127.f);
-      if (sc == 0.f) sc = 1.f;  // a row of zeros (or whose scale underflows)
-#pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = x[j] / sc;
-      if (r < rows) {
-        *reinterpret_cast<uint2*>(static_cast<uint8_t*>(cache) + row * D + c * 8) = codes8<KV>(x);
-        if (c == 0) (kind == 1 ? a.k_scale : a.v_scale)[(blk * Hkv + r) * a.block_size + off] = sc;
-      }
-    }
-    if (kind == 1 && a.scores != nullptr && c == 0 && r < rows)
-      a.scores[(blk * Hkv + r) * a.block_size + off] = 0.f;
+    for (int i = 0; i < NIT; ++i) raw[i] = nxt[i];
   }
 }
 
 template <int D, int KV, bool INTER, int NIT>
-cudaError_t launch_inst(const NormRopeArgs& a, cudaStream_t stream) {
-  constexpr int RW = NIT * (256 / D);
-  const long long wpt = (a.num_heads + RW - 1) / RW + 2 * ((a.num_kv_heads + RW - 1) / RW);
+cudaError_t launch_inst(NormRopeArgs a, int batches, cudaStream_t stream) {
+  a.rows_per_warp = NIT * (256 / D) * batches;
+  const long long RPT = a.rows_per_warp;
+  const long long wpt = (a.num_heads + RPT - 1) / RPT + 2 * ((a.num_kv_heads + RPT - 1) / RPT);
   const long long grid = (a.num_tokens * wpt + kNrWarps - 1) / kNrWarps;
-  if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  if (grid > 0x7fffffffLL / kNrWarps) return cudaErrorInvalidConfiguration;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(grid));
   cfg.blockDim = dim3(kNrWarps * 32);
@@ -264,10 +287,30 @@ cudaError_t launch_inst(const NormRopeArgs& a, cudaStream_t stream) {
   return cudaLaunchKernelEx(&cfg, norm_rope_kernel<D, KV, INTER, NIT>, a);
 }
 
+// Rounds of a batch and batches of a warp. One round each keeps the smallest
+// calls' latency down; with more rows than the machine holds warps for, two
+// rounds and up to four batches spend the token's factors on more rows and keep
+// reads under way. us per call, (rounds x batches) 1x1 / 2x1 / 2x2 / 2x4, from
+// graph replays on one GB300, 48 rows of 128 a token (bf16): 64 tokens 2.6 / 2.9
+// / 3.5 / 4.5, 256: 4.6 / 4.2 / 3.9 / 4.9, 512: 7.0 / 6.0 / 5.5 / 5.3, 1024:
+// 13.9 / 10.3 / 8.8 / 7.7, 8192: 106 / 67 / 48 / 43; 80 rows of 128 (E4M3): 128:
+// 5.0 / 4.9 / 5.3 / 5.2, 256: 7.4 / 6.3 / 7.1 / 5.6, 512: 13.0 / 9.4 / 9.2 / 8.5;
+// 24 rows of 64: 256: 2.6 / 2.9, 1024: 4.6 / 4.0, 8192: 30 / 19.
+template <int D, int KV, bool INTER>
+cudaError_t launch_rounds(const NormRopeArgs& a, cudaStream_t stream) {
+  constexpr int RPW = 256 / D;
+  const long long rounds = static_cast<long long>(a.num_tokens) *
+                           ((a.num_heads + 2LL * a.num_kv_heads + RPW - 1) / RPW);
+  const long long slots = 32LL * a.num_sms;  // rounds in flight with half the warps of an SM
+  if (rounds <= slots) return launch_inst<D, KV, INTER, 1>(a, 1, stream);
+  if (rounds <= 2 * slots) return launch_inst<D, KV, INTER, 2>(a, 2, stream);
+  return launch_inst<D, KV, INTER, 2>(a, 4, stream);
+}
+
 template <int D, int KV>
 cudaError_t launch_kind(const NormRopeArgs& a, cudaStream_t stream) {
-  return a.interleaved ? launch_inst<D, KV, true, 1>(a, stream)
-                       : launch_inst<D, KV, false, 1>(a, stream);
+  return a.interleaved ? launch_rounds<D, KV, true>(a, stream)
+                       : launch_rounds<D, KV, false>(a, stream);
 }
 
 }  // namespace

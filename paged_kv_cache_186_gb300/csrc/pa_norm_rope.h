@@ -30,6 +30,7 @@ struct NormRopeArgs {
   int kv;  // kKvBf16, kKvE4m3 or kKvInt8
   float eps;
   int num_sms;
+  int rows_per_warp;  // set by the launch
 };
 
 cudaError_t launch_norm_rope_store(const NormRopeArgs& a, cudaStream_t stream);

@@ -110,6 +110,17 @@ def test_special_values():
         check(s, budget, 1, 2)
 
 
+def test_every_nan_is_the_largest_whatever_its_bits():
+    s = make([300], 2, 64, 16, seed=309)
+    bits = s["scores"].view(torch.int32)
+    gen = torch.Generator().manual_seed(3)
+    r = torch.randint(0, 8, bits.shape, generator=gen)
+    for i, pattern in enumerate((0x7fc00000, -0x400000, 0x7f800001, -1, 0x7fffffff)):
+        bits[r == i] = pattern  # quiet and signalling, both signs
+    for budget in (10, 150, 250):
+        check(s, budget)
+
+
 def test_scores_that_differ_in_the_last_bits_only():
     s = make([600], 1, 64, 16, seed=302)
     bits = 0x3f800000 + torch.randint(0, 40, s["scores"].shape,

@@ -188,7 +188,8 @@ __device__ __forceinline__ void load_q(const DecodeArgs& a, int b, int kvh, int 
 // lane group r; acc = O^T fragments for heads 2q4, 2q4+1). The whole block is
 // one softmax step: S for its BS tokens (BS/8 n-tiles, independent MMA
 // chains), one max/sum update, then P.V per 16-token group.
-// `raw` (SC): where the block's scores go, (group, BS) floats.
+// `raw` (SC): where the block's scores go, (group, BS) floats, those of tokens
+// {8 n + 2 i, 8 n + 2 i + 1 : n} of a head together (i = 0 .. 3).
 template <int D, int BS, int KV, bool HOLE = false, bool SC = false>
 __device__ __forceinline__ void attend_block(uint32_t kt, uint32_t vt, const uint8_t* base_ptr,
                                              uint32_t base, const float* ksc, const float* vsc,
@@ -261,11 +262,11 @@ __device__ __forceinline__ void attend_block(uint32_t kt, uint32_t vt, const uin
       if (!valid(tok0 + (j >> 1) * 8 + 2 * q4 + (j & 1))) x[j] = -INFINITY;
   }
   if constexpr (SC) {
-    if (r < group) {
+    if (r < group) {  // the lane's scores of head r side by side: 16-byte stores
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
-        *reinterpret_cast<float2*>(raw + r * BS + nt * 8 + 2 * q4) =
-            make_float2(x[2 * nt], x[2 * nt + 1]);
+      for (int j = 0; j < 2 * NT; j += 4)
+        *reinterpret_cast<float4*>(raw + r * BS + q4 * (2 * NT) + j) =
+            make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
     }
   }
   float mx = x[0];

@@ -6,12 +6,14 @@
 //
 // How: the scores lie in the decode's block order (block i of all (sequence,
 // kv head) segments holds (group, block_size) floats), so a warp takes a
-// contiguous run of blocks, 128 keys at a time: each lane four consecutive
-// keys of one block, read as one 16-byte vector per query head, summed in the
-// order of the heads and added with one vector reduction. The adds are
-// reductions, not read-modify-writes by the lane, so that sequences that share
-// physical blocks (a common prefix) may add to them in one call; a slot of one
-// sequence gets one add per call.
+// contiguous run of blocks and goes through it segment by segment, 128 keys at
+// a time: each lane four keys of one block, read as one 16-byte vector per
+// query head, all heads' loads under way at once, summed in the order of the
+// heads and added with two vector reductions. The adds are reductions, not
+// read-modify-writes by the lane, so that sequences that share physical blocks
+// (a common prefix) may add to them in one call; a slot of one sequence gets
+// one add per call. Bound by the reads of the scores, 4 bytes per key and query
+// head, as far as L2 does not hold them any more.
 #include <algorithm>
 
 #include "pa_device.cuh"
@@ -22,79 +24,117 @@ namespace pa {
 namespace {
 
 constexpr int kAsWarps = 8;
+constexpr int kAsCtas = 4;  // per SM: all of them resident (at most 64 registers a thread)
 constexpr unsigned kAll = 0xffffffffu;
 
-__device__ __forceinline__ void red_add_v4(float* p, float4 v) {
-  asm volatile("red.relaxed.gpu.global.add.v4.f32 [%0], {%1, %2, %3, %4};" ::"l"(p), "f"(v.x),
-               "f"(v.y), "f"(v.z), "f"(v.w)
+__device__ __forceinline__ void red_add_v2(float* p, float x, float y) {
+  asm volatile("red.relaxed.gpu.global.add.v2.f32 [%0], {%1, %2};" ::"l"(p), "f"(x), "f"(y)
                : "memory");
 }
 
-template <int BS>
-__global__ void __launch_bounds__(kAsWarps * 32) add_scores_kernel(const DecodeArgs a,
+template <int BS, int GP>
+__global__ void __launch_bounds__(kAsWarps * 32, kAsCtas) add_scores_kernel(const DecodeArgs a,
                                                                    float* scores) {
   constexpr int KB = 128 / BS;   // blocks of a warp's step
   constexpr int LPB = BS / 4;    // lanes per block
+  // (no early start for the next launch: a decode's would bring its first tiles
+  // into L2 over the scores that are still to be read here)
   grid_dependency_wait();
-  grid_launch_dependents();
   const int lane = threadIdx.x & 31;
   const int B = a.batch, Hkv = a.num_kv_heads, G = a.group;
   const int* const prefix = a.prefix_out;
   const long long N = static_cast<long long>(prefix[B]) * Hkv;
-  const long long steps = (N + KB - 1) / KB;
   const long long W = static_cast<long long>(gridDim.x) * kAsWarps;
   const long long w = static_cast<long long>(blockIdx.x) * kAsWarps + (threadIdx.x >> 5);
-  const long long s0 = w * steps / W, s1 = (w + 1) * steps / W;
-  if (s0 >= s1) return;
+  const long long r0 = w * N / W, r1 = (w + 1) * N / W;  // the warp's blocks
+  if (r0 >= r1) return;
   // last sequence whose blocks start at or before the warp's first one: 32
   // candidates a round
   int b = 0;
   {
-    const long long g0 = s0 * KB;
-    int lo = 0, hi = B;  // invariant: prefix[lo] * Hkv <= g0 < prefix[hi] * Hkv
+    int lo = 0, hi = B;  // invariant: prefix[lo] * Hkv <= r0 < prefix[hi] * Hkv
     while (hi - lo > 1) {
       const int step = (hi - lo + 31) / 32;
       const int at = min(lo + (lane + 1) * step, hi);
-      const unsigned m = __ballot_sync(kAll, static_cast<long long>(prefix[at]) * Hkv <= g0);
-      const int n = __popc(m);  // candidates at or before g0: the first n
+      const unsigned m = __ballot_sync(kAll, static_cast<long long>(prefix[at]) * Hkv <= r0);
+      const int n = __popc(m);  // candidates at or before r0: the first n
       const int nlo = n == 0 ? lo : min(lo + n * step, hi);
       hi = min(lo + (n + 1) * step, hi);
       lo = nlo;
     }
     b = lo;
   }
-  const int t4 = (lane % LPB) * 4;  // the lane's first key in its block
-  for (long long s = s0; s < s1; ++s) {
-    const long long g = s * KB + lane / LPB;
-    if (g >= N) break;  // no warp-wide step below
-    while (static_cast<long long>(prefix[b + 1]) * Hkv <= g) ++b;
-    const int nblk = prefix[b + 1] - prefix[b];
-    const long long off = g - static_cast<long long>(prefix[b]) * Hkv;
-    const int kvh = static_cast<int>(off / nblk), blk = static_cast<int>(off % nblk);
-    const int left = min(max(a.context_lens[b], 0), a.len_cap) - blk * BS - t4;
-    if (left <= 0) continue;
-    const int phys = a.block_tables[static_cast<long long>(b) * a.max_blocks + blk];
-    if (phys < 0 || phys >= a.num_blocks) continue;  // reported by the decode launch
-    const float* x = a.raw_scores + g * (G * BS) + t4;
-    const float2* ml = a.head_ml + static_cast<long long>(b) * a.num_heads + kvh * G;
-    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int h = 0; h < G; ++h) {
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(x + h * BS));
-      const float2 c = __ldcg(ml + h);
-      sum.x += fast_exp2(v.x - c.x) * c.y;
-      sum.y += fast_exp2(v.y - c.x) * c.y;
-      sum.z += fast_exp2(v.z - c.x) * c.y;
-      sum.w += fast_exp2(v.w - c.x) * c.y;
+  int nblk = prefix[b + 1] - prefix[b];
+  const long long off = r0 - static_cast<long long>(prefix[b]) * Hkv;
+  int kvh = static_cast<int>(off / nblk), blk0 = static_cast<int>(off % nblk);
+  const bool drop = (G * BS * 4) % 128 == 0;  // a block's scores are whole lines
+  // the lane's keys in its block: t0, t0 + 1, t0 + 8, t0 + 9
+  const int s4 = lane % LPB, t0 = BS == 16 ? 2 * s4 : 16 * (s4 & 1) + 2 * (s4 >> 1);
+  for (long long g = r0; g < r1;) {  // segment (b, kvh) from block blk0 on
+    const int n = static_cast<int>(min(static_cast<long long>(nblk - blk0), r1 - g));
+    const int L = min(max(a.context_lens[b], 0), a.len_cap);
+    const int32_t* const table = a.block_tables + static_cast<long long>(b) * a.max_blocks + blk0;
+    const float2* const ml = a.head_ml + static_cast<long long>(b) * a.num_heads + kvh * G;
+    const float* const x0 = a.raw_scores + g * (G * BS) + 4 * s4;
+    float2 c[GP];
+#pragma unroll
+    for (int h = 0; h < GP; ++h) c[h] = h < G ? __ldcg(ml + h) : make_float2(0.f, 0.f);
+#pragma unroll 1
+    for (int i = lane / LPB; i < n; i += KB) {
+      const int phys = table[i];
+      float4 v[GP];
+#pragma unroll
+      for (int h = 0; h < GP; ++h)
+        v[h] = h < G ? __ldcs(reinterpret_cast<const float4*>(
+                           x0 + static_cast<long long>(i) * (G * BS) + h * BS))
+                     : make_float4(0.f, 0.f, 0.f, 0.f);
+      float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int h = 0; h < GP; ++h) {
+        sum.x += fast_exp2(v[h].x - c[h].x) * c[h].y;
+        sum.y += fast_exp2(v[h].y - c[h].x) * c[h].y;
+        sum.z += fast_exp2(v[h].z - c[h].x) * c[h].y;
+        sum.w += fast_exp2(v[h].w - c[h].x) * c[h].y;
+      }
+      // every lane of the block has its scores: drop their lines from L2, which
+      // would otherwise write them to memory some time
+      __syncwarp(__activemask());
+      if (drop) {
+        const char* line = reinterpret_cast<const char*>(x0 - 4 * s4 + static_cast<long long>(i) * (G * BS));
+        for (int k = s4 * 128; k < G * BS * 4; k += LPB * 128)
+          asm volatile("discard.global.L2 [%0], 128;" ::"l"(line + k) : "memory");
+      }
+      if (phys < 0 || phys >= a.num_blocks) continue;  // reported by the decode launch
+      float* const dst = scores + (static_cast<long long>(phys) * Hkv + kvh) * BS + t0;
+      const int left = L - (blk0 + i) * BS - t0;  // the lane's keys below `left` exist
+      if (left >= 10) {
+        red_add_v2(dst, sum.x, sum.y);
+        red_add_v2(dst + 8, sum.z, sum.w);
+      } else {
+        if (left > 0) atomicAdd(dst, sum.x);
+        if (left > 1) atomicAdd(dst + 1, sum.y);
+        if (left > 8) atomicAdd(dst + 8, sum.z);
+        if (left > 9) atomicAdd(dst + 9, sum.w);
+      }
     }
-    float* dst = scores + (static_cast<long long>(phys) * Hkv + kvh) * BS + t4;
-    if (left >= 4) {
-      red_add_v4(dst, sum);
-    } else {
-      atomicAdd(dst, sum.x);
-      if (left > 1) atomicAdd(dst + 1, sum.y);
-      if (left > 2) atomicAdd(dst + 2, sum.z);
+    g += n;
+    blk0 = 0;
+    if (g < r1 && ++kvh == Hkv) {
+      kvh = 0;
+      do {
+        ++b;
+      } while (prefix[b + 1] == prefix[b]);
+      nblk = prefix[b + 1] - prefix[b];
     }
   }
+}
+
+template <int BS>
+cudaError_t launch_bs(const cudaLaunchConfig_t& cfg, const DecodeArgs& a, float* scores) {
+  if (a.group <= 1) return cudaLaunchKernelEx(&cfg, add_scores_kernel<BS, 1>, a, scores);
+  if (a.group <= 2) return cudaLaunchKernelEx(&cfg, add_scores_kernel<BS, 2>, a, scores);
+  if (a.group <= 4) return cudaLaunchKernelEx(&cfg, add_scores_kernel<BS, 4>, a, scores);
+  return cudaLaunchKernelEx(&cfg, add_scores_kernel<BS, 8>, a, scores);
 }
 
 }  // namespace
@@ -104,7 +144,7 @@ cudaError_t launch_add_scores(const DecodeArgs& a, float* scores, int num_sms,
   const long long nblk = (static_cast<long long>(a.len_cap) + a.block_size - 1) / a.block_size;
   const long long steps = (nblk * a.batch * a.num_kv_heads * a.block_size + 127) / 128;
   const long long ctas = std::max(1LL, std::min<long long>((steps + kAsWarps - 1) / kAsWarps,
-                                                           static_cast<long long>(num_sms) * 8));
+                                                           static_cast<long long>(num_sms) * kAsCtas));
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(static_cast<unsigned>(ctas));
   cfg.blockDim = dim3(kAsWarps * 32);
@@ -114,8 +154,7 @@ cudaError_t launch_add_scores(const DecodeArgs& a, float* scores, int num_sms,
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return a.block_size == 16 ? cudaLaunchKernelEx(&cfg, add_scores_kernel<16>, a, scores)
-                            : cudaLaunchKernelEx(&cfg, add_scores_kernel<32>, a, scores);
+  return a.block_size == 16 ? launch_bs<16>(cfg, a, scores) : launch_bs<32>(cfg, a, scores);
 }
 
 }  // namespace pa

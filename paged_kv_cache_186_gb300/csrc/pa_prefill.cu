@@ -70,10 +70,15 @@ constexpr int kBN = 128;               // keys per tile
 constexpr int kD = 128;                // head_dim
 constexpr int kSub = 128 * kBM;        // bytes of one 64-dim (128-byte-wide) half of a 128-row tile
 constexpr int kTileBytes = 2 * kSub;   // 32 KB
-constexpr int kKStages = 2;            // K ring depth
-constexpr int kVStages = 2;            // V ring depth
-constexpr int kSmem = 1024 + (2 + kKStages + kVStages) * kTileBytes;
-static_assert(kSmem <= 227 * 1024, "shared memory over the per-CTA limit");
+// Depth of the K ring and of the V ring. SPLIT has one query tile in shared
+// memory instead of two, and a third stage each in its place.
+constexpr int kMaxStages = 3;
+__host__ __device__ constexpr int ring_stages(bool split) { return split ? 3 : 2; }
+constexpr int smem_bytes(bool split) {
+  return 1024 + ((split ? 1 : 2) + 2 * ring_stages(split)) * kTileBytes;
+}
+static_assert(smem_bytes(false) <= 226 * 1024 && smem_bytes(true) <= 226 * 1024,
+              "shared memory over the per-CTA limit");
 static_assert(32 % (kBN / 16) == 0 && 32 % (kBN / 32) == 0, "tiles must not straddle a block-id window");
 constexpr int kThreads = 384;          // 2 x 4 softmax warps, K producer, MMA, V producer, idle
 // Register split (setmaxnreg): launched at 65536/384 -> 168 per thread; the
@@ -91,14 +96,14 @@ constexpr float kRescaleThreshold = 8.0f;  // log2 units
 enum {
   BAR_Q = 0,
   BAR_KF = 1,                  // + stage: K tile landed
-  BAR_KE = BAR_KF + kKStages,  // + stage: K stage free (the S MMAs reading it done)
-  BAR_VF = BAR_KE + kKStages,  // + stage: V tile landed
-  BAR_VE = BAR_VF + kVStages,  // + stage: V stage free (the P.V MMAs reading it done)
-  BAR_S = BAR_VE + kVStages,   // + tile: S_i ready
+  BAR_KE = BAR_KF + kMaxStages,  // + stage: K stage free (the S MMAs reading it done)
+  BAR_VF = BAR_KE + kMaxStages,  // + stage: V tile landed
+  BAR_VE = BAR_VF + kMaxStages,  // + stage: V stage free (the P.V MMAs reading it done)
+  BAR_S = BAR_VE + kMaxStages,   // + tile: S_i ready
   BAR_P = BAR_S + 2,           // + tile: P_i written (4 warps)
   BAR_O = BAR_P + 2,           // + tile: P_i.V done
-  BAR_DRAIN = BAR_O + 2,
-  NBAR = BAR_DRAIN + 1
+  BAR_DRAIN = BAR_O + 2,       // + MMA warp
+  NBAR = BAR_DRAIN + 2
 };
 
 // Bounded wait that also gives up when another role of the CTA has aborted.
@@ -152,16 +157,18 @@ __device__ __forceinline__ PairKeys pair_keys(int first_pos, int window, int sin
   return k;
 }
 
-template <int BS, bool WIN>
+template <int BS, bool WIN, bool SPLIT>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap qmap,
                    const __grid_constant__ CUtensorMap kmap,
                    const __grid_constant__ CUtensorMap vmap, const PrefillArgs a) {
   constexpr int kBlocksPerTile = kBN / BS;
+  constexpr int kStages = ring_stages(SPLIT), kQTiles = SPLIT ? 1 : 2;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bars[NBAR];
   __shared__ uint32_t tmem_slot;
   __shared__ volatile int abort_flag;
+  __shared__ float2 half_ml[SPLIT ? kBM : 1];  // SPLIT: (max, sum) of the second half's rows
 
   // launched as a programmatic dependent of the store that wrote the new
   // tokens' K/V: wait for it before reading anything
@@ -182,7 +189,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (pair < 0) return;
   const int t00 = 2 * pair * TPT;  // first token of query tile 0
   if (t00 >= q_len) return;
-  const bool has1 = t00 + TPT < q_len;
+  const bool has1 = !SPLIT && t00 + TPT < q_len;
   // K/V tiles each query tile needs (keys its last row can see)
   int Tq[2];
   PairKeys pk{};
@@ -191,6 +198,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto tile_base = [&](int n) { return WIN ? pk.base(n) : n * kBN; };
   Tq[0] = tiles_to(min(cached + min(t00 + TPT, q_len), kv_len));
   Tq[1] = has1 ? tiles_to(min(cached + min(t00 + 2 * TPT, q_len), kv_len)) : 0;
+  // SPLIT: the CTA's only query tile is worked on by both halves of the CTA
+  // (softmax warpgroup, S and O, and an MMA warp each), which take the walked
+  // tiles in turn: half i the tiles n = i, i + 2, ...; tile n is the half's
+  // (n / nstep)-th. Their results merge at the end.
+  constexpr int nstep = SPLIT ? 2 : 1;
+  if (SPLIT) Tq[1] = Tq[0];
   const int T = max(Tq[0], Tq[1]);
   // P.V takes P as two bf16 terms on key tile 0 of a query tile whose first
   // row sees fewer than kBN keys (every key of such a row lies in tile 0), and
@@ -217,8 +230,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t base = (raw + 1023u) & ~1023u;
   uint8_t* const base_ptr = smem_raw + (base - raw);
   auto q_s = [&](int i) { return base + i * kTileBytes; };
-  auto k_s = [&](int s) { return base + (2 + s) * kTileBytes; };
-  auto v_s = [&](int s) { return base + (2 + kKStages + s) * kTileBytes; };
+  auto k_s = [&](int s) { return base + (kQTiles + s) * kTileBytes; };
+  auto v_s = [&](int s) { return base + (kQTiles + kStages + s) * kTileBytes; };
   const uint32_t bar0 = smem_addr(&bars[0]);
   auto bar = [&](int i) { return bar0 + 8u * i; };
 
@@ -248,7 +261,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool is_k = warp == 8;
     const CUtensorMap* map = is_k ? &kmap : &vmap;
     const int full0 = is_k ? BAR_KF : BAR_VF, empty0 = is_k ? BAR_KE : BAR_VE;
-    const int NS = is_k ? kKStages : kVStages;
+    constexpr int NS = kStages;
     int issued = 0;
     if (is_k && lane == 0) {
       mbar_arrive_expect_tx(bar(BAR_Q), (has1 ? 2 : 1) * kTileBytes);
@@ -309,18 +322,20 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int n = max(0, issued - NS); n < issued; ++n)
         (void)mbar_wait(bar(full0 + n % NS), (n / NS) & 1);
     }
-  } else if (warp == 9) {
+  } else if (warp == 9 || (SPLIT && warp == 11)) {
     // ------------------------------------------------------------ MMA issue
     constexpr uint32_t kIdescQK = tc::idesc_bf16_f32(kBM, kBN, false, false);
     constexpr uint32_t kIdescPV = tc::idesc_bf16_f32(kBM, kD, false, true);
+    // this warp's S / O pairs [i0, i1): both, or its half's
+    const int i0 = SPLIT && warp == 11 ? 1 : 0, i1 = SPLIT ? i0 + 1 : 2;
     auto issue_s = [&](int i, int n) {  // S_i = Q_i K(n)^T
-      const int ks = n % kKStages;
+      const int ks = n % kStages;
       tc::fence_after_sync();
       if (lane == 0) {
 #pragma unroll
         for (int kk = 0; kk < kD / 16; ++kk) {
           const uint32_t off = (kk >> 2) * kSub + (kk & 3) * 32;
-          tc::mma_ss(tS(i), tc::smem_desc_sw128(q_s(i) + off, 16, 1024),
+          tc::mma_ss(tS(i), tc::smem_desc_sw128(q_s(SPLIT ? 0 : i) + off, 16, 1024),
                      tc::smem_desc_sw128(k_s(ks) + off, 16, 1024), kIdescQK, kk > 0 ? 1u : 0u);
         }
         tc::commit(bar(BAR_S + i));
@@ -328,8 +343,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     };
     auto issue_pv = [&](int i, int n) {  // O_i += P_i V(n)
-      const int vs = n % kVStages;
-      const int terms = two_term(i, n) ? 2 : 1;
+      const int vs = n % kStages;
+      const int terms = two_term(SPLIT ? 0 : i, n) ? 2 : 1;
       tc::fence_after_sync();
       if (lane == 0) {
 #pragma unroll 1
@@ -338,23 +353,24 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int kk = 0; kk < kBN / 16; ++kk)
             tc::mma_ts(tO(i), tS(i) + 64 * t + kk * 8,
                        tc::smem_desc_sw128(v_s(vs) + kk * 16 * 128, kSub, 1024), kIdescPV,
-                       (n > 0 || kk > 0 || t > 0) ? 1u : 0u);
+                       (n >= nstep || kk > 0 || t > 0) ? 1u : 0u);
         }
         tc::commit(bar(BAR_O + i));
       }
       __syncwarp();
     };
-    bool ok = warp_wait(bar(BAR_Q), 0, &abort_flag, a.err) &&
-              warp_wait(bar(BAR_KF + 0), 0, &abort_flag, a.err);
+    const int n0 = SPLIT ? i0 : 0;
+    bool ok = (!SPLIT || n0 < T) && warp_wait(bar(BAR_Q), 0, &abort_flag, a.err) &&
+              warp_wait(bar(BAR_KF + n0), 0, &abort_flag, a.err);
     if (ok) {
-      for (int i = 0; i < 2; ++i)
-        if (Tq[i] > 0) issue_s(i, 0);
-      if (lane == 0) tc::commit(bar(BAR_KE + 0));
+      for (int i = i0; i < i1; ++i)
+        if (Tq[i] > n0) issue_s(i, n0);
+      if (lane == 0) tc::commit(bar(BAR_KE + n0));
       __syncwarp();
     }
-    for (int n = 0; ok && n < T; ++n) {
-      const int s = n % kVStages;
-      if (!warp_wait(bar(BAR_VF + s), (n / kVStages) & 1, &abort_flag, a.err)) break;
+    for (int n = n0; ok && n < T; n += nstep) {
+      const int s = n % kStages;
+      if (!warp_wait(bar(BAR_VF + s), (n / kStages) & 1, &abort_flag, a.err)) break;
       const int r0 = kv_len - tile_base(n);
       if constexpr (WIN) {
         // V rows of keys [se, lo), which no row sees, in the blocks around
@@ -389,23 +405,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_proxy_async_smem();
         __syncwarp();
       }
-      const bool more = n + 1 < T;
-      const int s1 = (n + 1) % kKStages;
-      if (more && !warp_wait(bar(BAR_KF + s1), ((n + 1) / kKStages) & 1, &abort_flag, a.err))
-        break;
-      for (int i = 0; i < 2; ++i) {
+      const int n1 = n + nstep;
+      const bool more = n1 < T;
+      const int s1 = n1 % kStages;
+      if (more && !warp_wait(bar(BAR_KF + s1), (n1 / kStages) & 1, &abort_flag, a.err)) break;
+      for (int i = i0; i < i1; ++i) {
         if (n >= Tq[i]) continue;
-        if (!warp_wait(bar(BAR_P + i), n & 1, &abort_flag, a.err)) {
+        if (!warp_wait(bar(BAR_P + i), (n / nstep) & 1, &abort_flag, a.err)) {
           ok = false;
           break;
         }
         issue_pv(i, n);
-        if (n + 1 < Tq[i]) {
-          if (!warp_wait(bar(BAR_O + i), n & 1, &abort_flag, a.err)) {
+        if (n1 < Tq[i]) {
+          if (!warp_wait(bar(BAR_O + i), (n / nstep) & 1, &abort_flag, a.err)) {
             ok = false;
             break;
           }
-          issue_s(i, n + 1);
+          issue_s(i, n1);
         }
       }
       if (!ok) break;
@@ -416,9 +432,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     }
     if (abort_flag) {  // make sure no MMA is still running before TMEM is freed
-      if (lane == 0) tc::commit(bar(BAR_DRAIN));
+      if (lane == 0) tc::commit(bar(BAR_DRAIN + i0));
       __syncwarp();
-      (void)mbar_wait(bar(BAR_DRAIN), 0);
+      (void)mbar_wait(bar(BAR_DRAIN + i0), 0);
     }
    }
   } else {
@@ -428,15 +444,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int Tn = Tq[ti];
     const int wq = warp & 3;        // TMEM lane quarter this warp may access
     const int r = 32 * wq + lane;
-    const int tok = t00 + ti * TPT + r / G, g = r % G;
+    const int qi = SPLIT ? 0 : ti;
+    const int tok = t00 + qi * TPT + r / G, g = r % G;
     const bool row_valid = tok < q_len;
     const int last_key = min(min(tok, q_len - 1) + cached, kv_len - 1);  // last visible key
     const uint32_t trow = static_cast<uint32_t>(32 * wq) << 16;
     const float sl2 = a.scale_log2;
     float m_used = -INFINITY, l = 0.f;
     bool ok = true;
-    for (int n = 0; n < Tn; ++n) {
-      if (!warp_wait(bar(BAR_S + ti), n & 1, &abort_flag, a.err)) {
+    const int n0 = SPLIT ? ti : 0;
+    for (int n = n0; n < Tn; n += nstep) {
+      if (!warp_wait(bar(BAR_S + ti), (n / nstep) & 1, &abort_flag, a.err)) {
         ok = false;
         break;
       }
@@ -465,10 +483,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         mx = fmaxf(mx, fmaxf(fmaxf(__uint_as_float(u[0][j]), __uint_as_float(u[1][j])),
                              fmaxf(__uint_as_float(u[2][j]), __uint_as_float(u[3][j]))));
       const float m_tile = mx * sl2;
-      if (n == 0) {
+      if (n == n0) {
         m_used = m_tile;
       } else if (__any_sync(0xffffffffu, m_tile > m_used + kRescaleThreshold)) {
-        if (!warp_wait(bar(BAR_O + ti), (n - 1) & 1, &abort_flag, a.err)) {
+        if (!warp_wait(bar(BAR_O + ti), (n / nstep - 1) & 1, &abort_flag, a.err)) {
           ok = false;
           break;
         }
@@ -511,7 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc::tmem_st32(tS(ti) + trow + 32 * h, w);
       }
-      if (two_term(ti, n)) {
+      if (two_term(qi, n)) {
         // second term of P, p - bf16(p) as bf16, into columns 64..127: P is
         // computed again from the scores (the same operations, the same values)
 #pragma unroll
@@ -541,7 +559,26 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(BAR_P + ti));
     }
-    if (ok && Tn > 0 && warp_wait(bar(BAR_O + ti), (Tn - 1) & 1, &abort_flag, a.err)) {
+    float f0 = 1.f, f1 = 0.f;  // factors of this half's rows and of the other's
+    bool both = false;
+    if constexpr (SPLIT) {
+      // rows' (max, sum) of the second half to the first, which writes the rows:
+      // it can read the second half's O, in the same TMEM lanes, itself
+      if (ti == 1) half_ml[r] = make_float2(m_used, l);
+      asm volatile("bar.sync 1, 256;" ::: "memory");
+      if (ti == 0 && Tn > 1) {
+        both = ok && warp_wait(bar(BAR_O + 1), (Tn / 2 - 1) & 1, &abort_flag, a.err);
+        ok = both;
+        const float2 o = half_ml[r];
+        const float m = fmaxf(m_used, o.x);
+        f0 = m_used == -INFINITY ? 0.f : fast_exp2(m_used - m);
+        f1 = o.x == -INFINITY ? 0.f : fast_exp2(o.x - m);
+        l = l * f0 + o.y * f1;
+      }
+    }
+    // (the half's last tile: Tn - 1 or, for the first of two, the last even one)
+    if (ok && !(SPLIT && ti == 1) && Tn > 0 &&
+        warp_wait(bar(BAR_O + ti), ((Tn - 1) / nstep) & 1, &abort_flag, a.err)) {
       tc::fence_after_sync();
       const float inv = l > 0.f ? 1.f / l : 0.f;
       __nv_bfloat16* orow = out + (static_cast<long long>(q0 + tok) * H + kvh * G + g) * kD;
@@ -550,6 +587,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t w[32];
         tc::tmem_ld32(tO(ti) + trow + 32 * c, w);
         tc::tmem_wait_ld();
+        if (SPLIT && both) {
+          uint32_t v[32];
+          tc::tmem_ld32(tO(1) + trow + 32 * c, v);
+          tc::tmem_wait_ld();
+#pragma unroll
+          for (int j = 0; j < 32; ++j)
+            w[j] = __float_as_uint(__uint_as_float(w[j]) * f0 + __uint_as_float(v[j]) * f1);
+        }
         if (row_valid) {
           uint32_t pk[16];
 #pragma unroll
@@ -572,7 +617,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int BS, bool WIN>
+template <int BS, bool WIN, bool SPLIT>
 cudaError_t launch_bs(const PrefillArgs& a, const CUtensorMap& qmap, const CUtensorMap& kmap,
                       const CUtensorMap& vmap, cudaStream_t stream) {
   static bool attr_set[64] = {};
@@ -581,7 +626,8 @@ cudaError_t launch_bs(const PrefillArgs& a, const CUtensorMap& qmap, const CUten
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!attr_set[dev]) {
-    e = cudaFuncSetAttribute(prefill_kernel<BS, WIN>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+    e = cudaFuncSetAttribute(prefill_kernel<BS, WIN, SPLIT>,
+                             cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(SPLIT));
     if (e != cudaSuccess) return e;
     attr_set[dev] = true;
   }
@@ -589,14 +635,14 @@ cudaError_t launch_bs(const PrefillArgs& a, const CUtensorMap& qmap, const CUten
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(a.num_kv_heads, a.batch, (a.num_qtiles + 1) / 2);
   cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmem;
+  cfg.dynamicSmemBytes = smem_bytes(SPLIT);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, prefill_kernel<BS, WIN>, qmap, kmap, vmap, a);
+  return cudaLaunchKernelEx(&cfg, prefill_kernel<BS, WIN, SPLIT>, qmap, kmap, vmap, a);
 }
 
 }  // namespace
@@ -605,11 +651,18 @@ cudaError_t launch_prefill(const PrefillArgs& a, const CUtensorMap& qmap, const 
                            const CUtensorMap& vmap, cudaStream_t stream) {
   if (a.head_dim != kD || kBM % a.group != 0) return cudaErrorInvalidValue;
   if (a.block_size != 16 && a.block_size != 32) return cudaErrorInvalidValue;
-  if (a.window > 0)
-    return a.block_size == 16 ? launch_bs<16, true>(a, qmap, kmap, vmap, stream)
-                              : launch_bs<32, true>(a, qmap, kmap, vmap, stream);
-  if (a.block_size == 16) return launch_bs<16, false>(a, qmap, kmap, vmap, stream);
-  if (a.block_size == 32) return launch_bs<32, false>(a, qmap, kmap, vmap, stream);
+  if (a.window > 0) {
+    // every sequence within one query tile (num_qtiles is of the longest): both
+    // halves of a CTA share it. Measured on one GB300, 32 sequences of 1-16 new
+    // tokens, window 1024, 32/8 heads: 48.2 -> 40.9 us
+    if (a.num_qtiles <= 1)
+      return a.block_size == 16 ? launch_bs<16, true, true>(a, qmap, kmap, vmap, stream)
+                                : launch_bs<32, true, true>(a, qmap, kmap, vmap, stream);
+    return a.block_size == 16 ? launch_bs<16, true, false>(a, qmap, kmap, vmap, stream)
+                              : launch_bs<32, true, false>(a, qmap, kmap, vmap, stream);
+  }
+  if (a.block_size == 16) return launch_bs<16, false, false>(a, qmap, kmap, vmap, stream);
+  if (a.block_size == 32) return launch_bs<32, false, false>(a, qmap, kmap, vmap, stream);
   return cudaErrorInvalidValue;
 }
 

@@ -44,12 +44,14 @@
 //     code's presence costs ~3 % there (measured 124.2 -> 128.4 us on the
 //     8-sequence benchmark, whose prefixes are all >= 250 tokens).
 //   * A sliding window with sinks (WIN): row p sees keys j <= p with j < sinks
-//     or j > p - window. The CTA walks the 128-key tiles that hold a key some
-//     row of its two query tiles sees: the sink keys' tiles, then tiles from
-//     the first window key's block on (PairKeys). Blocks of a walked tile
-//     without such a key are fetched out of bounds like those past the end
-//     (their table entries are not read), V rows that no row sees are zeroed,
-//     and a row's own bounds are masked on the tiles that cross them. A row
+//     or j > p - window. The CTA walks the blocks that hold a key some row of
+//     its two query tiles sees, packed into 128-key tiles: the sink keys'
+//     blocks, then those from the first window key's on (PairKeys; a tile of
+//     their own for a few sinks would be a tenth of the steps of a window of
+//     1000). V rows that no row sees are zeroed, and a row's own bounds are
+//     masked on the tiles that cross them. Where the sinks reach to the window
+//     all blocks are walked, and those without such a key are fetched out of
+//     bounds like those past the end (their table entries are not read). A row
 //     may see nothing of its first tiles: its maximum then stays -inf and its
 //     weights zero until it sees a key.
 //   * TMEM: 512 columns (S0, S1, O0, O1, 128 each); shared memory: Q0, Q1,
@@ -131,29 +133,28 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
 }
 
 // The keys a pair of query tiles walks: those below `se` (sinks) and from `lo`
-// on (the first row's window), up to n_keys. Walked tile `it` starts at key
-// base(it): `ns` tiles from key 0, the others from key wb (block-aligned) on.
-// Sinks whose tiles would reach into the window's are walked with it, from
-// key 0.
+// on (the first row's window). Walked position x is key x in the first nsb
+// blocks (the sinks') and key x + shift behind them (from key wb, a block's
+// first, on). Sinks that reach into the window's blocks, and windows past the
+// last key (more queries than keys), are walked from key 0 without a gap.
 struct PairKeys {
-  int se, lo, ns, wb;
-  __device__ __forceinline__ int base(int it) const {
-    return it < ns ? it * kBN : wb + (it - ns) * kBN;
-  }
+  int se, lo, nsb, wb, shift;
   // walked tiles that hold the keys below `end`
+  template <int BS>
   __device__ __forceinline__ int tiles(int end) const {
-    return ns + (max(end - wb, 0) + kBN - 1) / kBN;
+    return (nsb * BS + max(end - wb, 0) + kBN - 1) / kBN;
   }
 };
 
 template <int BS>
-__device__ __forceinline__ PairKeys pair_keys(int first_pos, int window, int sinks) {
+__device__ __forceinline__ PairKeys pair_keys(int first_pos, int kv_len, int window, int sinks) {
   PairKeys k;
   k.lo = max(0, first_pos - window + 1);
   k.se = min(sinks, k.lo);
-  k.ns = (k.se + kBN - 1) / kBN;
+  k.nsb = (k.se + BS - 1) / BS;
   k.wb = k.lo / BS * BS;
-  if (k.ns * kBN >= k.wb) k.ns = k.wb = 0;
+  if (k.nsb * BS >= k.wb || k.lo >= kv_len) k.nsb = k.wb = 0;
+  k.shift = k.wb - k.nsb * BS;
   return k;
 }
 
@@ -193,9 +194,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   // K/V tiles each query tile needs (keys its last row can see)
   int Tq[2];
   PairKeys pk{};
-  if constexpr (WIN) pk = pair_keys<BS>(cached + t00, a.window, a.sinks);
-  auto tiles_to = [&](int end) { return WIN ? pk.tiles(end) : (end + kBN - 1) / kBN; };
-  auto tile_base = [&](int n) { return WIN ? pk.base(n) : n * kBN; };
+  if constexpr (WIN) pk = pair_keys<BS>(cached + t00, kv_len, a.window, a.sinks);
+  auto tiles_to = [&](int end) {
+    if constexpr (WIN) return pk.template tiles<BS>(end);
+    else return (end + kBN - 1) / kBN;
+  };
+  // first key of walked tile n (behind the sinks' blocks, if it holds some)
+  auto tile_base = [&](int n) { return n * kBN + (WIN ? pk.shift : 0); };
   Tq[0] = tiles_to(min(cached + min(t00 + TPT, q_len), kv_len));
   Tq[1] = has1 ? tiles_to(min(cached + min(t00 + 2 * TPT, q_len), kv_len)) : 0;
   // SPLIT: the CTA's only query tile is worked on by both halves of the CTA
@@ -280,7 +285,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int lb = wb + lane;
       bool need = true;
       if constexpr (WIN) {  // wb + lane counts walked blocks
-        lb = tile_base((wb + lane) / kBlocksPerTile) / BS + (wb + lane) % kBlocksPerTile;
+        if (lb >= pk.nsb) lb += pk.shift / BS;
         need = lb * BS < pk.se || (lb + 1) * BS > pk.lo;
       }
       int rc = oob;
@@ -376,10 +381,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         // V rows of keys [se, lo), which no row sees, in the blocks around
         // the bounds (whole blocks of them were not fetched)
         uint8_t* vp = base_ptr + (v_s(s) - base);
-        const int kb = tile_base(n);
         bool wrote = false;
-        auto zero_rows = [&](int k0, int k1) {  // keys k0 .. k1-1, as far as in this tile
-          const int z0 = max(k0 - kb, 0), z1 = min(k1 - kb, kBN);
+        auto zero_rows = [&](int x0, int x1) {  // walked positions x0 .. x1-1 in this tile
+          const int z0 = max(x0 - n * kBN, 0), z1 = min(x1 - n * kBN, kBN);
           for (int e = lane; e < (z1 - z0) * 16; e += 32) {
             const int row = z0 + (e >> 4), c = e & 15;
             *reinterpret_cast<uint4*>(vp + (c >> 3) * kSub + row * 128 + (c & 7) * 16) =
@@ -387,8 +391,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           wrote |= z1 > z0;
         };
-        zero_rows(pk.se, min(pk.lo, (pk.se + BS - 1) / BS * BS));
-        zero_rows(max(pk.se, pk.lo / BS * BS), pk.lo);
+        zero_rows(pk.se, min(pk.lo - pk.shift, (pk.se + BS - 1) / BS * BS));
+        zero_rows(max(pk.se, pk.lo / BS * BS - pk.shift), pk.lo - pk.shift);
         if (wrote) {
           fence_proxy_async_smem();
           __syncwarp();
@@ -462,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int lim = last_key - tile_base(n);  // keys 0..lim of this tile are visible
       // ... and with a window, of those, the ones past wl or before sk
       const int wl = WIN ? tok + cached - a.window - tile_base(n) : -1;
-      const int sk = WIN ? a.sinks - tile_base(n) : 0;
+      const int sk = WIN ? a.sinks - n * kBN : 0;
       // the whole score row in registers: one TMEM round trip
       uint32_t u[4][32];
 #pragma unroll

@@ -262,11 +262,13 @@ __device__ __forceinline__ void attend_block(uint32_t kt, uint32_t vt, const uin
       if (!valid(tok0 + (j >> 1) * 8 + 2 * q4 + (j & 1))) x[j] = -INFINITY;
   }
   if constexpr (SC) {
-    if (r < group) {  // the lane's scores of head r side by side: 16-byte stores
+    // the lane's scores of head r side by side: 16-byte stores, kept in L2 for the
+    // launch that reads them (8 long contexts 381 -> 373 us, E4M3 batch 256 245 ->
+    // 242 us against plain stores, same box)
+    if (r < group) {
 #pragma unroll
       for (int j = 0; j < 2 * NT; j += 4)
-        *reinterpret_cast<float4*>(raw + r * BS + q4 * (2 * NT) + j) =
-            make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]);
+        st_keep(raw + r * BS + q4 * (2 * NT) + j, x[j], x[j + 1], x[j + 2], x[j + 3]);
     }
   }
   float mx = x[0];

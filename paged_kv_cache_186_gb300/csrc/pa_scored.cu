@@ -67,7 +67,8 @@ __global__ void __launch_bounds__(kAsWarps * 32, kAsCtas) add_scores_kernel(cons
   int nblk = prefix[b + 1] - prefix[b];
   const long long off = r0 - static_cast<long long>(prefix[b]) * Hkv;
   int kvh = static_cast<int>(off / nblk), blk0 = static_cast<int>(off % nblk);
-  const bool drop = (G * BS * 4) % 128 == 0;  // a block's scores are whole lines
+  // a block's scores are whole lines (the workspace is only sure to be 16-byte aligned)
+  const bool drop = ((reinterpret_cast<uintptr_t>(a.raw_scores) | (G * BS * 4)) & 127) == 0;
   // the lane's keys in its block: t0, t0 + 1, t0 + 8, t0 + 9
   const int s4 = lane % LPB, t0 = BS == 16 ? 2 * s4 : 16 * (s4 & 1) + 2 * (s4 >> 1);
   for (long long g = r0; g < r1;) {  // segment (b, kvh) from block blk0 on
@@ -96,25 +97,28 @@ __global__ void __launch_bounds__(kAsWarps * 32, kAsCtas) add_scores_kernel(cons
         sum.z += fast_exp2(v[h].z - c[h].x) * c[h].y;
         sum.w += fast_exp2(v[h].w - c[h].x) * c[h].y;
       }
-      // every lane of the block has its scores: drop their lines from L2, which
-      // would otherwise write them to memory some time
-      __syncwarp(__activemask());
-      if (drop) {
-        const char* line = reinterpret_cast<const char*>(x0 - 4 * s4 + static_cast<long long>(i) * (G * BS));
-        for (int k = s4 * 128; k < G * BS * 4; k += LPB * 128)
-          asm volatile("discard.global.L2 [%0], 128;" ::"l"(line + k) : "memory");
-      }
-      if (phys < 0 || phys >= a.num_blocks) continue;  // reported by the decode launch
-      float* const dst = scores + (static_cast<long long>(phys) * Hkv + kvh) * BS + t0;
       const int left = L - (blk0 + i) * BS - t0;  // the lane's keys below `left` exist
-      if (left >= 10) {
-        red_add_v2(dst, sum.x, sum.y);
-        red_add_v2(dst + 8, sum.z, sum.w);
-      } else {
-        if (left > 0) atomicAdd(dst, sum.x);
-        if (left > 1) atomicAdd(dst + 1, sum.y);
-        if (left > 8) atomicAdd(dst + 8, sum.z);
-        if (left > 9) atomicAdd(dst + 9, sum.w);
+      if (phys >= 0 && phys < a.num_blocks) {  // (others: reported by the decode launch)
+        float* const dst = scores + (static_cast<long long>(phys) * Hkv + kvh) * BS + t0;
+        if (left >= 10) {
+          red_add_v2(dst, sum.x, sum.y);
+          red_add_v2(dst + 8, sum.z, sum.w);
+        } else {
+          if (left > 0) atomicAdd(dst, sum.x);
+          if (left > 1) atomicAdd(dst + 1, sum.y);
+          if (left > 8) atomicAdd(dst + 8, sum.z);
+          if (left > 9) atomicAdd(dst + 9, sum.w);
+        }
+      }
+      // the block's lanes have all used their scores: drop the lines from L2,
+      // which would otherwise write them to memory some time; a line that is
+      // shared with the next block only loses the priority it was stored with
+      __syncwarp(((1u << LPB) - 1u) << (lane / LPB * LPB));
+      const uintptr_t first = reinterpret_cast<uintptr_t>(a.raw_scores + (g + i) * (G * BS));
+      for (uintptr_t line = (first & ~static_cast<uintptr_t>(127)) + s4 * 128;
+           line < first + G * BS * 4; line += LPB * 128) {
+        if (drop) asm volatile("discard.global.L2 [%0], 128;" ::"l"(line) : "memory");
+        else asm volatile("applypriority.global.L2::evict_normal [%0], 128;" ::"l"(line) : "memory");
       }
     }
     g += n;

@@ -174,6 +174,23 @@ def test_graph_replays_accumulate_and_two_graphs_share_a_workspace():
     check(g, before, scores, outs[0], lens, reps=6)
 
 
+@pytest.mark.parametrize("H, bs", [(8, 16), (6, 16), (2, 16), (2, 32), (16, 32)])
+def test_any_workspace_alignment_and_what_lies_around_it(H, bs):
+    lens = [300, 1, 77]
+    g, scores = inputs(3, H, 2, 128, bs, lens, seed=240 + H)
+    need = pa.decode_scored_workspace_size(g.k_cache, 3, H, g.block_tables.shape[1])
+    want = scores.clone()
+    step(g, want)
+    for shift in (0, 16, 64, 112):
+        big = torch.arange(need + 512, device="cuda").to(torch.uint8)
+        got = scores.clone()
+        step(g, got, workspace=big[128 + shift:128 + shift + need])
+        assert torch.equal(got, want)
+        ref = torch.arange(need + 512, device="cuda").to(torch.uint8)
+        assert torch.equal(big[:128 + shift], ref[:128 + shift])
+        assert torch.equal(big[128 + shift + need:], ref[128 + shift + need:])
+
+
 def test_other_stream_and_repeatability():
     lens = [900, 31, 5, 2048]
     g, scores = inputs(4, 32, 8, 128, 16, lens, seed=236)

@@ -158,3 +158,18 @@ def test_strided_q_and_graph_replay():
         graph.replay()
         torch.cuda.synchronize()
         assert_attention_close(res, want64(g, 48, 4), f"replay {k}")
+
+
+def test_short_sequences_repeat_bit_for_bit():
+    # one query tile a sequence, the walked tiles shared by the CTA's halves: back-to-back
+    # launches over many key tiles, and ring stages used by both halves in turn
+    g = case_inputs(8, 2, 16, [3000, 700, 5, 1234, 0], [1, 32, 7, 16, 9], seed=126)
+    first = run(g, 2000, 4, max_q_len=32)
+    assert_attention_close(first, want64(g, 2000, 4), "short sequences")
+    out = torch.empty_like(first)
+    for _ in range(20):
+        for _ in range(50):
+            pa.prefill_window(g.q, g.k_cache, g.v_cache, g.block_tables, g.cu_seqlens_q,
+                              g.cu_seqlens_k, g.scale, 2000, 4, max_q_len=32, out=out)
+        assert torch.equal(out, first)
+    assert pa.get_device_error() == 0

@@ -256,7 +256,8 @@ pa_status pa_decode_window(const void* q, const pa_kv_cache* cache, const int32_
  *             of sequences that share blocks sum over the sequences (in an order
  *             that may change from call to call). Slots at or past context_len
  *             are left as they were. pa_norm_rope_store can set a new slot's
- *             score to zero.
+ *             score to zero. After a launch that reported
+ *             PA_DEVERR_WAIT_TIMEOUT they are as invalid as out.
  *   workspace at least pa_decode_scored_workspace_size() bytes, contract as for
  *             pa_decode. It holds the scores of every key: 4 bytes per query
  *             head and key of the bound batch * max_context_len.
@@ -292,7 +293,8 @@ pa_status pa_decode_scored(const void* q, const pa_kv_cache* cache, const int32_
  * Keys carry their rotation, and attention does not depend on the order of the
  * keys, so decode calls over new_lens attend to exactly the kept keys; a later
  * token's position (for the rotation) is the caller's to keep counting. The
- * blocks of a cut sequence must not be shared with another sequence. A physical
+ * blocks of a cut sequence must be distinct and not shared with another
+ * sequence. Length bounds above 2^30 return PA_ERR_UNSUPPORTED. A physical
  * block id out of range sets PA_DEVERR_BLOCK_RANGE; scores there count as 0 and
  * rows there are not moved.
  */

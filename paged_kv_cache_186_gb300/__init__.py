@@ -392,7 +392,8 @@ def norm_rope_store(q, k, v, positions, slot_mapping, k_cache, v_cache, *, q_wei
     qp, qs, qc = _token_rows(q, "q", (T, H, D))
     kp, ks, kc = _token_rows(k, "k", (T, Hkv, D))
     vp, vs, vc = _token_rows(v, "v", (T, Hkv, D))
-    _want(slot_mapping, "slot_mapping", torch.int64, (T,))
+    _want(slot_mapping, "slot_mapping", torch.int64, (T,), contiguous=False)
+    slot_mapping = slot_mapping.contiguous()
     rows = rot = 0
     if cos_sin is not None:
         if cos_sin.dim() != 2:
@@ -402,7 +403,8 @@ def norm_rope_store(q, k, v, positions, slot_mapping, k_cache, v_cache, *, q_wei
         if positions is None:
             raise ValueError("a rotation needs positions")
     if positions is not None:
-        _want(positions, "positions", torch.int64, (T,))
+        _want(positions, "positions", torch.int64, (T,), contiguous=False)
+        positions = positions.contiguous()
     if q_weight is not None:
         _want(q_weight, "q_weight", torch.bfloat16, (D,))
     if k_weight is not None:
@@ -433,12 +435,14 @@ def prefill_window(q, k_cache, v_cache, block_tables, cu_seqlens_q, cu_seqlens_k
     T, H, D = q.shape
     _want(q, "q", torch.bfloat16, (T, H, k_cache.shape[3]), contiguous=False)
     n = cu_seqlens_q.numel()
-    _want(cu_seqlens_q, "cu_seqlens_q", torch.int32, (n,))
-    _want(cu_seqlens_k, "cu_seqlens_k", torch.int32, (n,))
+    _want(cu_seqlens_q, "cu_seqlens_q", torch.int32, (n,), contiguous=False)
+    _want(cu_seqlens_k, "cu_seqlens_k", torch.int32, (n,), contiguous=False)
     if n < 1 or block_tables.dim() != 2:
         raise ValueError("block_tables must be (batch, blocks), cu_seqlens (batch + 1,)")
-    _want(block_tables, "block_tables", torch.int32, (n - 1, block_tables.shape[1]))
-    qc = q.contiguous()
+    _want(block_tables, "block_tables", torch.int32, (n - 1, block_tables.shape[1]),
+          contiguous=False)
+    qc, block_tables = q.contiguous(), block_tables.contiguous()
+    cu_seqlens_q, cu_seqlens_k = cu_seqlens_q.contiguous(), cu_seqlens_k.contiguous()
     if out is None:
         out = torch.empty((T, H, D), dtype=torch.bfloat16, device=q.device)
     else:
@@ -472,10 +476,11 @@ def decode_scored(q, k_cache, v_cache, block_tables, context_lens, scores, scale
         raise ValueError("q must be (batch, num_heads, head_dim)")
     B, H, D = q.shape
     _want(q, "q", torch.bfloat16, (B, H, k_cache.shape[3]), contiguous=False)
-    _want(context_lens, "context_lens", torch.int32, (B,))
+    _want(context_lens, "context_lens", torch.int32, (B,), contiguous=False)
     if block_tables.dim() != 2:
         raise ValueError("block_tables must be (batch, blocks)")
-    _want(block_tables, "block_tables", torch.int32, (B, block_tables.shape[1]))
+    _want(block_tables, "block_tables", torch.int32, (B, block_tables.shape[1]), contiguous=False)
+    context_lens, block_tables = context_lens.contiguous(), block_tables.contiguous()
     _want(scores, "scores", torch.float32, (k_cache.shape[0], k_cache.shape[2], k_cache.shape[1]))
     qc = q.contiguous()
     if out is None:
@@ -490,6 +495,8 @@ def decode_scored(q, k_cache, v_cache, block_tables, context_lens, scores, scale
                                                          int(max_context_len)))
         if need:
             workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    elif not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _run(q.get_device(), "pa_decode_scored", lib().pa_decode_scored, qc.data_ptr(), ctypes.byref(cache),
          block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(),
@@ -506,10 +513,11 @@ def evict(k_cache, v_cache, scores, block_tables, context_lens, budget: int, *, 
     its blocks (K, V, scales and scores, in place). Returns (new_lens (B,) int32,
     kept (B, Hkv, budget) int32: the positions the rows came from)."""
     B = context_lens.numel()
-    _want(context_lens, "context_lens", torch.int32, (B,))
+    _want(context_lens, "context_lens", torch.int32, (B,), contiguous=False)
     if block_tables.dim() != 2:
         raise ValueError("block_tables must be (batch, blocks)")
-    _want(block_tables, "block_tables", torch.int32, (B, block_tables.shape[1]))
+    _want(block_tables, "block_tables", torch.int32, (B, block_tables.shape[1]), contiguous=False)
+    context_lens, block_tables = context_lens.contiguous(), block_tables.contiguous()
     Hkv = k_cache.shape[2]
     _want(scores, "scores", torch.float32, (k_cache.shape[0], Hkv, k_cache.shape[1]))
     budget = int(budget)

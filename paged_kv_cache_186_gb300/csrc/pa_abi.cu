@@ -536,7 +536,8 @@ pa_status pa_evict(const pa_kv_cache* cache, float* scores, const int32_t* block
       new_lens == nullptr)
     return PA_ERR_NULL;
   if (new_lens < context_lens + batch && context_lens < new_lens + batch) return PA_ERR_SHAPE;
-  if (batch > 65535) return PA_ERR_UNSUPPORTED;
+  const int cap = decode_len_cap(cache, max_blocks_per_seq, max_context_len);
+  if (batch > 65535 || cap > (1 << 30)) return PA_ERR_UNSUPPORTED;
   if (!aligned16(scores)) return PA_ERR_ALIGN;
   DeviceInfo* dev = nullptr;
   if ((st = device_info(&dev)) != PA_OK) return st;
@@ -556,7 +557,7 @@ pa_status pa_evict(const pa_kv_cache* cache, float* scores, const int32_t* block
   a.block_size = cache->block_size;
   a.num_blocks = cache->num_blocks;
   a.max_blocks = max_blocks_per_seq;
-  a.len_cap = decode_len_cap(cache, max_blocks_per_seq, max_context_len);
+  a.len_cap = cap;
   a.row_bytes = cache->head_dim * elem_bytes(cache);
   a.budget = budget;
   a.sinks = sinks;

@@ -93,11 +93,14 @@ __device__ __forceinline__ uint64_t l2_evict_first_policy() {
   return p;
 }
 
-// 16-byte store of data that is read back soon: its lines are the last to be evicted from L2.
+// 16-byte store of data that is read back soon: its lines are the last to be
+// evicted from L2. (The policy's instruction is not volatile: made once, outside
+// the loops.)
 __device__ __forceinline__ void st_keep(float* p, float x, float y, float z, float w) {
-  asm volatile("{\n\t.reg .b64 pol;\n\tcreatepolicy.fractional.L2::evict_last.b64 pol, 1.0;\n\t"
-               "st.global.L2::cache_hint.v4.f32 [%0], {%1, %2, %3, %4}, pol;\n\t}" ::"l"(p),
-               "f"(x), "f"(y), "f"(z), "f"(w)
+  uint64_t policy;
+  asm("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(policy));
+  asm volatile("st.global.L2::cache_hint.v4.f32 [%0], {%1, %2, %3, %4}, %5;" ::"l"(p), "f"(x),
+               "f"(y), "f"(z), "f"(w), "l"(policy)
                : "memory");
 }
 

@@ -99,3 +99,25 @@ def test_generation_over_a_bounded_cache(kv):
             cut += int((np.array(host) > budget).sum())
     assert pa.get_device_error() == 0
     assert cut >= 5 and lens.max() <= budget + every
+
+
+def test_empty_calls_change_nothing():
+    kc, vc = (torch.ones((4, 16, 2, 128), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    scores = torch.ones((4, 2, 16), device="cuda")
+    bf = lambda *s: torch.zeros(s, dtype=torch.bfloat16, device="cuda")
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")
+    i64 = lambda *s: torch.zeros(s, dtype=torch.int64, device="cuda")
+    assert pa.norm_rope_store(bf(0, 4, 128), bf(0, 2, 128), bf(0, 2, 128), i64(0), i64(0), kc, vc,
+                              cos_sin=torch.ones((3, 64), device="cuda"),
+                              scores=scores).shape == (0, 4, 128)
+    assert pa.prefill_window(bf(0, 4, 128), kc, vc, i32(2, 1), i32(3), i32(3), 0.1, 8).numel() == 0
+    assert pa.prefill_window(bf(0, 4, 128), kc, vc, i32(0, 1), i32(1), i32(1), 0.1, 8).numel() == 0
+    assert pa.decode_scored(bf(0, 4, 128), kc, vc, i32(0, 1), i32(0), scores, 0.1).numel() == 0
+    new, kept = pa.evict(kc, vc, scores, i32(0, 1), i32(0), 8)
+    assert new.numel() == 0 and kept.shape == (0, 2, 8)
+    out = pa.decode_scored(bf(2, 4, 128) + 1, kc, vc, i32(2, 1), i32(2), scores, 0.1)
+    new, kept = pa.evict(kc, vc, scores, i32(2, 1), i32(2), 8, sinks=1, recent=2)
+    torch.cuda.synchronize()
+    assert (out == 0).all() and (new == 0).all() and (kept == -1).all()
+    assert (kc == 1).all() and (vc == 1).all() and (scores == 1).all()
+    assert pa.get_device_error() == 0

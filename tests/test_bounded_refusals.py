@@ -105,7 +105,7 @@ def evict(L, cache=None, scores=P(0x10), bt=P(0x20), mb=4, cl=P(0x1000), B=2, bu
     (dict(sinks=10, recent=7), 2), (dict(sinks=0x7fffffff, recent=0x7fffffff), 2),
     (dict(B=-1), 2), (dict(mb=0), 2), (dict(B=0), 0), (dict(B=70000, new=P(0x9000000)), 4),
     (dict(new=P(0x1000)), 2), (dict(new=P(0x1004)), 2),  # new_lens over context_lens
-    (dict(scores=P(0x18)), 7),
+    (dict(scores=P(0x18)), 7), (dict(mb=(1 << 26) + 1), 4),
 ])
 def test_evict_arguments(L, kw, want):
     assert evict(L, **kw) == want

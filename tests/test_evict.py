@@ -198,6 +198,17 @@ def test_other_stream_graph_replay_and_given_outputs():
                                                      s["lens"], 64, 16))
 
 
+def test_strided_tables_and_lengths_are_taken():
+    s = make([90, 30], 2, 64, 16, seed=310)
+    want, _ = ops64.evict_rows(s["scores"].numpy(), s["bt"].numpy(), s["lens"], 20, 0, 4)
+    wide = torch.full((2, s["bt"].shape[1] + 3), -1, dtype=torch.int32, device="cuda")
+    wide[:, :s["bt"].shape[1]] = s["bt"].cuda()
+    lens = torch.tensor([[90, 1], [30, 1]], dtype=torch.int32, device="cuda")
+    _, kept = pa.evict(s["kc"].cuda(), s["vc"].cuda(), s["scores"].cuda(),
+                       wide[:, :s["bt"].shape[1]], lens[:, 0], 20, recent=4)
+    assert np.array_equal(kept.cpu().numpy(), want)
+
+
 def test_decode_after_evict_sees_the_new_lengths_and_rows():
     # evict directly before a decode that takes its new_lens, repeatedly
     h = W.make_decode(4, 8, 2, 128, 16, [100, 300, 20, 64], seed=307)

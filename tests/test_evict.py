@@ -148,6 +148,25 @@ def test_a_long_sequence():
     check(s, 3000, 4, 100)
 
 
+@pytest.mark.parametrize("lens, budget", [([9000, 16384, 5], 2000), ([33000, 8192], 500),
+                                          ([100000], 4096)])
+def test_clusters_of_every_size_and_keys_that_are_not_held(lens, budget):
+    check(make(lens, 1, 64, 16, seed=len(lens) + budget), budget, 3, 40)
+
+
+@pytest.mark.parametrize("lens", [[6000], [20000, 12001], [90000]])
+def test_more_equal_keys_than_a_warp_lists(lens):
+    s = make(lens, 1, 64, 32, seed=311)
+    s["scores"][:] = 2.5
+    check(s, 1500, 2, 30)
+    gen = torch.Generator().manual_seed(5)
+    # one bin of the first digit, then a few values far below it
+    s["scores"] = 1.0 + torch.rand(s["scores"].shape, generator=gen) * 2.0 ** -4
+    s["scores"][torch.rand(s["scores"].shape, generator=gen) < 0.1] = 1e-20
+    check(s, 1500, 2, 30)
+    check(s, min(lens) - 3, 0, 0)
+
+
 def test_length_bound_and_capacity_clamp_the_lengths():
     s = make([100, 50], 2, 64, 16, seed=304)
     check(s, 20, 2, 5, lens=[60, 50], max_context_len=60)

@@ -145,6 +145,9 @@ CASES = [
     (13, 6, 2, 128, 16, "int8", 112, False),
     (700, 32, 8, 128, 16, "bf16", 128, False),
     (701, 9, 3, 128, 16, "fp8", 128, True),
+    (600, 16, 4, 128, 32, "int8", 64, False),
+    (900, 33, 5, 64, 16, "bf16", 32, False),
+    (300, 71, 2, 128, 16, "bf16", 128, False),
 ]
 
 

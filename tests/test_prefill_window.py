@@ -160,6 +160,20 @@ def test_strided_q_and_graph_replay():
         assert_attention_close(res, want64(g, 48, 4), f"replay {k}")
 
 
+@pytest.mark.parametrize("group", [1, 2, 4, 8, 16])
+@pytest.mark.parametrize("bs", [16, 32])
+@pytest.mark.parametrize("window, sinks", [(1, 0), (60, 70), (130, 4), (700, 0), (4000, 40)])
+def test_one_query_tile_a_sequence(group, bs, window, sinks):
+    # one to a dozen key tiles, shared in turn by the halves of a CTA
+    most = 128 // group
+    q_lens = [1, most, max(1, most // 2), 1, most, 0, min(3, most)]
+    cached = [0, 0, 127, 128, 260, 33, 1500]
+    g = case_inputs(2 * group, 2, bs, cached, q_lens, seed=130 + group + bs + window)
+    want = want64(g, window, sinks)
+    poison_unseen(g, window, sinks, bs)
+    assert_attention_close(run(g, window, sinks, most), want, f"{group} {bs} {window} {sinks}")
+
+
 def test_short_sequences_repeat_bit_for_bit():
     # one query tile a sequence, the walked tiles shared by the CTA's halves: back-to-back
     # launches over many key tiles, and ring stages used by both halves in turn

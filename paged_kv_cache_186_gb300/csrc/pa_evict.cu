@@ -529,8 +529,9 @@ cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream) {
   const long long segs = static_cast<long long>(a.batch) * a.num_kv_heads;
   const long long parts = 2 * (a.row_bytes / 128) + 1;
   // CTAs per (sequence, kv head): one per 8192 keys of the length bound. 8 long
-  // contexts (bound 131072) with 8 / 4 / 2 / 1 CTAs a head: 104 / 104 / 109 /
-  // 207 us a call; one CTA holds 2176 keys best (113 us, two of them 136).
+  // contexts (bound 131072) with 8 / 4 CTAs a head: 104 / 109 us a call (with 2 /
+  // 1, on an earlier form, 140 / 207); 64 sequences of 2176 keys with 1 / 2 CTAs,
+  // on that form, 118 / 136.
   int C = 1;
   while (C < kMaxCluster && (a.len_cap + C - 1) / C > 8192) C *= 2;
   if (segs * std::max<long long>(parts, C) > 0x7fffffffLL) return cudaErrorInvalidConfiguration;

@@ -152,35 +152,54 @@ def _check(code: int, what: str):
         raise PAError(code, what)
 
 
-def _want(t: torch.Tensor, name: str, dtype: torch.dtype, shape, contiguous: bool = True):
-    """Refuse a tensor of another type, shape or layout than a call reads or writes."""
+def _state(t: torch.Tensor, name: str, dtype: torch.dtype, shape, dev: int) -> torch.Tensor:
+    """A tensor that a call writes, or reads where it lies: refuse any other type, shape, device
+    or layout."""
     if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != shape:  # a torch.Size is a tuple
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if contiguous and not t.is_contiguous():
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on the caches' device, not on {t.device}")
+    if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
+    return t
 
 
-def _checked_cache(k_cache, v_cache, k_scale, v_scale, *others) -> KVCache:
-    """make_cache of caches that agree with each other, on one device with `others`."""
-    shape = k_cache.shape
-    if v_cache.shape != shape or v_cache.dtype is not k_cache.dtype or len(shape) != 4:
+def _input(t: torch.Tensor, name: str, dtype: torch.dtype, shape, dev: int) -> torch.Tensor:
+    """A tensor that a call reads, made contiguous if it is not."""
+    if t.is_contiguous():
+        return _state(t, name, dtype, shape, dev)
+    return _state(t.contiguous(), name, dtype, shape, dev)
+
+
+_KV_CODES = {torch.bfloat16: PA_KV_BF16, torch.uint8: PA_KV_FP8_E4M3,
+             torch.float8_e4m3fn: PA_KV_FP8_E4M3, torch.int8: PA_KV_INT8}
+
+
+def _cache_of(k_cache, v_cache, k_scale, v_scale, dev: int) -> KVCache:
+    """make_cache of caches that agree with each other, all on device `dev` (-1: not a CUDA
+    device, refused)."""
+    shape, dtype = k_cache.shape, k_cache.dtype
+    code = _KV_CODES.get(dtype)
+    if code is None:
+        raise TypeError(f"unsupported cache dtype {dtype}")
+    if len(shape) != 4 or v_cache.shape != shape or v_cache.dtype is not dtype:
         raise ValueError("k_cache and v_cache must have the same 4-D shape and dtype")
-    if (k_scale is None) != (v_scale is None):
-        raise ValueError("k_scale and v_scale come together")
-    if k_scale is not None:
-        sshape = (shape[0], shape[2], shape[1])
-        _want(k_scale, "k_scale", torch.float32, sshape)
-        _want(v_scale, "v_scale", torch.float32, sshape)
-    cache = make_cache(k_cache, v_cache, k_scale, v_scale)
-    dev = k_cache.get_device()  # -1: not a CUDA tensor
+    if not (k_cache.is_contiguous() and v_cache.is_contiguous()):
+        raise ValueError("cache tensors must be contiguous")
+    if v_cache.get_device() != dev:
+        raise ValueError("k_cache and v_cache must be on the same device")
+    nb, bs, hkv, d = shape
+    ks = vs = None
+    if k_scale is not None or v_scale is not None:
+        if k_scale is None or v_scale is None:
+            raise ValueError("k_scale and v_scale come together")
+        ks = _state(k_scale, "k_scale", torch.float32, (nb, hkv, bs), dev).data_ptr()
+        vs = _state(v_scale, "v_scale", torch.float32, (nb, hkv, bs), dev).data_ptr()
     if dev < 0:
         raise ValueError("the tensors must be on a CUDA device")
-    for t in (v_cache, k_scale, v_scale) + others:
-        if t is not None and t.get_device() != dev:
-            raise ValueError(f"all tensors must be on {k_cache.device}, got one on {t.device}")
-    return cache
+    return KVCache(nb, bs, hkv, d, code, k_cache.data_ptr(), v_cache.data_ptr(), ks, vs)
 
 
 _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
@@ -355,7 +374,7 @@ def prefill_varlen(q, k_cache, v_cache, block_tables, cu_seqlens_q, cu_seqlens_k
     return out
 
 
-def _token_rows(t: torch.Tensor, name: str, shape):
+def _token_rows(t: torch.Tensor, name: str, shape, dev: int):
     """(address, element stride between tokens, tensor) of bf16 `shape` = (T, heads, head_dim)
     whose tokens' heads are contiguous: a view of a fused projection's output is taken as it
     is, any other layout is copied."""
@@ -363,13 +382,15 @@ def _token_rows(t: torch.Tensor, name: str, shape):
         raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
     if t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on the caches' device, not on {t.device}")
     T, H, D = shape
     row = H * D
     st, sh, sd = t.stride()
     if T == 1:
         st = row
     p = t.data_ptr()
-    if sd != 1 or (H > 1 and sh != D) or st < row or st % 8 != 0 or p % 16 != 0:
+    if sd != 1 or (sh != D and H > 1) or st < row or st % 8 or p % 16:
         t = t.clone(memory_format=torch.contiguous_format)
         return t.data_ptr(), row, t
     return p, st, t
@@ -385,43 +406,41 @@ def norm_rope_store(q, k, v, positions, slot_mapping, k_cache, v_cache, *, q_wei
     for an 8-bit cache. Returns q_out (T, H, D) bf16 (rows of padding tokens are not written);
     it may be q itself if q is contiguous. q, k and v may be views of one fused projection's
     output. scores: set the slots' scores (decode_scored) to 0."""
+    dev = k_cache.get_device()
     NB, bs, Hkv, D = k_cache.shape
     if q.dim() != 3:
         raise ValueError("q must be (tokens, num_heads, head_dim)")
     T, H, _ = q.shape
-    qp, qs, qc = _token_rows(q, "q", (T, H, D))
-    kp, ks, kc = _token_rows(k, "k", (T, Hkv, D))
-    vp, vs, vc = _token_rows(v, "v", (T, Hkv, D))
-    _want(slot_mapping, "slot_mapping", torch.int64, (T,), contiguous=False)
-    slot_mapping = slot_mapping.contiguous()
+    qp, qs, qc = _token_rows(q, "q", (T, H, D), dev)
+    kp, ks, kc = _token_rows(k, "k", (T, Hkv, D), dev)
+    vp, vs, vc = _token_rows(v, "v", (T, Hkv, D), dev)
+    slot_mapping = _input(slot_mapping, "slot_mapping", torch.int64, (T,), dev)
     rows = rot = 0
+    cp = pp = qw = kw = sp = None
     if cos_sin is not None:
         if cos_sin.dim() != 2:
             raise ValueError("cos_sin must be (max_positions, rotary_dim)")
         rows, rot = cos_sin.shape
-        _want(cos_sin, "cos_sin", torch.float32, (rows, rot))
+        cp = _state(cos_sin, "cos_sin", torch.float32, (rows, rot), dev).data_ptr()
         if positions is None:
             raise ValueError("a rotation needs positions")
     if positions is not None:
-        _want(positions, "positions", torch.int64, (T,), contiguous=False)
-        positions = positions.contiguous()
+        positions = _input(positions, "positions", torch.int64, (T,), dev)
+        pp = positions.data_ptr()
     if q_weight is not None:
-        _want(q_weight, "q_weight", torch.bfloat16, (D,))
+        qw = _state(q_weight, "q_weight", torch.bfloat16, (D,), dev).data_ptr()
     if k_weight is not None:
-        _want(k_weight, "k_weight", torch.bfloat16, (D,))
+        kw = _state(k_weight, "k_weight", torch.bfloat16, (D,), dev).data_ptr()
     if scores is not None:
-        _want(scores, "scores", torch.float32, (NB, Hkv, bs))
+        sp = _state(scores, "scores", torch.float32, (NB, Hkv, bs), dev).data_ptr()
     if q_out is None:
         q_out = torch.empty((T, H, D), dtype=torch.bfloat16, device=q.device)
     else:
-        _want(q_out, "q_out", torch.bfloat16, (T, H, D))
-    cache = _checked_cache(k_cache, v_cache, k_scale, v_scale, q, k, v, positions, slot_mapping,
-                           q_weight, k_weight, cos_sin, q_out, scores)
-    params = NormRope(_ptr(q_weight), _ptr(k_weight), _ptr(cos_sin), rows, rot,
-                      1 if interleaved else 0, eps)
-    _run(q.get_device(), "pa_norm_rope_store", lib().pa_norm_rope_store, qp, qs, kp, ks, vp, vs,
-         ctypes.byref(params), _ptr(positions), slot_mapping.data_ptr(), T, H,
-         ctypes.byref(cache), _ptr(scores), q_out.data_ptr())
+        _state(q_out, "q_out", torch.bfloat16, (T, H, D), dev)
+    cache = _cache_of(k_cache, v_cache, k_scale, v_scale, dev)
+    _run(dev, "pa_norm_rope_store", (_lib or lib()).pa_norm_rope_store, qp, qs, kp, ks, vp, vs,
+         ctypes.byref(NormRope(qw, kw, cp, rows, rot, 1 if interleaved else 0, eps)), pp,
+         slot_mapping.data_ptr(), T, H, ctypes.byref(cache), sp, q_out.data_ptr())
     return q_out
 
 
@@ -432,27 +451,24 @@ def prefill_window(q, k_cache, v_cache, block_tables, cu_seqlens_q, cu_seqlens_k
     its own and the first `sinks` keys."""
     if q.dim() != 3:
         raise ValueError("q must be (total_q, num_heads, head_dim)")
+    dev = k_cache.get_device()
     T, H, D = q.shape
-    _want(q, "q", torch.bfloat16, (T, H, k_cache.shape[3]), contiguous=False)
     n = cu_seqlens_q.numel()
-    _want(cu_seqlens_q, "cu_seqlens_q", torch.int32, (n,), contiguous=False)
-    _want(cu_seqlens_k, "cu_seqlens_k", torch.int32, (n,), contiguous=False)
     if n < 1 or block_tables.dim() != 2:
         raise ValueError("block_tables must be (batch, blocks), cu_seqlens (batch + 1,)")
-    _want(block_tables, "block_tables", torch.int32, (n - 1, block_tables.shape[1]),
-          contiguous=False)
-    qc, block_tables = q.contiguous(), block_tables.contiguous()
-    cu_seqlens_q, cu_seqlens_k = cu_seqlens_q.contiguous(), cu_seqlens_k.contiguous()
+    width = block_tables.shape[1]
+    q = _input(q, "q", torch.bfloat16, (T, H, k_cache.shape[3]), dev)
+    cu_q = _input(cu_seqlens_q, "cu_seqlens_q", torch.int32, (n,), dev)
+    cu_k = _input(cu_seqlens_k, "cu_seqlens_k", torch.int32, (n,), dev)
+    bt = _input(block_tables, "block_tables", torch.int32, (n - 1, width), dev)
     if out is None:
         out = torch.empty((T, H, D), dtype=torch.bfloat16, device=q.device)
     else:
-        _want(out, "out", torch.bfloat16, (T, H, D))
-    cache = _checked_cache(k_cache, v_cache, None, None, q, block_tables, cu_seqlens_q,
-                           cu_seqlens_k, out)
-    _run(q.get_device(), "pa_prefill_window", lib().pa_prefill_window, qc.data_ptr(),
-         ctypes.byref(cache), block_tables.data_ptr(), block_tables.shape[1],
-         cu_seqlens_q.data_ptr(), cu_seqlens_k.data_ptr(), n - 1, H, T, int(max_q_len),
-         float(scale), int(window), int(sinks), out.data_ptr())
+        _state(out, "out", torch.bfloat16, (T, H, D), dev)
+    cache = _cache_of(k_cache, v_cache, None, None, dev)
+    _run(dev, "pa_prefill_window", (_lib or lib()).pa_prefill_window, q.data_ptr(),
+         ctypes.byref(cache), bt.data_ptr(), width, cu_q.data_ptr(), cu_k.data_ptr(), n - 1, H, T,
+         int(max_q_len), scale, int(window), int(sinks), out.data_ptr())
     return out
 
 
@@ -474,34 +490,34 @@ def decode_scored(q, k_cache, v_cache, block_tables, context_lens, scores, scale
     given."""
     if q.dim() != 3:
         raise ValueError("q must be (batch, num_heads, head_dim)")
+    dev = k_cache.get_device()
     B, H, D = q.shape
-    _want(q, "q", torch.bfloat16, (B, H, k_cache.shape[3]), contiguous=False)
-    _want(context_lens, "context_lens", torch.int32, (B,), contiguous=False)
     if block_tables.dim() != 2:
         raise ValueError("block_tables must be (batch, blocks)")
-    _want(block_tables, "block_tables", torch.int32, (B, block_tables.shape[1]), contiguous=False)
-    context_lens, block_tables = context_lens.contiguous(), block_tables.contiguous()
-    _want(scores, "scores", torch.float32, (k_cache.shape[0], k_cache.shape[2], k_cache.shape[1]))
-    qc = q.contiguous()
+    width = block_tables.shape[1]
+    nb, bs, hkv, d = k_cache.shape
+    q = _input(q, "q", torch.bfloat16, (B, H, d), dev)
+    cl = _input(context_lens, "context_lens", torch.int32, (B,), dev)
+    bt = _input(block_tables, "block_tables", torch.int32, (B, width), dev)
+    _state(scores, "scores", torch.float32, (nb, hkv, bs), dev)
     if out is None:
         out = torch.empty((B, H, D), dtype=torch.bfloat16, device=q.device)
     else:
-        _want(out, "out", torch.bfloat16, (B, H, D))
-    cache = _checked_cache(k_cache, v_cache, k_scale, v_scale, q, block_tables, context_lens,
-                           scores, out, workspace)
+        _state(out, "out", torch.bfloat16, (B, H, D), dev)
+    cache = _cache_of(k_cache, v_cache, k_scale, v_scale, dev)
+    ws = ws_bytes = 0
     if workspace is None:  # a caller-provided workspace is checked by the library
-        need = int(lib().pa_decode_scored_workspace_size(ctypes.byref(cache), B, H,
-                                                         block_tables.shape[1],
-                                                         int(max_context_len)))
+        need = decode_scored_workspace_size(k_cache, B, H, width, int(max_context_len), v_cache,
+                                            k_scale, v_scale)
         if need:
             workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    elif not workspace.is_contiguous():
-        raise ValueError("workspace must be contiguous")
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _run(q.get_device(), "pa_decode_scored", lib().pa_decode_scored, qc.data_ptr(), ctypes.byref(cache),
-         block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(),
-         int(max_context_len), B, H, float(scale), scores.data_ptr(), out.data_ptr(),
-         _ptr(workspace), ws_bytes)
+    elif not workspace.is_contiguous() or workspace.get_device() != dev:
+        raise ValueError("workspace must be contiguous and on the caches' device")
+    if workspace is not None:
+        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _run(dev, "pa_decode_scored", (_lib or lib()).pa_decode_scored, q.data_ptr(),
+         ctypes.byref(cache), bt.data_ptr(), width, cl.data_ptr(), int(max_context_len), B, H,
+         scale, scores.data_ptr(), out.data_ptr(), ws or None, ws_bytes)
     return out
 
 
@@ -512,29 +528,30 @@ def evict(k_cache, v_cache, scores, block_tables, context_lens, budget: int, *, 
     `sinks`, its last `recent` and the best scores between them, moved in order to the front of
     its blocks (K, V, scales and scores, in place). Returns (new_lens (B,) int32,
     kept (B, Hkv, budget) int32: the positions the rows came from)."""
+    dev = scores.get_device()
     B = context_lens.numel()
-    _want(context_lens, "context_lens", torch.int32, (B,), contiguous=False)
     if block_tables.dim() != 2:
         raise ValueError("block_tables must be (batch, blocks)")
-    _want(block_tables, "block_tables", torch.int32, (B, block_tables.shape[1]), contiguous=False)
-    context_lens, block_tables = context_lens.contiguous(), block_tables.contiguous()
-    Hkv = k_cache.shape[2]
-    _want(scores, "scores", torch.float32, (k_cache.shape[0], Hkv, k_cache.shape[1]))
+    width = block_tables.shape[1]
+    nb, bs, hkv, _ = k_cache.shape
+    cl = _input(context_lens, "context_lens", torch.int32, (B,), dev)
+    bt = _input(block_tables, "block_tables", torch.int32, (B, width), dev)
+    _state(scores, "scores", torch.float32, (nb, hkv, bs), dev)
     budget = int(budget)
     if kept is None:
-        kept = torch.empty((B, Hkv, max(budget, 0)), dtype=torch.int32, device=scores.device)
+        kept = torch.empty((B, hkv, max(budget, 0)), dtype=torch.int32, device=scores.device)
     else:
-        _want(kept, "kept", torch.int32, (B, Hkv, budget))
+        _state(kept, "kept", torch.int32, (B, hkv, budget), dev)
     if new_lens is None:
         new_lens = torch.empty((B,), dtype=torch.int32, device=scores.device)
     else:
-        _want(new_lens, "new_lens", torch.int32, (B,))
-    cache = _checked_cache(k_cache, v_cache, k_scale, v_scale, scores, block_tables,
-                           context_lens, kept, new_lens)
-    _run(scores.get_device(), "pa_evict", lib().pa_evict, ctypes.byref(cache), scores.data_ptr(),
-         block_tables.data_ptr(), block_tables.shape[1], context_lens.data_ptr(),
-         int(max_context_len), B, budget, int(sinks), int(recent), kept.data_ptr(),
-         new_lens.data_ptr())
+        _state(new_lens, "new_lens", torch.int32, (B,), dev)
+    if k_cache.get_device() != dev:
+        raise ValueError("k_cache must be on the scores' device")
+    cache = _cache_of(k_cache, v_cache, k_scale, v_scale, dev)
+    _run(dev, "pa_evict", (_lib or lib()).pa_evict, ctypes.byref(cache), scores.data_ptr(),
+         bt.data_ptr(), width, cl.data_ptr(), int(max_context_len), B, budget, int(sinks),
+         int(recent), kept.data_ptr(), new_lens.data_ptr())
     return new_lens, kept
 
 

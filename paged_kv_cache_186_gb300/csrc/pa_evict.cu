@@ -112,6 +112,7 @@ __global__ void __launch_bounds__(NT, 4) select_kernel(const EvictArgs a, int he
   for (int i = tid; i < kBins0; i += NT) hist0[i] = 0;
   for (int i = tid; i < kDigits * kBins; i += NT) (&hist[0][0])[i] = (&total[0][0])[i] = 0;
   if (tid < NW) nlisted[tid] = 0;
+  if (tid <= kDigits) sel[tid][0] = sel[tid][1] = 0;
   grid_dependency_wait();
   grid_launch_dependents();  // move waits for this grid before it reads anything
   const int L = min(max(a.context_lens[b], 0), a.len_cap);
@@ -397,10 +398,14 @@ __global__ void __launch_bounds__(kMvThreads) move_kernel(const EvictArgs a) {
   const int parts = 2 * cols + 1;
   const int seg = blockIdx.x / parts, part = blockIdx.x % parts;
   const int b = seg / a.num_kv_heads, kvh = seg % a.num_kv_heads;
-  if (min(max(a.context_lens[b], 0), a.len_cap) <= a.budget) return;
+  const int L = min(max(a.context_lens[b], 0), a.len_cap);
+  if (L <= a.budget) return;
   const int32_t* const kept = a.kept + static_cast<long long>(seg) * a.budget;
   const int32_t* const table = a.block_tables + static_cast<long long>(b) * a.max_blocks;
   const int bs_shift = a.block_size == 16 ? 4 : 5, bs_mask = a.block_size - 1;
+  // A kept entry; -1 should scores that changed under select (a call on another
+  // stream) have left no position of the sequence there.
+  auto checked = [&](int p) { return p >= 0 && p < L ? p : -1; };
   // pool block of logical position p; -1: outside the pool
   auto block_of = [&](int p) {
     const int phys = table[p >> bs_shift];
@@ -432,7 +437,7 @@ __global__ void __launch_bounds__(kMvThreads) move_kernel(const EvictArgs a) {
       p1 = indexer && row_of(tile) < a.budget ? kept[row_of(tile)] : -1;
     };
     auto read_blocks = [&](int tile) {  // of the tile read_kept was last called for
-      p2 = p1;
+      p2 = checked(p1);
       if (p2 > row_of(tile)) {
         sb = table[p2 >> bs_shift];
         db = table[row_of(tile) >> bs_shift];
@@ -443,8 +448,8 @@ __global__ void __launch_bounds__(kMvThreads) move_kernel(const EvictArgs a) {
         index[(tile % kMvIndex) * kMvRows + threadIdx.x] =
             p2 > row_of(tile) && in_pool(sb) && in_pool(db)
                 ? make_int2((sb << bs_shift) + (p2 & bs_mask),
-                                           (db << bs_shift) + (row_of(tile) & bs_mask))
-                               : make_int2(-1, -1);
+                            (db << bs_shift) + (row_of(tile) & bs_mask))
+                : make_int2(-1, -1);
     };
     auto issue = [&](int tile) {
       const int2* ix = index + (tile % kMvIndex) * kMvRows + r;
@@ -502,8 +507,8 @@ __global__ void __launch_bounds__(kMvThreads) move_kernel(const EvictArgs a) {
       const int row = t0 + i * kMvThreads + threadIdx.x;
       to[i] = -1;
       if (row >= a.budget) continue;
-      const int p = kept[row];
-      if (p == row) continue;
+      const int p = checked(kept[row]);
+      if (p <= row) continue;
       const long long sb = block_of(p), db = block_of(row);
       if (sb < 0 || db < 0) continue;
       to[i] = ((db * a.num_kv_heads + kvh) << bs_shift) + (row & bs_mask);

@@ -31,8 +31,8 @@
 //     one thread per row.
 // On one GB300: 64 sequences of 2176 keys to 2048 (8 heads, E4M3) 13 us of
 // selection and 97 us of moving 536 MB (HBM-bound, 5.5 TB/s); 8 contexts of
-// 32768-131072 keys to 4096 (8 heads, bf16) about 42 and 40 us, the selection
-// bound by its passes over 4.4 M keys and the cluster's barriers.
+// 32768-131072 keys to 4096 (8 heads, bf16) 42 and 56 us, the selection bound by
+// the latency of its three passes over 4.4 M keys and of the cluster's barriers.
 #include <algorithm>
 
 #include "pa_device.cuh"
@@ -542,6 +542,7 @@ cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream) {
   if (segs * std::max<long long>(parts, C) > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   const int share = ((a.len_cap + C - 1) / C + 127) / 128 * 128;
   const int held = std::min(share, kMaxHeld);
+  // (the 8 long contexts with 256 threads a CTA: 120 us instead of 102)
   auto* const select = share <= 4096 ? select_kernel<256> : select_kernel<512>;
   static bool attr_set[64] = {};
   int dev = 0;

@@ -258,8 +258,8 @@ pa_status pa_decode_window(const void* q, const pa_kv_cache* cache, const int32_
  *             are left as they were. pa_norm_rope_store can set a new slot's
  *             score to zero. After a launch that reported
  *             PA_DEVERR_WAIT_TIMEOUT they are as invalid as out.
- *   workspace at least pa_decode_scored_workspace_size() bytes, contract as for
- *             pa_decode. It holds the scores of every key: 4 bytes per query
+ *   workspace at least pa_decode_scored_workspace_size() bytes (0: the shape is
+ *             not supported), contract as for pa_decode. It holds the scores of every key: 4 bytes per query
  *             head and key of the bound batch * max_context_len.
  *   other arguments as pa_decode; out equals pa_decode's bit for bit. Batches
  *   above 16384 return PA_ERR_UNSUPPORTED.

@@ -121,3 +121,48 @@ def test_empty_calls_change_nothing():
     assert (out == 0).all() and (new == 0).all() and (kept == -1).all()
     assert (kc == 1).all() and (vc == 1).all() and (scores == 1).all()
     assert pa.get_device_error() == 0
+
+
+def test_lengths_written_right_before_a_store_and_a_decode():
+    # a torch kernel raises the lengths, norm_rope_store follows it, then a decode that reads
+    # the lengths before its own dependency wait: every step sees that step's lengths
+    g = torch.Generator().manual_seed(401)
+    B, H, Hkv, D, bs, width = 16, 8, 2, 128, 16, 30
+    kc, vc = (torch.randn((B * width, bs, Hkv, D), generator=g).to(torch.bfloat16).cuda()
+              for _ in range(2))
+    bt = torch.randperm(B * width, generator=g).view(B, width).to(torch.int32).cuda()
+    lens = torch.randint(1, 200, (B,), generator=g).to(torch.int32).cuda()
+    start = lens.clone()
+    steps = 200
+    qkv = torch.randn((steps, B, H + 2 * Hkv, D), generator=g).to(torch.bfloat16).cuda()
+    rows = torch.arange(B, device="cuda")
+    slots = []
+    for s in range(steps):
+        p = (start + s).long()
+        slots.append(bt[rows, p // bs].long() * bs + p % bs)
+    outs = torch.zeros((steps, B, H, D), dtype=torch.bfloat16, device="cuda")
+    scores = torch.zeros((B * width, Hkv, bs), device="cuda")
+    ws = torch.empty(pa.decode_scored_workspace_size(kc, B, H, width), dtype=torch.uint8,
+                     device="cuda")
+    first = kc.clone(), vc.clone()
+    torch.cuda.synchronize()
+    for s in range(steps):
+        x = qkv[s]
+        lens.add_(1)
+        q = pa.norm_rope_store(x[:, :H], x[:, H:H + Hkv], x[:, H + Hkv:], None, slots[s], kc, vc)
+        if s % 2:
+            pa.decode_scored(q, kc, vc, bt, lens, scores, 0.1, out=outs[s], workspace=ws)
+        else:
+            pa.decode(q, kc, vc, bt, lens, 0.1, out=outs[s], workspace=ws)
+    torch.cuda.synchronize()
+    kc.copy_(first[0])
+    vc.copy_(first[1])
+    for s in range(steps):
+        x = qkv[s]
+        now = (start + s + 1).to(torch.int32)
+        pa.store_kv(x[:, H:H + Hkv], x[:, H + Hkv:], slots[s], kc, vc)
+        torch.cuda.synchronize()
+        ref = pa.decode(x[:, :H], kc, vc, bt, now, 0.1)
+        torch.cuda.synchronize()
+        assert torch.equal(outs[s], ref), s
+    assert pa.get_device_error() == 0

@@ -48,7 +48,8 @@
 //     its two query tiles sees, packed into 128-key tiles: the sink keys'
 //     blocks, then those from the first window key's on (PairKeys; a tile of
 //     their own for a few sinks would be a tenth of the steps of a window of
-//     1000). V rows that no row sees are zeroed, and a row's own bounds are
+//     1000). V rows that no row of the pair sees (between sinks and window, and
+//     behind the pair's last key) are zeroed, and a row's own bounds are
 //     masked on the tiles that cross them. Where the sinks reach to the window
 //     all blocks are walked, and those without such a key are fetched out of
 //     bounds like those past the end (their table entries are not read). A row
@@ -214,6 +215,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr int nstep = SPLIT ? 2 : 1;
   if (SPLIT) Tq[1] = Tq[0];
   const int T = max(Tq[0], Tq[1]);
+  const int pair_end = min(cached + min(t00 + 2 * TPT, q_len), kv_len);  // keys the pair sees: below
   // P.V takes P as two bf16 terms on key tile 0 of a query tile whose first
   // row sees fewer than kBN keys (every key of such a row lies in tile 0), and
   // on every tile of a window of fewer than kBN keys
@@ -280,7 +282,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     const long long bt_row = static_cast<long long>(b) * a.max_blocks;
-    const int n_keys = min(cached + min(t00 + 2 * TPT, q_len), kv_len);
     const int oob = a.num_blocks * BS;  // first row past the pool: TMA fills zeros
     // Block ids come 32 at a time (lane l: logical block wb + l, as the pool
     // row of its first key), the next window's table reads in flight while
@@ -293,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         need = lb * BS < pk.se || (lb + 1) * BS > pk.lo;
       }
       int rc = oob;
-      if (need && lb * BS < n_keys && lb < a.max_blocks) {
+      if (need && lb * BS < pair_end && lb < a.max_blocks) {
         const int phys = a.block_tables[bt_row + lb];
         if (phys >= 0 && phys < a.num_blocks) {
           rc = phys * BS;
@@ -385,7 +386,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int n = 0; ok && n < T; ++n) {
       const int s = n % kStages;
       if (!warp_wait(bar(BAR_VF + s), (n / kStages) & 1, &abort_flag, a.err)) break;
-      const int r0 = kv_len - tile_base(n);
+      // V rows behind the last key, in its block (later blocks were not fetched):
+      // for a window behind the pair's last key, so that a later token's V may
+      // hold anything
+      const int r0 = (WIN ? pair_end : kv_len) - tile_base(n);
       if constexpr (WIN) {
         // V rows of keys [se, lo), which no row sees, in the blocks around
         // the bounds (whole blocks of them were not fetched)

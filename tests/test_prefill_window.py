@@ -187,3 +187,26 @@ def test_short_sequences_repeat_bit_for_bit():
                               g.cu_seqlens_k, g.scale, 2000, 4, max_q_len=32, out=out)
         assert torch.equal(out, first)
     assert pa.get_device_error() == 0
+
+
+@pytest.mark.parametrize("group, bs", [(4, 16), (1, 32), (16, 16), (8, 32)])
+@pytest.mark.parametrize("window, sinks", [(20, 4), (130, 0), (1000, 4), (60, 300)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_later_tokens_in_a_pairs_last_block_may_hold_anything(group, bs, window, sinks, bad):
+    # the last block a pair of query tiles sees also holds the next pair's first keys: K and V
+    # there reach no row of the pairs before
+    pair = 2 * (128 // group)
+    g = case_inputs(group, 1, bs, [5], [3 * pair + 7], seed=140 + group + window)
+    want = want64(g, window, sinks)
+    bt = g.block_tables.cpu().numpy()
+    clean = g.k_cache.clone(), g.v_cache.clone()
+    for k in (1, 2, 3):
+        end = 5 + k * pair  # keys of the pairs before the k-th
+        assert end % bs
+        for j in range(end, -(-end // bs) * bs):
+            g.k_cache[bt[0, j // bs], j % bs] = bad
+            g.v_cache[bt[0, j // bs], j % bs] = bad
+        rows = k * pair
+        assert_attention_close(run(g, window, sinks)[:rows], want[:rows], f"{k} {bad}")
+        g.k_cache.copy_(clean[0])
+        g.v_cache.copy_(clean[1])

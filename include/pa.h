@@ -295,7 +295,7 @@ pa_status pa_decode_scored(const void* q, const pa_kv_cache* cache, const int32_
  * token's position (for the rotation) is the caller's to keep counting. The
  * blocks of a cut sequence must be distinct and not shared with another
  * sequence, and no other call may read or write them (or their scores) at the
- * same time. Length bounds above 2^30 return PA_ERR_UNSUPPORTED. A physical
+ * same time. Length bounds and budgets above 2^30 return PA_ERR_UNSUPPORTED. A physical
  * block id out of range sets PA_DEVERR_BLOCK_RANGE; scores there count as 0 and
  * rows there are not moved.
  */

@@ -537,7 +537,8 @@ pa_status pa_evict(const pa_kv_cache* cache, float* scores, const int32_t* block
     return PA_ERR_NULL;
   if (new_lens < context_lens + batch && context_lens < new_lens + batch) return PA_ERR_SHAPE;
   const int cap = decode_len_cap(cache, max_blocks_per_seq, max_context_len);
-  if (batch > 65535 || cap > (1 << 30)) return PA_ERR_UNSUPPORTED;
+  // (the kernels step 32-bit positions and rows past the length bound and the budget)
+  if (batch > 65535 || cap > (1 << 30) || budget > (1 << 30)) return PA_ERR_UNSUPPORTED;
   if (!aligned16(scores)) return PA_ERR_ALIGN;
   DeviceInfo* dev = nullptr;
   if ((st = device_info(&dev)) != PA_OK) return st;

@@ -111,6 +111,11 @@ def test_evict_arguments(L, kw, want):
     assert evict(L, **kw) == want
 
 
+@pytest.mark.parametrize("budget", [(1 << 30) + 1, 0x7fffffff - 4096, 0x7fffffff])
+def test_evict_refuses_budgets_whose_rows_32_bits_cannot_step_over(L, budget):
+    assert evict(L, budget=budget) == 4
+
+
 @pytest.mark.parametrize("kw, want", BAD_CACHES)
 def test_every_call_checks_the_cache(L, kw, want):
     for f in (norm_rope, prefill, scored, evict):

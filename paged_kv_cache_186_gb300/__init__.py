@@ -173,6 +173,13 @@ def _input(t: torch.Tensor, name: str, dtype: torch.dtype, shape, dev: int) -> t
     return _state(t.contiguous(), name, dtype, shape, dev)
 
 
+def _check_i32(**numbers: int) -> None:
+    """Refuse arguments of a C call that do not fit 32 bits: ctypes would drop their upper bits."""
+    for name, x in numbers.items():
+        if not -0x80000000 <= x <= 0x7fffffff:
+            raise ValueError(f"{name} must fit 32 bits, got {x}")
+
+
 _KV_CODES = {torch.bfloat16: PA_KV_BF16, torch.uint8: PA_KV_FP8_E4M3,
              torch.float8_e4m3fn: PA_KV_FP8_E4M3, torch.int8: PA_KV_INT8}
 
@@ -451,6 +458,9 @@ def prefill_window(q, k_cache, v_cache, block_tables, cu_seqlens_q, cu_seqlens_k
     its own and the first `sinks` keys."""
     if q.dim() != 3:
         raise ValueError("q must be (total_q, num_heads, head_dim)")
+    max_q_len, window, sinks = int(max_q_len), int(window), int(sinks)
+    if not 0 <= max_q_len | window | sinks <= 0x7fffffff:  # (all of them: one comparison)
+        _check_i32(max_q_len=max_q_len, window=window, sinks=sinks)
     dev = k_cache.get_device()
     T, H, D = q.shape
     n = cu_seqlens_q.numel()
@@ -468,7 +478,7 @@ def prefill_window(q, k_cache, v_cache, block_tables, cu_seqlens_q, cu_seqlens_k
     cache = _cache_of(k_cache, v_cache, None, None, dev)
     _run(dev, "pa_prefill_window", (_lib or lib()).pa_prefill_window, q.data_ptr(),
          ctypes.byref(cache), bt.data_ptr(), width, cu_q.data_ptr(), cu_k.data_ptr(), n - 1, H, T,
-         int(max_q_len), scale, int(window), int(sinks), out.data_ptr())
+         max_q_len, scale, window, sinks, out.data_ptr())
     return out
 
 
@@ -476,6 +486,8 @@ def decode_scored_workspace_size(k_cache, batch: int, num_heads: int, max_blocks
                                  max_context_len: int = 0, v_cache=None, k_scale=None,
                                  v_scale=None) -> int:
     """Bytes of the workspace of decode_scored (0: the shape is not supported)."""
+    _check_i32(batch=batch, num_heads=num_heads, max_blocks_per_seq=max_blocks_per_seq,
+               max_context_len=max_context_len)
     cache = make_cache(k_cache, k_cache if v_cache is None else v_cache, k_scale, v_scale)
     return int(lib().pa_decode_scored_workspace_size(ctypes.byref(cache), batch, num_heads,
                                                      max_blocks_per_seq, max_context_len))
@@ -490,6 +502,9 @@ def decode_scored(q, k_cache, v_cache, block_tables, context_lens, scores, scale
     given."""
     if q.dim() != 3:
         raise ValueError("q must be (batch, num_heads, head_dim)")
+    max_context_len = int(max_context_len)
+    if not 0 <= max_context_len <= 0x7fffffff:
+        _check_i32(max_context_len=max_context_len)
     dev = k_cache.get_device()
     B, H, D = q.shape
     if block_tables.dim() != 2:
@@ -507,7 +522,7 @@ def decode_scored(q, k_cache, v_cache, block_tables, context_lens, scores, scale
     cache = _cache_of(k_cache, v_cache, k_scale, v_scale, dev)
     ws = ws_bytes = 0
     if workspace is None:  # a caller-provided workspace is checked by the library
-        need = decode_scored_workspace_size(k_cache, B, H, width, int(max_context_len), v_cache,
+        need = decode_scored_workspace_size(k_cache, B, H, width, max_context_len, v_cache,
                                             k_scale, v_scale)
         if need:
             workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
@@ -516,7 +531,7 @@ def decode_scored(q, k_cache, v_cache, block_tables, context_lens, scores, scale
     if workspace is not None:
         ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     _run(dev, "pa_decode_scored", (_lib or lib()).pa_decode_scored, q.data_ptr(),
-         ctypes.byref(cache), bt.data_ptr(), width, cl.data_ptr(), int(max_context_len), B, H,
+         ctypes.byref(cache), bt.data_ptr(), width, cl.data_ptr(), max_context_len, B, H,
          scale, scores.data_ptr(), out.data_ptr(), ws or None, ws_bytes)
     return out
 
@@ -528,6 +543,10 @@ def evict(k_cache, v_cache, scores, block_tables, context_lens, budget: int, *, 
     `sinks`, its last `recent` and the best scores between them, moved in order to the front of
     its blocks (K, V, scales and scores, in place). Returns (new_lens (B,) int32,
     kept (B, Hkv, budget) int32: the positions the rows came from)."""
+    budget, sinks, recent = int(budget), int(sinks), int(recent)
+    max_context_len = int(max_context_len)
+    if not 0 <= budget | sinks | recent | max_context_len <= 0x7fffffff:
+        _check_i32(budget=budget, sinks=sinks, recent=recent, max_context_len=max_context_len)
     dev = scores.get_device()
     B = context_lens.numel()
     if block_tables.dim() != 2:
@@ -537,7 +556,6 @@ def evict(k_cache, v_cache, scores, block_tables, context_lens, budget: int, *, 
     cl = _input(context_lens, "context_lens", torch.int32, (B,), dev)
     bt = _input(block_tables, "block_tables", torch.int32, (B, width), dev)
     _state(scores, "scores", torch.float32, (nb, hkv, bs), dev)
-    budget = int(budget)
     if kept is None:
         kept = torch.empty((B, hkv, max(budget, 0)), dtype=torch.int32, device=scores.device)
     else:
@@ -550,8 +568,8 @@ def evict(k_cache, v_cache, scores, block_tables, context_lens, budget: int, *, 
         raise ValueError("k_cache must be on the scores' device")
     cache = _cache_of(k_cache, v_cache, k_scale, v_scale, dev)
     _run(dev, "pa_evict", (_lib or lib()).pa_evict, ctypes.byref(cache), scores.data_ptr(),
-         bt.data_ptr(), width, cl.data_ptr(), int(max_context_len), B, budget, int(sinks),
-         int(recent), kept.data_ptr(), new_lens.data_ptr())
+         bt.data_ptr(), width, cl.data_ptr(), max_context_len, B, budget, sinks,
+         recent, kept.data_ptr(), new_lens.data_ptr())
     return new_lens, kept
 
 

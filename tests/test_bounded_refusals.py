@@ -186,3 +186,29 @@ def test_other_bindings_refuse_wrong_types_shapes_and_devices():
     for fn, args, err in bad:
         with pytest.raises(err):
             fn(*args)
+
+
+@pytest.mark.parametrize("big", [2 ** 31, 2 ** 32, 2 ** 32 + 1, 2 ** 63, -2 ** 32 + 5])
+def test_bindings_refuse_numbers_that_do_not_fit_32_bits(big):
+    # ctypes drops their upper bits: a window of 2^32 + 1 would be a window of 1
+    kc, vc = _t((8, 16, 2, 128)), _t((8, 16, 2, 128))
+    bt, cl = _t((2, 4), torch.int32), _t(2, torch.int32)
+    cu, sc = _t(3, torch.int32), _t((8, 2, 16), torch.float32)
+    q = _t((2, 4, 128))
+    calls = [
+        (pa.prefill_window, (q, kc, vc, bt, cu, cu, 0.1, big), {}, "window"),
+        (pa.prefill_window, (q, kc, vc, bt, cu, cu, 0.1, 8, big), {}, "sinks"),
+        (pa.prefill_window, (q, kc, vc, bt, cu, cu, 0.1, 8), dict(max_q_len=big), "max_q_len"),
+        (pa.decode_scored, (q, kc, vc, bt, cl, sc, 0.1), dict(max_context_len=big),
+         "max_context_len"),
+        (pa.decode_scored_workspace_size, (kc, 2, 4, 4), dict(max_context_len=big),
+         "max_context_len"),
+        (pa.decode_scored_workspace_size, (kc, big, 4, 4), {}, "batch"),
+        (pa.evict, (kc, vc, sc, bt, cl, big), {}, "budget"),
+        (pa.evict, (kc, vc, sc, bt, cl, 16), dict(sinks=big), "sinks"),
+        (pa.evict, (kc, vc, sc, bt, cl, 16), dict(recent=big), "recent"),
+        (pa.evict, (kc, vc, sc, bt, cl, 16), dict(max_context_len=big), "max_context_len"),
+    ]
+    for fn, args, kw, name in calls:
+        with pytest.raises(ValueError, match=f"{name} must fit 32 bits"):
+            fn(*args, **kw)

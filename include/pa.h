@@ -388,7 +388,8 @@ pa_status pa_prefill_varlen(const void* q, const pa_kv_cache* cache, const int32
  *            pa_prefill_varlen's mask.
  *   sinks    >= 0 (PA_ERR_SHAPE if negative).
  *   other arguments, support and arithmetic as pa_prefill_varlen, with P as two
- *   bf16 terms on every tile where window + sinks < 128.
+ *   bf16 terms also on the first 128-key tile (the sinks') where sinks > 0, and
+ *   on every tile where window + sinks < 128.
  * Blocks that hold no key visible to a 128-row query tile pair are not read, nor
  * their table entries, so the blocks of keys no row of the call sees may have
  * been freed. K and V there, and in keys of a partly visible block that no row

@@ -218,10 +218,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int pair_end = min(cached + min(t00 + 2 * TPT, q_len), kv_len);  // keys the pair sees: below
   // P.V takes P as two bf16 terms on key tile 0 of a query tile whose first
   // row sees fewer than kBN keys (every key of such a row lies in tile 0), and
-  // on every tile of a window of fewer than kBN keys
+  // with a window where there are sinks (they lie in tile 0, and draw most of
+  // a row's weight onto a few keys, whose roundings do not average out) and on
+  // every tile of a window of fewer than kBN keys
   const bool narrow = WIN && min(a.window, kBN) + min(a.sinks, kBN) < kBN;
   auto two_term = [&](int i, int n) {
-    return (n == 0 && cached + t00 + i * TPT < kBN) || narrow;
+    return (n == 0 && (cached + t00 + i * TPT < kBN || (WIN && a.sinks > 0))) || narrow;
   };
   __nv_bfloat16* const out = static_cast<__nv_bfloat16*>(a.out);
   const int H = a.num_heads;

@@ -210,3 +210,36 @@ def test_later_tokens_in_a_pairs_last_block_may_hold_anything(group, bs, window,
         assert_attention_close(run(g, window, sinks)[:rows], want[:rows], f"{k} {bad}")
         g.k_cache.copy_(clean[0])
         g.v_cache.copy_(clean[1])
+
+
+@pytest.mark.parametrize("cached, q_lens", [([300, 0, 700], [70, 200, 1]),  # two query tiles a CTA
+                                            ([300, 129, 2000], [32, 20, 1])])  # one
+@pytest.mark.parametrize("window, sinks", [(200, 4), (1000, 4), (300, 128), (5000, 1)])
+def test_rows_whose_weight_lies_on_the_sinks(cached, q_lens, window, sinks):
+    """Four sinks hold nearly all the weight, in proportions that differ from row to row.
+
+    Only the first dim of q and K is not zero, so every score is one exact product. Of the
+    weights, exp2's argument (below 8 where the weight counts: 2 roundings of 2^-24 * 8, times
+    ln 2) and ex2.approx (2^-22) give 2^-20, two bf16 terms 2^-17; the fp32 sums of at most a few
+    hundred terms 2^-16 each: together below 2^-14 of sum w |v|, next to the output's own
+    rounding, 2^-8 of it. With the weights rounded once to bf16 an output would be off by up to
+    2^-9 of sum w |v|, thirty times as much."""
+    g = case_inputs(8, 2, 16, cached, q_lens, seed=150 + window + sinks)
+    gen = torch.Generator().manual_seed(151)
+    bt = g.block_tables.cpu().numpy()
+    g.k_cache.zero_()
+    g.k_cache[..., 0] = -40.0
+    for b in range(len(q_lens)):
+        g.k_cache[bt[b, 0], :4, :, 0] = -torch.rand((4, 2), generator=gen).to(torch.bfloat16).cuda()
+    q0 = (0.5 + 1.5 * torch.rand(g.q.shape[:2], generator=gen)).to(torch.bfloat16).cuda()
+    g.q.zero_()
+    g.q[..., 0] = q0
+    g.scale = 1.0
+    want = want64(g, window, sinks)
+    v = g.v_cache.clone()
+    g.v_cache.abs_()
+    mag = want64(g, window, sinks)
+    g.v_cache.copy_(v)
+    got = run(g, window, sinks, max(q_lens)).float().cpu().double().numpy()
+    over = np.abs(got - want) - (np.abs(want) * 2.0 ** -8 + mag * 2.0 ** -14)
+    assert over.max() <= 0, f"{float(over.max()):.3e} past the bound"

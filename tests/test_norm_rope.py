@@ -296,3 +296,33 @@ def test_other_stream_and_graph_replay():
         graph.replay()
         torch.cuda.synchronize()
         check(s, before, out)
+
+
+@pytest.mark.parametrize("kv", ["fp8", "int8"])
+@pytest.mark.parametrize("case", [(450, 8, 8, False), (900, 8, 8, True), (520, 24, 20, False),
+                                  (1201, 64, 8, False)], ids=lambda c: f"T{c[0]}H{c[1]}kv{c[2]}")
+def test_large_8_bit_stores(case, kv):
+    # past the first launch bound a warp takes two rounds of two rows, two or four times over:
+    # with eight kv heads and more the quantised rows go round that loop as well
+    T, H, Hkv, inter = case
+    s = make(T, H, Hkv, 128, 16, kv, 128, seed=T)
+    s["slots"][T // 3] = -1
+    before = snapshot(s)
+    out = call(s, inter)
+    assert pa.get_device_error() == 0
+    check(s, before, out, inter)
+
+
+@pytest.mark.parametrize("kv", ["fp8", "int8"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+def test_every_element_of_a_row_with_a_nan_or_infinity_reads_back_as_nan(kv, bad):
+    s = make(6, 2, 2, 128, 16, kv, seed=13)
+    s["v"], s["k"] = s["v"].clone(), s["k"].clone()
+    s["v"][2, 1, 77] = bad
+    s["k"][4, 0, 3] = bad
+    call(s)
+    for name, t, h in (("v", 2, 1), ("k", 4, 0)):
+        slot = int(s["slots"][t])
+        got = ops64.cache_values(s[name + "c"].cpu(), s[name + "s"].cpu())[slot // 16, slot % 16]
+        assert np.isnan(got[h]).all()
+        assert np.isfinite(got[1 - h]).all()

@@ -406,12 +406,10 @@ __global__ void __launch_bounds__(kMvThreads) move_kernel(const EvictArgs a) {
   // A kept entry; -1 should scores that changed under select (a call on another
   // stream) have left no position of the sequence there.
   auto checked = [&](int p) { return p >= 0 && p < L ? p : -1; };
-  // pool block of logical position p; -1: outside the pool
-  auto block_of = [&](int p) {
-    const int phys = table[p >> bs_shift];
-    if (phys >= 0 && phys < a.num_blocks) return phys;
+  auto in_pool = [&](int phys) {
+    if (phys >= 0 && phys < a.num_blocks) return true;
     report_error(a.err, PA_DEVERR_BLOCK_RANGE);
-    return -1;
+    return false;
   };
   if (part < 2 * cols) {
     uint8_t* const base = static_cast<uint8_t*>(part < cols ? a.k_cache : a.v_cache) +
@@ -427,11 +425,6 @@ __global__ void __launch_bounds__(kMvThreads) move_kernel(const EvictArgs a) {
     const bool indexer = threadIdx.x < kMvRows;
     // (used only a step after they are read, so that no lookup is waited for)
     int p1 = -1, p2 = -1, sb = -1, db = -1;  // kept entries of two tiles, blocks of the second
-    auto in_pool = [&](int phys) {
-      if (phys >= 0 && phys < a.num_blocks) return true;
-      report_error(a.err, PA_DEVERR_BLOCK_RANGE);
-      return false;
-    };
     auto row_of = [&](int tile) { return tile * kMvRows + static_cast<int>(threadIdx.x); };
     auto read_kept = [&](int tile) {
       p1 = indexer && row_of(tile) < a.budget ? kept[row_of(tile)] : -1;
@@ -509,10 +502,11 @@ __global__ void __launch_bounds__(kMvThreads) move_kernel(const EvictArgs a) {
       if (row >= a.budget) continue;
       const int p = checked(kept[row]);
       if (p <= row) continue;
-      const long long sb = block_of(p), db = block_of(row);
-      if (sb < 0 || db < 0) continue;
-      to[i] = ((db * a.num_kv_heads + kvh) << bs_shift) + (row & bs_mask);
-      const long long from = ((sb * a.num_kv_heads + kvh) << bs_shift) + (p & bs_mask);
+      const int sb = table[p >> bs_shift], db = table[row >> bs_shift];
+      if (!in_pool(sb) || !in_pool(db)) continue;
+      to[i] = ((static_cast<long long>(db) * a.num_kv_heads + kvh) << bs_shift) + (row & bs_mask);
+      const long long from =
+          ((static_cast<long long>(sb) * a.num_kv_heads + kvh) << bs_shift) + (p & bs_mask);
 #pragma unroll
       for (int j = 0; j < 3; ++j)
         if (j < n) x[i][j] = arr[j][from];

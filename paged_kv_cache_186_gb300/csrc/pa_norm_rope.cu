@@ -90,7 +90,8 @@ __device__ __forceinline__ uint2 codes8(const float (&x)[8]) {
 // rounds of 256/D rows; a batch's rows are read while the one before is worked
 // on.
 template <int D, int KV, bool INTER, int NIT>
-__global__ void __launch_bounds__(kNrWarps * 32, NIT == 2 ? 8 : NIT == 4 ? 6 : 1) norm_rope_kernel(const NormRopeArgs a) {
+__global__ void __launch_bounds__(kNrWarps * 32, NIT == 2 ? 8 : 1)
+    norm_rope_kernel(const NormRopeArgs a) {
   constexpr int LPR = D / 8;     // lanes per row
   constexpr int RPW = 32 / LPR;  // rows of a round
   constexpr int RW = NIT * RPW;  // rows of a batch

@@ -41,10 +41,11 @@
  *     Decode launches may start while the previous launch of this library on
  *     the stream is finishing (programmatic dependent launch): they read
  *     context_lens and block_tables before waiting for it, and everything
- *     else after. No kernel of this library writes those two arrays (except
- *     pa_evict its new_lens, complete before its last launch begins); a
- *     caller's own kernel that writes them and lets its dependents start
- *     early must not directly precede a decode call.
+ *     else after. No kernel of this library writes those two arrays, except
+ *     pa_evict its new_lens: they are complete before its last launch ends,
+ *     and that launch lets nothing behind it start before its end, so a decode
+ *     may follow it. A caller's own kernel that writes them and lets its
+ *     dependents start early must not directly precede a decode call.
  *   - Argument errors are returned before anything is launched. A launch
  *     failure returns PA_ERR_CUDA. Out-of-range indices found on the device
  *     (a slot beyond the pool, a wait that timed out) never fault: the access
@@ -259,8 +260,11 @@ pa_status pa_decode_window(const void* q, const pa_kv_cache* cache, const int32_
  *             score to zero. After a launch that reported
  *             PA_DEVERR_WAIT_TIMEOUT they are as invalid as out.
  *   workspace at least pa_decode_scored_workspace_size() bytes (0: the shape is
- *             not supported), contract as for pa_decode. It holds the scores of every key: 4 bytes per query
- *             head and key of the bound batch * max_context_len.
+ *             not supported), contract as for pa_decode. It holds the scores of
+ *             every key: 4 bytes per query head and key of the bound batch *
+ *             max_context_len, which can be as large as the cache. A tight
+ *             max_context_len keeps it small; without one it goes by the width
+ *             of the block table.
  *   other arguments as pa_decode; out equals pa_decode's bit for bit. Batches
  *   above 16384 return PA_ERR_UNSUPPORTED.
  */
@@ -288,6 +292,10 @@ pa_status pa_decode_scored(const void* q, const pa_kv_cache* cache, const int32_
  *   kept           (batch, num_kv_heads, budget) int32 out: the positions the
  *                  rows came from, ascending; 0 .. L-1 and then -1 for a
  *                  sequence left as it is.
+ *   max_context_len as pa_decode. It also chooses how many CTAs share the
+ *                  selection of a (sequence, kv head): without a bound close to
+ *                  the longest sequence, short ones under a wide block table
+ *                  are selected from by too many (twice the time of a call).
  *   new_lens       (batch) int32 out: min(L, budget). Not context_lens itself
  *                  (PA_ERR_SHAPE): the lengths are read by several CTAs.
  * Keys carry their rotation, and attention does not depend on the order of the
@@ -363,7 +371,8 @@ pa_status pa_decode_window_append(const void* q, const void* k_new, const void* 
  *   cu_seqlens_k    (batch+1) int32 on the device, prefix sums of kv_len.
  *   total_q         packed rows of q/out (host-side).
  *   max_q_len       host-side bound of every q_len (sizes the grid; <= 0 means
- *                   total_q). Rows past this bound are not computed.
+ *                   total_q). Of a sequence longer than the bound some rows are
+ *                   not computed.
  *   scale           softmax scale, > 0.
  *   out             (total_q, num_heads, head_dim) bf16.
  * A sequence with q_len > kv_len is invalid input: its cached length is taken
@@ -372,7 +381,9 @@ pa_status pa_decode_window_append(const void* q, const void* k_new, const void* 
  * Arithmetic: bf16 operands on the tensor cores, fp32 scores and
  * accumulation, probabilities rounded to bf16 for P.V (as two bf16 terms,
  * bf16(p) + bf16(p - bf16(p)), on the first 128 keys of the query tiles that
- * hold rows seeing fewer than 128 keys), bf16 output.
+ * hold rows seeing fewer than 128 keys), bf16 output. V of every key of a
+ * sequence must be finite: a row that does not see a key may give it the weight
+ * 0.
  */
 pa_status pa_prefill_varlen(const void* q, const pa_kv_cache* cache, const int32_t* block_tables,
                             int32_t max_blocks_per_seq, const int32_t* cu_seqlens_q,
@@ -387,7 +398,10 @@ pa_status pa_prefill_varlen(const void* q, const pa_kv_cache* cache, const int32
  *   window   >= 1 (PA_ERR_SHAPE otherwise); a window of kv_len keys or more is
  *            pa_prefill_varlen's mask.
  *   sinks    >= 0 (PA_ERR_SHAPE if negative).
- *   other arguments, support and arithmetic as pa_prefill_varlen, with P as two
+ *   max_q_len also chooses the kernel: with a bound of 128 / (heads a kv head)
+ *            tokens or fewer, both halves of a CTA share its one query tile.
+ *   other arguments, support (bf16 caches, head_dim 128; 8-bit caches return
+ *   PA_ERR_UNSUPPORTED) and arithmetic as pa_prefill_varlen, with P as two
  *   bf16 terms also on the first 128-key tile (the sinks') where sinks > 0, and
  *   on every tile where window + sinks < 128.
  * Blocks that hold no key visible to a 128-row query tile pair are not read, nor

@@ -455,7 +455,8 @@ def prefill_window(q, k_cache, v_cache, block_tables, cu_seqlens_q, cu_seqlens_k
                    window: int, sinks: int = 0, *, max_q_len: int = 0,
                    out=None) -> torch.Tensor:
     """pa_prefill_window: prefill_varlen where a query sees the last `window` (>= 1) keys up to
-    its own and the first `sinks` keys."""
+    its own and the first `sinks` keys. bf16 caches of head_dim 128. max_q_len (a bound of every
+    sequence's new tokens) lets short continuations take their own variant."""
     if q.dim() != 3:
         raise ValueError("q must be (total_q, num_heads, head_dim)")
     max_q_len, window, sinks = int(max_q_len), int(window), int(sinks)
@@ -498,8 +499,8 @@ def decode_scored(q, k_cache, v_cache, block_tables, context_lens, scores, scale
                   v_scale=None) -> torch.Tensor:
     """pa_decode_scored: decode, and every visible key's softmax weight, summed over the query
     heads of its kv head, added in place to scores (num_blocks, num_kv_heads, block_size) fp32.
-    A workspace (uint8 tensor of decode_scored_workspace_size bytes) is allocated when none is
-    given."""
+    A workspace (uint8 tensor of decode_scored_workspace_size bytes: four per query head and key
+    of the bound) is allocated in every call that gives none."""
     if q.dim() != 3:
         raise ValueError("q must be (batch, num_heads, head_dim)")
     max_context_len = int(max_context_len)
@@ -542,7 +543,8 @@ def evict(k_cache, v_cache, scores, block_tables, context_lens, budget: int, *, 
     """pa_evict: cut every sequence of more than `budget` keys to, per kv head, its first
     `sinks`, its last `recent` and the best scores between them, moved in order to the front of
     its blocks (K, V, scales and scores, in place). Returns (new_lens (B,) int32,
-    kept (B, Hkv, budget) int32: the positions the rows came from)."""
+    kept (B, Hkv, budget) int32: the positions the rows came from). Pass max_context_len where
+    the block table is much wider than the sequences: it sizes the selection."""
     budget, sinks, recent = int(budget), int(sinks), int(recent)
     max_context_len = int(max_context_len)
     if not 0 <= budget | sinks | recent | max_context_len <= 0x7fffffff:

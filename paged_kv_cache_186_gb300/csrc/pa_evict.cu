@@ -29,10 +29,13 @@
 //     in shared memory filled by 16-byte asynchronous copies, with the pool rows
 //     of source and destination in a second ring, looked up two tiles ahead by
 //     one thread per row.
-// On one GB300: 64 sequences of 2176 keys to 2048 (8 heads, E4M3) 13 us of
-// selection and 97 us of moving 536 MB (HBM-bound, 5.5 TB/s); 8 contexts of
-// 32768-131072 keys to 4096 (8 heads, bf16) 42 and 56 us, the selection bound by
-// the latency of its three passes over 4.4 M keys and of the cluster's barriers.
+// On one GB300, first calls on inputs that L2 does not hold (ncu, one pass): 64
+// sequences of 2176 keys to 2048 (8 heads, E4M3) 14 us of selection and 94 us of
+// moving 536 MB (HBM-bound, 5.7 TB/s); 8 contexts of 32768-131072 keys to 4096 (8
+// heads, bf16) 46 and 52 us, the selection bound by the latency of its three
+// passes over 4.4 M keys and of the cluster's barriers. 8 short segments 9 and 8
+// us: two launches, since a sequence's scores and scales and all columns of K and
+// V move in parallel CTAs, which can start only when its selection is complete.
 #include <algorithm>
 
 #include "pa_device.cuh"
@@ -527,16 +530,17 @@ __global__ void __launch_bounds__(kMvThreads) move_kernel(const EvictArgs a) {
 cudaError_t launch_evict(const EvictArgs& a, cudaStream_t stream) {
   const long long segs = static_cast<long long>(a.batch) * a.num_kv_heads;
   const long long parts = 2 * (a.row_bytes / 128) + 1;
-  // CTAs per (sequence, kv head): one per 8192 keys of the length bound. 8 long
-  // contexts (bound 131072) with 8 / 4 CTAs a head: 104 / 109 us a call (with 2 /
-  // 1, on an earlier form, 140 / 207); 64 sequences of 2176 keys with 1 / 2 CTAs,
-  // on that form, 118 / 136.
+  // CTAs per (sequence, kv head): one per 8192 keys of the length bound. Whole
+  // calls on restored inputs, CUDA events, one GB300: 8 long contexts (bound
+  // 131072) with 8 / 4 / 2 / 1 CTAs a head 100 / 104 / 129 / 195 us; 64 sequences
+  // of 2176 keys with 1 / 2 CTAs 106 / 119. The bound decides, the lengths are on
+  // the device: the same 64 sequences with a bound of 131072 take 221 us.
   int C = 1;
   while (C < kMaxCluster && (a.len_cap + C - 1) / C > 8192) C *= 2;
   if (segs * std::max<long long>(parts, C) > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   const int share = ((a.len_cap + C - 1) / C + 127) / 128 * 128;
   const int held = std::min(share, kMaxHeld);
-  // (the 8 long contexts with 256 threads a CTA: 120 us instead of 102)
+  // (the 8 long contexts with 256 threads a CTA: 117 us instead of 100)
   auto* const select = share <= 4096 ? select_kernel<256> : select_kernel<512>;
   static bool attr_set[64] = {};
   int dev = 0;

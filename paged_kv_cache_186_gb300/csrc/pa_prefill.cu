@@ -54,10 +54,15 @@
 //     all blocks are walked, and those without such a key are fetched out of
 //     bounds like those past the end (their table entries are not read). A row
 //     may see nothing of its first tiles: its maximum then stays -inf and its
-//     weights zero until it sees a key. One GB300, 8 sequences of the benchmark's
-//     lengths, window 1000 + 4 sinks: 105 us, 0.31 of the bf16 rate; 2 prompts of
-//     9001-16384 new tokens, window 4096: 3.64 ms, 0.53 of it (the chain S,
-//     softmax, P.V, next S of each key tile).
+//     weights zero until it sees a key. P is one bf16 term on most tiles, as
+//     without a window (its roundings, at most 2^-8 of a weight, average out over
+//     many keys; two terms on every tile cost a third of the time), and two where
+//     the weight lies on few keys: the sinks' tile, and every tile of a window
+//     below 128 keys. The sinks' second term: 105.1 -> 108.9 us and 3.63 -> 3.68
+//     ms below, 39.8 -> 41.1 on 32 short sequences. One GB300, 8 sequences of the
+//     benchmark's lengths, window 1000 + 4 sinks: 109 us, 0.30 of the bf16 rate; 2
+//     prompts of 9001-16384 new tokens, window 4096: 3.68 ms, 0.52 of it (the
+//     chain S, softmax, P.V, next S of each key tile).
 //   * TMEM: 512 columns (S0, S1, O0, O1, 128 each); shared memory: Q0, Q1,
 //     two K and two V stages (192 KB).
 #include <algorithm>

@@ -166,3 +166,53 @@ def test_lengths_written_right_before_a_store_and_a_decode():
         torch.cuda.synchronize()
         assert torch.equal(outs[s], ref), s
     assert pa.get_device_error() == 0
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+def test_blocks_far_into_a_large_pool(kv):
+    # offsets past 2^32 elements (bf16) or bytes (E4M3): the same calls give the same bits as
+    # over a pool that holds just the blocks in use
+    H, Hkv, D, bs, B, width = 32, 8, 128, 16, 3, 24
+    n = B * width
+    g = torch.Generator().manual_seed(402)
+    NB = (2 ** 32 // (Hkv * D * bs)) + 500
+    lens, budget, sinks, recent = [300, 150, 384], 100, 4, 30
+    T = sum(lens)
+    perm = torch.randperm(n, generator=g).view(B, width).to(torch.int32)
+    qkv = torch.randn((T, H + 2 * Hkv, D), generator=g).to(torch.bfloat16).cuda()
+    cs = torch.from_numpy(table(512, D)).cuda()
+    pos = torch.cat([torch.arange(m) for m in lens])
+    seq = torch.cat([torch.full((m,), b) for b, m in enumerate(lens)])
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32).cuda()
+    cl = torch.tensor(lens, dtype=torch.int32).cuda()
+    got = []
+    for blocks in (n, NB):
+        first = blocks - n
+        bt = perm + first
+        slots = (bt.long()[seq, pos // bs] * bs + pos % bs).cuda()
+        dt = torch.bfloat16 if kv == "bf16" else torch.uint8
+        kc, vc = (torch.empty((blocks, bs, Hkv, D), dtype=dt, device="cuda") for _ in range(2))
+        ks = vs = None
+        if kv != "bf16":
+            ks, vs = (torch.zeros((blocks, Hkv, bs), device="cuda") for _ in range(2))
+        scores = torch.zeros((blocks, Hkv, bs), device="cuda")
+        kc[first:] = 0
+        vc[first:] = 0
+        bt = bt.cuda()
+        q = pa.norm_rope_store(qkv[:, :H], qkv[:, H:H + Hkv], qkv[:, H + Hkv:], pos.cuda(), slots,
+                               kc, vc, cos_sin=cs, k_scale=ks, v_scale=vs, scores=scores)
+        res = [q]
+        if kv == "bf16":
+            res.append(pa.prefill_window(q, kc, vc, bt, cu, cu, 0.1, 64, 4))
+        res.append(pa.decode_scored(q[cu[1:].long() - 1], kc, vc, bt, cl, scores, 0.1, k_scale=ks,
+                                    v_scale=vs))
+        res += pa.evict(kc, vc, scores, bt, cl, budget, sinks=sinks, recent=recent, k_scale=ks,
+                        v_scale=vs)
+        res += [t[first:].clone() for t in (kc, vc, scores, ks, vs) if t is not None]
+        torch.cuda.synchronize()
+        assert pa.get_device_error() == 0
+        got.append(res)
+        del kc, vc, ks, vs, scores
+        torch.cuda.empty_cache()
+    for a, b in zip(*got):
+        assert torch.equal(a, b)

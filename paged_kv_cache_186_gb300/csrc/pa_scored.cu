@@ -14,8 +14,8 @@
 // (a common prefix) may add to them in one call; a slot of one sequence gets
 // one add per call. Bound by the reads of the scores, 4 bytes per key and query
 // head, and by memory as far as L2 does not hold them any more: on one GB300 (ncu,
-// one pass) 8 us for the 17 MB of batch 64 (contexts 512-4096, 32/8 heads; none
-// from memory), 15 us for 70 MB (8 contexts of 32768-131072; 11-14 MB from
+// one pass) 8-9 us for the 17 MB of batch 64 (contexts 512-4096, 32/8 heads; none
+// from memory), 15-17 us for 70 MB (8 contexts of 32768-131072; 11-15 MB from
 // memory), 23-24 us for 122 MB (E4M3, 64/8 heads; 72 MB from memory).
 #include <algorithm>
 

@@ -257,7 +257,9 @@ pa_status pa_decode_window(const void* q, const pa_kv_cache* cache, const int32_
  *             of sequences that share blocks sum over the sequences (in an order
  *             that may change from call to call). Slots at or past context_len
  *             are left as they were. pa_norm_rope_store can set a new slot's
- *             score to zero. After a launch that reported
+ *             score to zero. A query head whose scores hold a NaN or +infinity
+ *             (its out is NaN) adds NaN to those keys' scores and nothing to
+ *             the others'. After a launch that reported
  *             PA_DEVERR_WAIT_TIMEOUT they are as invalid as out.
  *   workspace at least pa_decode_scored_workspace_size() bytes (0: the shape is
  *             not supported), contract as for pa_decode. It holds the scores of

@@ -220,3 +220,27 @@ def test_workspace_and_batch_refusals():
     with pytest.raises(pa.PAError, match="UNSUPPORTED"):
         pa.decode_scored(q, kc, kc.clone(), bt, bt[:, 0].contiguous(),
                          torch.zeros((4, 1, 16), device="cuda"), 0.1)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_a_key_that_is_not_finite_spoils_its_own_score_only(bad):
+    # in a sequence that one warp holds and in one that is split over many
+    lens = [40, 5000, 700]
+    g, scores = inputs(3, 8, 2, 128, 16, lens, seed=240)
+    bt = g.block_tables.cpu().long()
+    before = scores.clone()
+    g.q.abs_()  # a key of +infinity in one dim scores +infinity, not NaN
+    clean = scores.clone()
+    ref = step(g, clean)
+    for b, p in ((0, 21), (1, 3333)):
+        g.k_cache[bt[b, p // 16], p % 16, 1, 5] = bad
+    out = step(g, scores)
+    assert torch.isnan(out[:2, 4:].float()).all()
+    assert torch.equal(out[:2, :4], ref[:2, :4]) and torch.equal(out[2], ref[2])
+    want = clean.clone()
+    for b, p in ((0, 21), (1, 3333)):
+        blocks = bt[b, :-(-lens[b] // 16)].cuda()
+        want[blocks, 1] = before[blocks, 1]
+        want[bt[b, p // 16], 1, p % 16] = float("nan")
+    assert torch.equal(torch.isnan(scores), torch.isnan(want))
+    assert torch.equal(scores.nan_to_num(-1.0), want.nan_to_num(-1.0))

@@ -31,6 +31,14 @@
  *                      a score kept beside the cache.
  *   pa_evict           cut sequences to a budget of keys by those scores and
  *                      move the kept rows to the front.
+ * And for many requests over one shared context (system prompts, samples of one
+ * prompt, questions about one document or video), whose blocks are in the cache
+ * once (the pages' prefix caching) and begin every such sequence's block table:
+ *   pa_norm_rope_axes_store  pa_norm_rope_store with a position on each of up to
+ *                      four axes (time, height, width).
+ *   pa_decode_shared   pa_decode that attends to the shared keys once for all
+ *                      sequences of a group.
+ *   pa_prefill_shared  pa_prefill_varlen, likewise.
  *
  * Conventions shared by every call
  *   - Every tensor pointer is a DEVICE pointer owned by the caller. The
@@ -98,7 +106,8 @@ typedef enum { PA_KV_BF16 = 0, PA_KV_FP8_E4M3 = 1, PA_KV_INT8 = 2 } pa_kv_dtype;
 #define PA_DEVERR_SLOT_RANGE 0x1u   /* store_kv: slot >= num_blocks*block_size, skipped */
 #define PA_DEVERR_WAIT_TIMEOUT 0x2u /* a kernel's bounded wait on a copy gave up */
 #define PA_DEVERR_BLOCK_RANGE 0x4u  /* block table entry outside [0, num_blocks), zero-filled */
-#define PA_DEVERR_POSITION_RANGE 0x8u /* norm_rope_store: position outside the table, skipped */
+#define PA_DEVERR_POSITION_RANGE 0x8u /* norm_rope_store, norm_rope_axes_store: position outside
+                                         the table, token skipped */
 
 /* A paged KV cache (one layer). Pointers are device pointers; the struct
  * itself is read on the host during the call and may live on the stack. */
@@ -184,6 +193,27 @@ pa_status pa_norm_rope_store(const void* q, int64_t q_stride, const void* k, int
                              const int64_t* positions, const int64_t* slot_mapping,
                              int32_t num_tokens, int32_t num_heads, const pa_kv_cache* cache,
                              float* scores, void* q_out, void* stream);
+
+/*
+ * pa_norm_rope_axes_store - pa_norm_rope_store for tokens with a position on each
+ * of several axes (an image's height and width, a video's time too): the rotated
+ * pair i takes its cosine and sine from column i of the table's row
+ * positions[pair_axis[i]][t]. Frequencies are the table's, so every axis may have
+ * its own.
+ *   positions   (num_axes, num_tokens) int64. A token with any position outside
+ *               [0, max_positions) is skipped (PA_DEVERR_POSITION_RANGE).
+ *   num_axes    1 .. 4 (PA_ERR_SHAPE below, PA_ERR_UNSUPPORTED above).
+ *   pair_axis   HOST array of rotary_dim/2 bytes, read during the call: the axis
+ *               of each pair, below num_axes (PA_ERR_SHAPE).
+ *   params      rotary_dim > 0 (PA_ERR_SHAPE); otherwise and all other arguments as
+ *               pa_norm_rope_store. One axis is pa_norm_rope_store bit for bit.
+ */
+pa_status pa_norm_rope_axes_store(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                  const void* v, int64_t v_stride, const pa_norm_rope* params,
+                                  const int64_t* positions, int32_t num_axes,
+                                  const uint8_t* pair_axis, const int64_t* slot_mapping,
+                                  int32_t num_tokens, int32_t num_heads, const pa_kv_cache* cache,
+                                  float* scores, void* q_out, void* stream);
 
 /*
  * pa_decode_workspace_size - bytes of device scratch pa_decode needs for this
@@ -277,6 +307,40 @@ pa_status pa_decode_scored(const void* q, const pa_kv_cache* cache, const int32_
                            int32_t max_context_len, int32_t batch, int32_t num_heads, float scale,
                            float* scores, void* out, void* workspace, size_t workspace_bytes,
                            void* stream);
+
+/*
+ * pa_decode_shared - pa_decode of a batch in which groups of sequences share
+ * their first keys: what pa_decode returns for the same arguments (within
+ * rounding), with the shared keys read and attended to once for a whole group.
+ *   cu_groups    (num_groups+1) int32 on the device, ascending, within [0, batch]:
+ *                group g is the sequences cu_groups[g] .. cu_groups[g+1]-1. The
+ *                others share nothing. Entries that do not ascend or lie outside
+ *                are taken as the nearest that do.
+ *   prefix_lens  (num_groups) int32 on the device: the group's sequences share
+ *                their first prefix_lens[g] keys. Whole blocks are shared: the
+ *                first prefix_lens[g] / block_size entries of the block table rows
+ *                of a group must agree (as far as a sequence's context_len
+ *                reaches); they are read from one of the rows. Sequences shorter
+ *                than the prefix attend to their context_len keys; if all of a
+ *                group are shorter, nothing is shared. A padding sequence
+ *                (context_len 0) may stand in any group, its row of the table may
+ *                hold anything.
+ *   num_groups   >= 0; 0: nothing is shared, cu_groups and prefix_lens may be NULL.
+ *   workspace    at least pa_decode_shared_workspace_size() bytes (0: the shape is
+ *                not supported), contract as for pa_decode.
+ *   other arguments as pa_decode. Batches and num_groups above 16384 return
+ *   PA_ERR_UNSUPPORTED. K and V of shared keys past the context_len of a shorter
+ *   sequence of the group must be finite: it gives them the weight 0.
+ */
+size_t pa_decode_shared_workspace_size(const pa_kv_cache* cache, int32_t batch, int32_t num_heads,
+                                       int32_t max_blocks_per_seq, int32_t num_groups,
+                                       int32_t max_context_len);
+pa_status pa_decode_shared(const void* q, const pa_kv_cache* cache, const int32_t* block_tables,
+                           int32_t max_blocks_per_seq, const int32_t* context_lens,
+                           int32_t max_context_len, const int32_t* cu_groups,
+                           const int32_t* prefix_lens, int32_t num_groups, int32_t batch,
+                           int32_t num_heads, float scale, void* out, void* workspace,
+                           size_t workspace_bytes, void* stream);
 
 /*
  * pa_evict - cut sequences to `budget` keys per kv head. For a sequence of
@@ -417,6 +481,30 @@ pa_status pa_prefill_window(const void* q, const pa_kv_cache* cache, const int32
                             const int32_t* cu_seqlens_k, int32_t batch, int32_t num_heads,
                             int32_t total_q, int32_t max_q_len, float scale, int32_t window,
                             int32_t sinks, void* out, void* stream);
+
+/*
+ * pa_prefill_shared - pa_prefill_varlen of sequences that share their first keys
+ * in groups: questions over one document, drafts to verify behind one prompt.
+ *   cu_groups, prefix_lens, num_groups  as pa_decode_shared (a sequence's length
+ *                being its kv_len): the block tables of a group begin with the same
+ *                blocks. New tokens may lie within the prefix; they see the keys up
+ *                to their own.
+ *   workspace    at least pa_prefill_shared_workspace_size() bytes (0: the shape is
+ *                not supported): about 8 * head_dim bytes per query row. Contents on
+ *                entry are ignored; calls sharing one workspace must not overlap.
+ *   other arguments, support (bf16 caches, head_dim 128) and arithmetic as
+ *   pa_prefill_varlen. Batches and num_groups above 16384 return
+ *   PA_ERR_UNSUPPORTED. max_q_len also chooses the kernel of a sequence's own keys,
+ *   as for pa_prefill_window.
+ */
+size_t pa_prefill_shared_workspace_size(const pa_kv_cache* cache, int32_t num_heads,
+                                        int32_t total_q, int32_t num_groups);
+pa_status pa_prefill_shared(const void* q, const pa_kv_cache* cache, const int32_t* block_tables,
+                            int32_t max_blocks_per_seq, const int32_t* cu_seqlens_q,
+                            const int32_t* cu_seqlens_k, const int32_t* cu_groups,
+                            const int32_t* prefix_lens, int32_t num_groups, int32_t batch,
+                            int32_t num_heads, int32_t total_q, int32_t max_q_len, float scale,
+                            void* out, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
  * pa_decode_noalloc - pa_decode for callers that cannot allocate device memory.

@@ -10,7 +10,9 @@ Names follow the C ABI: store_kv, decode, decode_window, decode_append,
 decode_workspace_size, prefill_varlen, decode_noalloc, get_device_error,
 debug_inject_wait_timeout; for a decode loop over a bounded cache:
 norm_rope_store, prefill_window, decode_scored, decode_scored_workspace_size,
-evict.
+evict; for many requests over one shared context: norm_rope_axes_store,
+decode_shared, decode_shared_workspace_size, prefill_shared,
+prefill_shared_workspace_size.
 """
 from __future__ import annotations
 
@@ -42,7 +44,9 @@ DECODE_NOALLOC_SCRATCH_BYTES = 32 << 20
 EXPORTED = ("pa_abi_version", "pa_status_string", "pa_store_kv", "pa_decode_workspace_size",
             "pa_decode", "pa_decode_window", "pa_decode_append", "pa_decode_window_append",
             "pa_prefill_varlen", "pa_norm_rope_store", "pa_prefill_window", "pa_decode_scored",
-            "pa_decode_scored_workspace_size", "pa_evict",
+            "pa_decode_scored_workspace_size", "pa_evict", "pa_norm_rope_axes_store",
+            "pa_decode_shared", "pa_decode_shared_workspace_size", "pa_prefill_shared",
+            "pa_prefill_shared_workspace_size",
             "pa_decode_noalloc", "pa_get_device_error", "pa_debug_inject_wait_timeout")
 
 
@@ -127,6 +131,19 @@ def lib() -> ctypes.CDLL:
                                    ctypes.c_size_t, P]
     L.pa_evict.restype = ctypes.c_int
     L.pa_evict.argtypes = [cache, P, P, i32, P, i32, i32, i32, i32, i32, P, P, P]
+    L.pa_norm_rope_axes_store.restype = ctypes.c_int
+    L.pa_norm_rope_axes_store.argtypes = [P, i64, P, i64, P, i64, ctypes.POINTER(NormRope), P, i32,
+                                          ctypes.c_char_p, P, i32, i32, cache, P, P, P]
+    L.pa_decode_shared_workspace_size.restype = ctypes.c_size_t
+    L.pa_decode_shared_workspace_size.argtypes = [cache, i32, i32, i32, i32, i32]
+    L.pa_decode_shared.restype = ctypes.c_int
+    L.pa_decode_shared.argtypes = [P, cache, P, i32, P, i32, P, P, i32, i32, i32, ctypes.c_float,
+                                   P, P, ctypes.c_size_t, P]
+    L.pa_prefill_shared_workspace_size.restype = ctypes.c_size_t
+    L.pa_prefill_shared_workspace_size.argtypes = [cache, i32, i32, i32]
+    L.pa_prefill_shared.restype = ctypes.c_int
+    L.pa_prefill_shared.argtypes = [P, cache, P, i32, P, P, P, P, i32, i32, i32, i32, i32,
+                                    ctypes.c_float, P, P, ctypes.c_size_t, P]
     _lib = L
     return L
 
@@ -413,6 +430,31 @@ def norm_rope_store(q, k, v, positions, slot_mapping, k_cache, v_cache, *, q_wei
     for an 8-bit cache. Returns q_out (T, H, D) bf16 (rows of padding tokens are not written);
     it may be q itself if q is contiguous. q, k and v may be views of one fused projection's
     output. scores: set the slots' scores (decode_scored) to 0."""
+    return _norm_rope(q, k, v, positions, slot_mapping, k_cache, v_cache, None, q_weight, k_weight,
+                      eps, cos_sin, interleaved, q_out, k_scale, v_scale, scores)
+
+
+def norm_rope_axes_store(q, k, v, positions, slot_mapping, k_cache, v_cache, pair_axis, cos_sin, *,
+                         q_weight=None, k_weight=None, eps: float = 1e-6,
+                         interleaved: bool = False, q_out=None, k_scale=None, v_scale=None,
+                         scores=None) -> torch.Tensor:
+    """pa_norm_rope_axes_store: norm_rope_store for tokens with a position on each of one to four
+    axes (time, height, width): positions is (axes, T) int64, and pair i of the rotated dims takes
+    column i of the table's row positions[pair_axis[i]]. pair_axis: the axis of each of the
+    rotary_dim / 2 pairs, as bytes (quickest) or integers, e.g. [0] * 16 + [1] * 24 + [2] * 24."""
+    if cos_sin is None or positions is None:
+        raise ValueError("norm_rope_axes_store needs cos_sin and positions")
+    if positions.dim() != 2:
+        raise ValueError("positions must be (axes, tokens)")
+    if not isinstance(pair_axis, bytes):
+        pair_axis = bytes(pair_axis)  # refuses what is not 0 .. 255
+    return _norm_rope(q, k, v, positions, slot_mapping, k_cache, v_cache, pair_axis, q_weight,
+                      k_weight, eps, cos_sin, interleaved, q_out, k_scale, v_scale, scores)
+
+
+def _norm_rope(q, k, v, positions, slot_mapping, k_cache, v_cache, pair_axis, q_weight, k_weight,
+               eps, cos_sin, interleaved, q_out, k_scale, v_scale, scores) -> torch.Tensor:
+    """The body of norm_rope_store (pair_axis None) and norm_rope_axes_store."""
     dev = k_cache.get_device()
     NB, bs, Hkv, D = k_cache.shape
     if q.dim() != 3:
@@ -431,9 +473,12 @@ def norm_rope_store(q, k, v, positions, slot_mapping, k_cache, v_cache, *, q_wei
         cp = _state(cos_sin, "cos_sin", torch.float32, (rows, rot), dev).data_ptr()
         if positions is None:
             raise ValueError("a rotation needs positions")
+    axes = () if pair_axis is None else (positions.shape[0],)
     if positions is not None:
-        positions = _input(positions, "positions", torch.int64, (T,), dev)
+        positions = _input(positions, "positions", torch.int64, axes + (T,), dev)
         pp = positions.data_ptr()
+    if pair_axis is not None and len(pair_axis) != rot // 2:
+        raise ValueError(f"pair_axis must name {rot // 2} axes, one per pair, got {len(pair_axis)}")
     if q_weight is not None:
         qw = _state(q_weight, "q_weight", torch.bfloat16, (D,), dev).data_ptr()
     if k_weight is not None:
@@ -445,9 +490,15 @@ def norm_rope_store(q, k, v, positions, slot_mapping, k_cache, v_cache, *, q_wei
     else:
         _state(q_out, "q_out", torch.bfloat16, (T, H, D), dev)
     cache = _cache_of(k_cache, v_cache, k_scale, v_scale, dev)
-    _run(dev, "pa_norm_rope_store", (_lib or lib()).pa_norm_rope_store, qp, qs, kp, ks, vp, vs,
-         ctypes.byref(NormRope(qw, kw, cp, rows, rot, 1 if interleaved else 0, eps)), pp,
-         slot_mapping.data_ptr(), T, H, ctypes.byref(cache), sp, q_out.data_ptr())
+    params = NormRope(qw, kw, cp, rows, rot, 1 if interleaved else 0, eps)
+    if pair_axis is None:
+        _run(dev, "pa_norm_rope_store", (_lib or lib()).pa_norm_rope_store, qp, qs, kp, ks, vp, vs,
+             ctypes.byref(params), pp, slot_mapping.data_ptr(), T, H, ctypes.byref(cache), sp,
+             q_out.data_ptr())
+    else:
+        _run(dev, "pa_norm_rope_axes_store", (_lib or lib()).pa_norm_rope_axes_store, qp, qs, kp,
+             ks, vp, vs, ctypes.byref(params), pp, axes[0], pair_axis, slot_mapping.data_ptr(), T,
+             H, ctypes.byref(cache), sp, q_out.data_ptr())
     return q_out
 
 
@@ -534,6 +585,121 @@ def decode_scored(q, k_cache, v_cache, block_tables, context_lens, scores, scale
     _run(dev, "pa_decode_scored", (_lib or lib()).pa_decode_scored, q.data_ptr(),
          ctypes.byref(cache), bt.data_ptr(), width, cl.data_ptr(), max_context_len, B, H,
          scale, scores.data_ptr(), out.data_ptr(), ws or None, ws_bytes)
+    return out
+
+
+def _groups(cu_groups, prefix_lens, dev: int):
+    """(cu_groups, prefix_lens, number of groups), checked."""
+    n = prefix_lens.numel()
+    return (_input(cu_groups, "cu_groups", torch.int32, (n + 1,), dev),
+            _input(prefix_lens, "prefix_lens", torch.int32, (n,), dev), n)
+
+
+def decode_shared_workspace_size(k_cache, batch: int, num_heads: int, max_blocks_per_seq: int,
+                                 num_groups: int, max_context_len: int = 0, v_cache=None,
+                                 k_scale=None, v_scale=None) -> int:
+    """Bytes of the workspace of decode_shared (0: the shape is not supported)."""
+    _check_i32(batch=batch, num_heads=num_heads, max_blocks_per_seq=max_blocks_per_seq,
+               num_groups=num_groups, max_context_len=max_context_len)
+    cache = make_cache(k_cache, k_cache if v_cache is None else v_cache, k_scale, v_scale)
+    return int(lib().pa_decode_shared_workspace_size(ctypes.byref(cache), batch, num_heads,
+                                                     max_blocks_per_seq, num_groups,
+                                                     max_context_len))
+
+
+def decode_shared(q, k_cache, v_cache, block_tables, context_lens, cu_groups, prefix_lens,
+                  scale: float, *, max_context_len: int = 0, out=None, workspace=None,
+                  k_scale=None, v_scale=None) -> torch.Tensor:
+    """pa_decode_shared: decode where the sequences cu_groups[g] .. cu_groups[g+1]-1 (int32
+    (groups + 1,)) share their first prefix_lens[g] keys (int32 (groups,)): their block table rows
+    begin with the same prefix_lens[g] // block_size blocks, which are read and attended to once
+    for the whole group. A workspace (uint8 tensor of decode_shared_workspace_size bytes) is
+    allocated in every call that gives none."""
+    if q.dim() != 3:
+        raise ValueError("q must be (batch, num_heads, head_dim)")
+    max_context_len = int(max_context_len)
+    if not 0 <= max_context_len <= 0x7fffffff:
+        _check_i32(max_context_len=max_context_len)
+    dev = k_cache.get_device()
+    B, H, D = q.shape
+    if block_tables.dim() != 2:
+        raise ValueError("block_tables must be (batch, blocks)")
+    width = block_tables.shape[1]
+    q = _input(q, "q", torch.bfloat16, (B, H, k_cache.shape[3]), dev)
+    cl = _input(context_lens, "context_lens", torch.int32, (B,), dev)
+    bt = _input(block_tables, "block_tables", torch.int32, (B, width), dev)
+    cg, pl, n = _groups(cu_groups, prefix_lens, dev)
+    if out is None:
+        out = torch.empty((B, H, D), dtype=torch.bfloat16, device=q.device)
+    else:
+        _state(out, "out", torch.bfloat16, (B, H, D), dev)
+    cache = _cache_of(k_cache, v_cache, k_scale, v_scale, dev)
+    ws = ws_bytes = 0
+    if workspace is None:  # a caller-provided workspace is checked by the library
+        need = decode_shared_workspace_size(k_cache, B, H, width, n, max_context_len, v_cache,
+                                            k_scale, v_scale)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    elif not workspace.is_contiguous() or workspace.get_device() != dev:
+        raise ValueError("workspace must be contiguous and on the caches' device")
+    if workspace is not None:
+        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _run(dev, "pa_decode_shared", (_lib or lib()).pa_decode_shared, q.data_ptr(),
+         ctypes.byref(cache), bt.data_ptr(), width, cl.data_ptr(), max_context_len, cg.data_ptr(),
+         pl.data_ptr(), n, B, H, scale, out.data_ptr(), ws or None, ws_bytes)
+    return out
+
+
+def prefill_shared_workspace_size(k_cache, total_q: int, num_heads: int, num_groups: int) -> int:
+    """Bytes of the workspace of prefill_shared (0: the shape is not supported)."""
+    _check_i32(total_q=total_q, num_heads=num_heads, num_groups=num_groups)
+    cache = make_cache(k_cache, k_cache)
+    return int(lib().pa_prefill_shared_workspace_size(ctypes.byref(cache), num_heads, total_q,
+                                                      num_groups))
+
+
+def prefill_shared(q, k_cache, v_cache, block_tables, cu_seqlens_q, cu_seqlens_k, cu_groups,
+                   prefix_lens, scale: float, *, max_q_len: int = 0, out=None,
+                   workspace=None) -> torch.Tensor:
+    """pa_prefill_shared: prefill_varlen of sequences that share their first keys in groups
+    (cu_groups, prefix_lens: as decode_shared). bf16 caches of head_dim 128. max_q_len (a bound of
+    every sequence's new tokens) sizes the grid and lets short questions take their own variant. A
+    workspace (uint8 tensor of prefill_shared_workspace_size bytes, about 8 * head_dim per query
+    row) is allocated in every call that gives none."""
+    if q.dim() != 3:
+        raise ValueError("q must be (total_q, num_heads, head_dim)")
+    max_q_len = int(max_q_len)
+    if not 0 <= max_q_len <= 0x7fffffff:
+        _check_i32(max_q_len=max_q_len)
+    dev = k_cache.get_device()
+    T, H, D = q.shape
+    n = cu_seqlens_q.numel()
+    if n < 1 or block_tables.dim() != 2:
+        raise ValueError("block_tables must be (batch, blocks), cu_seqlens (batch + 1,)")
+    width = block_tables.shape[1]
+    q = _input(q, "q", torch.bfloat16, (T, H, k_cache.shape[3]), dev)
+    cu_q = _input(cu_seqlens_q, "cu_seqlens_q", torch.int32, (n,), dev)
+    cu_k = _input(cu_seqlens_k, "cu_seqlens_k", torch.int32, (n,), dev)
+    bt = _input(block_tables, "block_tables", torch.int32, (n - 1, width), dev)
+    cg, pl, groups = _groups(cu_groups, prefix_lens, dev)
+    if out is None:
+        out = torch.empty((T, H, D), dtype=torch.bfloat16, device=q.device)
+    else:
+        _state(out, "out", torch.bfloat16, (T, H, D), dev)
+    cache = _cache_of(k_cache, v_cache, None, None, dev)
+    ws = ws_bytes = 0
+    if workspace is None:  # a caller-provided workspace is checked by the library
+        need = prefill_shared_workspace_size(k_cache, T, H, groups)
+        if need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    elif not workspace.is_contiguous() or workspace.get_device() != dev:
+        raise ValueError("workspace must be contiguous and on the caches' device")
+    if workspace is not None:
+        ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    _run(dev, "pa_prefill_shared", (_lib or lib()).pa_prefill_shared, q.data_ptr(),
+         ctypes.byref(cache), bt.data_ptr(), width, cu_q.data_ptr(), cu_k.data_ptr(),
+         cg.data_ptr(), pl.data_ptr(), groups, n - 1, H, T, max_q_len, scale, out.data_ptr(),
+         ws or None, ws_bytes)
     return out
 
 

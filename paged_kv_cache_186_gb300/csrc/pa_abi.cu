@@ -257,11 +257,17 @@ pa_status pa_store_kv(const void* k, const void* v, const float* k_scale_new,
                                                                                   : PA_ERR_CUDA;
 }
 
-pa_status pa_norm_rope_store(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
-                             const void* v, int64_t v_stride, const pa_norm_rope* params,
-                             const int64_t* positions, const int64_t* slot_mapping,
-                             int32_t num_tokens, int32_t num_heads, const pa_kv_cache* cache,
-                             float* scores, void* q_out, void* stream) {
+}  // extern "C"
+
+namespace {
+
+// Shared body of pa_norm_rope_store (num_axes 0) and pa_norm_rope_axes_store.
+pa_status norm_rope_common(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                           const void* v, int64_t v_stride, const pa_norm_rope* params,
+                           const int64_t* positions, const int64_t* slot_mapping,
+                           int32_t num_tokens, int32_t num_heads, const pa_kv_cache* cache,
+                           float* scores, void* q_out, void* stream, int32_t num_axes = 0,
+                           const uint8_t* pair_axis = nullptr) {
   pa_status st = check_cache(cache);
   if (st != PA_OK) return st;
   if (params == nullptr) return PA_ERR_NULL;
@@ -317,9 +323,46 @@ pa_status pa_norm_rope_store(const void* q, int64_t q_stride, const void* k, int
   a.kv = static_cast<int>(cache->dtype);
   a.eps = params->eps;
   a.num_sms = dev->num_sms;
+  a.num_axes = num_axes;
+  if (num_axes > 0) {
+    uint32_t w[4] = {0u, 0u, 0u, 0u};
+    for (int i = 0; i < rot / 2; ++i) w[i / 16] |= static_cast<uint32_t>(pair_axis[i]) << (2 * (i % 16));
+    a.pair_axis = make_uint4(w[0], w[1], w[2], w[3]);
+  }
   return pa::launch_norm_rope_store(a, static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? PA_OK
              : PA_ERR_CUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+pa_status pa_norm_rope_store(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                             const void* v, int64_t v_stride, const pa_norm_rope* params,
+                             const int64_t* positions, const int64_t* slot_mapping,
+                             int32_t num_tokens, int32_t num_heads, const pa_kv_cache* cache,
+                             float* scores, void* q_out, void* stream) {
+  return norm_rope_common(q, q_stride, k, k_stride, v, v_stride, params, positions, slot_mapping,
+                          num_tokens, num_heads, cache, scores, q_out, stream);
+}
+
+pa_status pa_norm_rope_axes_store(const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                                  const void* v, int64_t v_stride, const pa_norm_rope* params,
+                                  const int64_t* positions, int32_t num_axes,
+                                  const uint8_t* pair_axis, const int64_t* slot_mapping,
+                                  int32_t num_tokens, int32_t num_heads, const pa_kv_cache* cache,
+                                  float* scores, void* q_out, void* stream) {
+  const pa_status st = check_cache(cache);
+  if (st != PA_OK) return st;
+  if (params == nullptr || pair_axis == nullptr) return PA_ERR_NULL;
+  if (num_axes < 1 || params->rotary_dim <= 0 || params->rotary_dim > cache->head_dim)
+    return PA_ERR_SHAPE;
+  if (num_axes > 4) return PA_ERR_UNSUPPORTED;
+  for (int i = 0; i < params->rotary_dim / 2; ++i)
+    if (pair_axis[i] >= num_axes) return PA_ERR_SHAPE;
+  return norm_rope_common(q, q_stride, k, k_stride, v, v_stride, params, positions, slot_mapping,
+                          num_tokens, num_heads, cache, scores, q_out, stream, num_axes, pair_axis);
 }
 
 size_t pa_decode_workspace_size(const pa_kv_cache* cache, int32_t batch, int32_t num_heads,
@@ -601,12 +644,23 @@ pa_status pa_decode_window_append(const void* q, const void* k_new, const void* 
 
 namespace {
 
-// Shared body of pa_prefill_varlen (window 0) and pa_prefill_window.
+// The groups and the workspace of a call over shared context.
+struct SharedCall {
+  const int32_t* cu_groups;
+  const int32_t* prefix_lens;
+  int32_t num_groups;
+  void* workspace;
+  size_t workspace_bytes;
+};
+
+// Shared body of pa_prefill_varlen (window 0), pa_prefill_window and
+// pa_prefill_shared.
 pa_status prefill_common(const void* q, const pa_kv_cache* cache, const int32_t* block_tables,
                          int32_t max_blocks_per_seq, const int32_t* cu_seqlens_q,
                          const int32_t* cu_seqlens_k, int32_t batch, int32_t num_heads,
                          int32_t total_q, int32_t max_q_len, float scale, int32_t window,
-                         int32_t sinks, void* out, void* stream) {
+                         int32_t sinks, void* out, void* stream,
+                         const SharedCall* shared = nullptr) {
   pa_status st = check_cache(cache);
   if (st != PA_OK) return st;
   if (batch < 0 || num_heads <= 0 || total_q < 0 || max_blocks_per_seq <= 0) return PA_ERR_SHAPE;
@@ -629,6 +683,13 @@ pa_status prefill_common(const void* q, const pa_kv_cache* cache, const int32_t*
   const int qbound = max_q_len > 0 ? std::min(max_q_len, total_q) : total_q;
   // the grid's z extent is the number of query-tile pairs of the longest sequence
   if ((static_cast<long long>(qbound) + 2 * tpt - 1) / (2 * tpt) > 65535) return PA_ERR_UNSUPPORTED;
+  if (shared != nullptr) {
+    const size_t need =
+        pa_prefill_shared_workspace_size(cache, num_heads, total_q, shared->num_groups);
+    if (shared->workspace == nullptr || shared->workspace_bytes < need ||
+        !aligned16(shared->workspace))
+      return PA_ERR_WORKSPACE;
+  }
   // Q viewed as (head_dim, num_heads, total_q); one box = the G heads of a kv
   // head for tpt consecutive tokens, 64 dims (128 bytes) wide.
   CUtensorMap qmap, kmap, vmap;
@@ -694,6 +755,58 @@ pa_status pa_prefill_window(const void* q, const pa_kv_cache* cache, const int32
   if (window < 1 || sinks < 0) return PA_ERR_SHAPE;
   return prefill_common(q, cache, block_tables, max_blocks_per_seq, cu_seqlens_q, cu_seqlens_k,
                         batch, num_heads, total_q, max_q_len, scale, window, sinks, out, stream);
+}
+
+size_t pa_decode_shared_workspace_size(const pa_kv_cache* cache, int32_t batch, int32_t num_heads,
+                                       int32_t max_blocks_per_seq, int32_t num_groups,
+                                       int32_t max_context_len) {
+  if (num_groups < 0 || num_groups > pa::kMaxPersistentBatch || batch > pa::kMaxPersistentBatch)
+    return 0;
+  return pa_decode_workspace_size(cache, batch, num_heads, max_blocks_per_seq, max_context_len);
+}
+
+pa_status pa_decode_shared(const void* q, const pa_kv_cache* cache, const int32_t* block_tables,
+                           int32_t max_blocks_per_seq, const int32_t* context_lens,
+                           int32_t max_context_len, const int32_t* cu_groups,
+                           const int32_t* prefix_lens, int32_t num_groups, int32_t batch,
+                           int32_t num_heads, float scale, void* out, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+  const pa_status st = check_cache(cache);
+  if (st != PA_OK) return st;
+  if (num_groups < 0) return PA_ERR_SHAPE;
+  if (batch > 0 && num_groups > 0 && (cu_groups == nullptr || prefix_lens == nullptr))
+    return PA_ERR_NULL;
+  if (batch > pa::kMaxPersistentBatch || num_groups > pa::kMaxPersistentBatch)
+    return PA_ERR_UNSUPPORTED;
+  return decode_common(q, cache, block_tables, max_blocks_per_seq, context_lens, max_context_len,
+                       batch, num_heads, scale, out, workspace, workspace_bytes, stream, nullptr,
+                       nullptr, nullptr, nullptr, 0, 0);
+}
+
+size_t pa_prefill_shared_workspace_size(const pa_kv_cache* cache, int32_t num_heads,
+                                        int32_t total_q, int32_t num_groups) {
+  return check_cache(cache) == PA_OK && num_heads > 0 && total_q > 0 && num_groups >= 0 &&
+                 num_groups <= pa::kMaxPersistentBatch
+             ? 16
+             : 0;
+}
+
+pa_status pa_prefill_shared(const void* q, const pa_kv_cache* cache, const int32_t* block_tables,
+                            int32_t max_blocks_per_seq, const int32_t* cu_seqlens_q,
+                            const int32_t* cu_seqlens_k, const int32_t* cu_groups,
+                            const int32_t* prefix_lens, int32_t num_groups, int32_t batch,
+                            int32_t num_heads, int32_t total_q, int32_t max_q_len, float scale,
+                            void* out, void* workspace, size_t workspace_bytes, void* stream) {
+  const pa_status st = check_cache(cache);
+  if (st != PA_OK) return st;
+  if (num_groups < 0) return PA_ERR_SHAPE;
+  if (batch > 0 && num_groups > 0 && (cu_groups == nullptr || prefix_lens == nullptr))
+    return PA_ERR_NULL;
+  if (batch > pa::kMaxPersistentBatch || num_groups > pa::kMaxPersistentBatch)
+    return PA_ERR_UNSUPPORTED;
+  const SharedCall shared{cu_groups, prefix_lens, num_groups, workspace, workspace_bytes};
+  return prefill_common(q, cache, block_tables, max_blocks_per_seq, cu_seqlens_q, cu_seqlens_k,
+                        batch, num_heads, total_q, max_q_len, scale, 0, 0, out, stream, &shared);
 }
 
 pa_status pa_debug_inject_wait_timeout(int32_t skip_copy, uint64_t wait_limit_ns) {

@@ -9,6 +9,9 @@
 // dims (i, i + rotary_dim/2) or (2i, 2i+1). q rows go to q_out (one rounding to
 // bf16), k and v rows to the cache: bf16, or 8-bit codes c = round(x / sc) with
 // sc = max|x| / 448 (E4M3) or / 127 (INT8) taken from the unrounded row.
+// norm_rope_axes_store (AXES): a token has a position on each of up to four axes
+// (time, height, width of an image or a video), and pair i takes its row of the
+// table from the position on its own axis, positions[pair_axis[i]][t].
 //
 // How: a row of head_dim elements belongs to head_dim/8 lanes with one 16-byte
 // chunk each, so every load and store is a 16-byte vector and a warp holds 2
@@ -89,7 +92,7 @@ __device__ __forceinline__ uint2 codes8(const float (&x)[8]) {
 // One warp: rows_per_warp rows of one kind of one token, in batches of NIT
 // rounds of 256/D rows; a batch's rows are read while the one before is worked
 // on.
-template <int D, int KV, bool INTER, int NIT>
+template <int D, int KV, bool INTER, int NIT, bool AXES>
 __global__ void __launch_bounds__(kNrWarps * 32, NIT == 2 ? 8 : 1)
     norm_rope_kernel(const NormRopeArgs a) {
   constexpr int LPR = D / 8;     // lanes per row
@@ -131,8 +134,20 @@ __global__ void __launch_bounds__(kNrWarps * 32, NIT == 2 ? 8 : 1)
   const long long slot = a.slot_mapping[t];
   if (slot < 0) return;  // padding token
   const int rot = a.rotary_dim;
-  long long pos = 0;
-  if (rot > 0) {
+  long long pos = 0, pos1 = 0, pos2 = 0, pos3 = 0;  // the last three: AXES
+  if (AXES && rot > 0) {
+    const long long T = a.num_tokens;
+    pos = a.positions[t];
+    pos1 = a.num_axes > 1 ? a.positions[T + t] : 0;
+    pos2 = a.num_axes > 2 ? a.positions[2 * T + t] : 0;
+    pos3 = a.num_axes > 3 ? a.positions[3 * T + t] : 0;
+    const unsigned long long top = a.max_positions;  // (a negative one is far above it)
+    if (static_cast<unsigned long long>(pos) >= top || static_cast<unsigned long long>(pos1) >= top ||
+        static_cast<unsigned long long>(pos2) >= top || static_cast<unsigned long long>(pos3) >= top) {
+      if (lane == 0) report_error(a.err, PA_DEVERR_POSITION_RANGE);
+      return;
+    }
+  } else if (rot > 0) {
     pos = a.positions[t];
     if (pos < 0 || pos >= a.max_positions) {
       if (lane == 0) report_error(a.err, PA_DEVERR_POSITION_RANGE);
@@ -161,12 +176,44 @@ __global__ void __launch_bounds__(kNrWarps * 32, NIT == 2 ? 8 : 1)
   }
   if (kind != 2) {
     if (c * 8 < rot) {
-      const float* cs = a.cos_sin + pos * rot;
+      // N cosines and sines from pair i0 on. With axes, pairs of one axis come by
+      // 16-byte loads, as without; others one at a time from their axes' rows.
+      auto factors = [&](int i0, auto& cv, auto& sv) {
+        constexpr int N = sizeof(cv) / sizeof(float);
+        const float* cs = a.cos_sin + pos * rot + i0;
+        bool one_axis = true;
+        if constexpr (AXES) {
+          // two bits a pair; i0 is a multiple of N, so its pairs share a word
+          const uint32_t w = (i0 < 16 ? a.pair_axis.x : i0 < 32 ? a.pair_axis.y
+                              : i0 < 48 ? a.pair_axis.z : a.pair_axis.w) >> (2 * (i0 & 15));
+          auto at = [&](uint32_t x) { return x == 0 ? pos : x == 1 ? pos1 : x == 2 ? pos2 : pos3; };
+          const uint32_t mask = N == 8 ? 0xffffu : 0xffu;
+          one_axis = (w & mask) == ((w & 3u) * 0x5555u & mask);
+          if (one_axis) {
+            cs = a.cos_sin + at(w & 3u) * rot + i0;
+          } else {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+              const float* row = a.cos_sin + at((w >> (2 * i)) & 3u) * rot + i0 + i;
+              cv[i] = __ldg(row);
+              sv[i] = __ldg(row + rot / 2);
+            }
+          }
+        }
+        if (one_axis) {
+#pragma unroll
+          for (int i = 0; i < N; i += 4) {
+            const float4 co = __ldg(reinterpret_cast<const float4*>(cs + i));
+            const float4 si = __ldg(reinterpret_cast<const float4*>(cs + rot / 2 + i));
+            cv[i] = co.x, cv[i + 1] = co.y, cv[i + 2] = co.z, cv[i + 3] = co.w;
+            sv[i] = si.x, sv[i + 1] = si.y, sv[i + 2] = si.z, sv[i + 3] = si.w;
+          }
+        }
+      };
       if constexpr (INTER) {
         // pairs (2i, 2i+1): four of them in this chunk
-        const float4 co = __ldg(reinterpret_cast<const float4*>(cs + c * 4));
-        const float4 si = __ldg(reinterpret_cast<const float4*>(cs + rot / 2 + c * 4));
-        const float cv[4] = {co.x, co.y, co.z, co.w}, sv[4] = {si.x, si.y, si.z, si.w};
+        float cv[4], sv[4];
+        factors(c * 4, cv, sv);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           A[2 * i] = wf[2 * i] * cv[i];
@@ -182,11 +229,8 @@ __global__ void __launch_bounds__(kNrWarps * 32, NIT == 2 ? 8 : 1)
 #pragma unroll
         for (int i = 0; i < 8; ++i) pw[i] = 1.f;
         if (norm) unpack8(__ldg(static_cast<const uint4*>(wt) + pc), pw);
-        const float4* cp = reinterpret_cast<const float4*>(cs + 8 * (second ? pc : c));
-        const float4* sp = reinterpret_cast<const float4*>(cs + rot / 2 + 8 * (second ? pc : c));
-        const float4 c0 = __ldg(cp), c1 = __ldg(cp + 1), s0 = __ldg(sp), s1 = __ldg(sp + 1);
-        const float cv[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
-        const float sv[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+        float cv[8], sv[8];
+        factors(8 * (second ? pc : c), cv, sv);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           A[i] = wf[i] * cv[i];
@@ -275,7 +319,7 @@ __global__ void __launch_bounds__(kNrWarps * 32, NIT == 2 ? 8 : 1)
   }
 }
 
-template <int D, int KV, bool INTER, int NIT>
+template <int D, int KV, bool INTER, int NIT, bool AXES>
 cudaError_t launch_inst(NormRopeArgs a, int batches, cudaStream_t stream) {
   a.rows_per_warp = NIT * (256 / D) * batches;
   const long long RPT = a.rows_per_warp;
@@ -291,7 +335,7 @@ cudaError_t launch_inst(NormRopeArgs a, int batches, cudaStream_t stream) {
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, norm_rope_kernel<D, KV, INTER, NIT>, a);
+  return cudaLaunchKernelEx(&cfg, norm_rope_kernel<D, KV, INTER, NIT, AXES>, a);
 }
 
 // Rounds of a batch and batches of a warp. One round each keeps the smallest
@@ -303,21 +347,24 @@ cudaError_t launch_inst(NormRopeArgs a, int batches, cudaStream_t stream) {
 // 13.9 / 10.3 / 8.8 / 7.7, 8192: 106 / 67 / 48 / 43; 80 rows of 128 (E4M3): 128:
 // 5.0 / 4.9 / 5.3 / 5.2, 256: 7.4 / 6.3 / 7.1 / 5.6, 512: 13.0 / 9.4 / 9.2 / 8.5;
 // 24 rows of 64: 256: 2.6 / 2.9, 1024: 4.6 / 4.0, 8192: 30 / 19.
-template <int D, int KV, bool INTER>
+template <int D, int KV, bool INTER, bool AXES>
 cudaError_t launch_rounds(const NormRopeArgs& a, cudaStream_t stream) {
   constexpr int RPW = 256 / D;
   const long long rounds = static_cast<long long>(a.num_tokens) *
                            ((a.num_heads + 2LL * a.num_kv_heads + RPW - 1) / RPW);
   const long long slots = 32LL * a.num_sms;  // rounds in flight with half the warps of an SM
-  if (rounds <= slots) return launch_inst<D, KV, INTER, 1>(a, 1, stream);
-  if (rounds <= 2 * slots) return launch_inst<D, KV, INTER, 2>(a, 2, stream);
-  return launch_inst<D, KV, INTER, 2>(a, 4, stream);
+  if (rounds <= slots) return launch_inst<D, KV, INTER, 1, AXES>(a, 1, stream);
+  if (rounds <= 2 * slots) return launch_inst<D, KV, INTER, 2, AXES>(a, 2, stream);
+  return launch_inst<D, KV, INTER, 2, AXES>(a, 4, stream);
 }
 
 template <int D, int KV>
 cudaError_t launch_kind(const NormRopeArgs& a, cudaStream_t stream) {
-  return a.interleaved ? launch_rounds<D, KV, true>(a, stream)
-                       : launch_rounds<D, KV, false>(a, stream);
+  if (a.num_axes > 0)
+    return a.interleaved ? launch_rounds<D, KV, true, true>(a, stream)
+                         : launch_rounds<D, KV, false, true>(a, stream);
+  return a.interleaved ? launch_rounds<D, KV, true, false>(a, stream)
+                       : launch_rounds<D, KV, false, false>(a, stream);
 }
 
 }  // namespace

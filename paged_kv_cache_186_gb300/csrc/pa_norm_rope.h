@@ -31,6 +31,10 @@ struct NormRopeArgs {
   float eps;
   int num_sms;
   int rows_per_warp;  // set by the launch
+  // norm_rope_axes_store: positions is (num_axes, T), and two bits per rotated
+  // pair (pair i in word i / 16) name its axis; 0 axes: norm_rope_store
+  int num_axes;
+  uint4 pair_axis;
 };
 
 cudaError_t launch_norm_rope_store(const NormRopeArgs& a, cudaStream_t stream);

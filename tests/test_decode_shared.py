@@ -1,0 +1,279 @@
+"""pa_decode_shared against a plain 64-bit implementation (the library's attention tolerance)
+and against pa_decode of the same batch."""
+import numpy as np
+import pytest
+import torch
+
+import paged_kv_cache_186_gb300 as pa
+from gpu_util import assert_attention_close
+from shared_util import decode64, make
+
+pytestmark = pytest.mark.gpu
+
+
+def run(s, **kw):
+    out = pa.decode_shared(s.q, s.k_cache, s.v_cache, s.bt, s.context_lens, s.cu_groups,
+                           s.prefix_lens, s.scale, k_scale=s.k_scale, v_scale=s.v_scale, **kw)
+    torch.cuda.synchronize()
+    assert pa.get_device_error() == 0
+    return out
+
+
+def plain(s):
+    return pa.decode(s.q, s.k_cache, s.v_cache, s.bt, s.context_lens, s.scale, k_scale=s.k_scale,
+                     v_scale=s.v_scale)
+
+
+CASES = [
+    # groups [(prefix, lengths)], H, Hkv, D, bs, kv
+    ([(64, [65, 70, 100])], 8, 2, 128, 16, "bf16"),
+    ([(1, [1])], 1, 1, 128, 16, "bf16"),
+    ([(16, [16, 17, 33])], 4, 4, 64, 16, "bf16"),
+    ([(500, [501, 700, 0, 512, 530])], 8, 2, 128, 32, "bf16"),   # a padding row
+    ([(128, [129] * 40)], 8, 1, 128, 16, "bf16"),                # 320 rows: three tiles
+    ([(257, [300] * 33), (1000, [1001, 1024]), (48, [49] * 7)], 12, 4, 128, 16, "bf16"),  # group 3
+    ([(130, [131] * 20)], 10, 2, 128, 16, "bf16"),               # group 5
+    ([(300, [301 + i for i in range(19)])], 14, 2, 64, 32, "bf16"),  # group 7, head_dim 64
+    ([(1000, [1100] * 70)], 8, 2, 64, 16, "bf16"),
+    ([(640, [641, 1300, 650, 0])], 16, 2, 128, 32, "fp8"),
+    ([(100, [101] * 36), (333, [400, 334])], 8, 1, 128, 16, "fp8"),
+    ([(640, [641, 1300, 650])], 6, 2, 128, 16, "int8"),
+    ([(96, [97] * 50)], 8, 1, 128, 32, "int8"),
+]
+
+
+@pytest.mark.parametrize("case", CASES, ids=lambda c: f"{len(c[0])}g{sum(len(x[1]) for x in c[0])}"
+                         f"H{c[1]}kv{c[2]}D{c[3]}bs{c[4]}{c[5]}")
+def test_matches_64_bits_and_decode(case):
+    groups, H, Hkv, D, bs, kv = case
+    s = make(groups, H, Hkv, D, bs, kv, seed=500 + H + D + bs + len(groups))
+    out = run(s)
+    want = decode64(s)
+    assert_attention_close(out, want, str(case))
+    assert_attention_close(plain(s), want, "decode")
+    for b, n in enumerate(s.lens):
+        if n == 0:
+            assert (out[b] == 0).all()
+
+
+@pytest.mark.parametrize("prefix", [0, 1, 15, 16, 17, 127, 128, 129, 255, 256, 257, 384, 1 << 20])
+@pytest.mark.parametrize("bs", [16, 32])
+def test_prefix_lengths_around_blocks_and_tiles(prefix, bs):
+    s = make([(prefix, [300, 290, 299])], 8, 2, 128, bs, seed=520 + prefix % 97)
+    assert_attention_close(run(s), decode64(s), f"prefix {prefix}")
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+def test_sequences_shorter_than_the_prefix_and_padding(kv):
+    # the first rows of the group are padding and too short to name the blocks; a group of short
+    # sequences only shares nothing; rows of padding hold anything in the table
+    s = make([(200, [0, 30, 3, 205, 0, 200, 144]), (500, [40, 0, 20]), (64, [0, 0])], 8, 2, 128, 16,
+             kv, seed=540)
+    s.bt[s.context_lens == 0] = 1 << 30
+    out = run(s)
+    assert_attention_close(out, decode64(s), "short")
+    assert (out[s.context_lens == 0] == 0).all()
+
+
+def test_groups_that_are_empty_missing_or_leave_sequences_out():
+    s = make([(64, [80, 81]), (32, []), (100, [120])], 8, 2, 64, 16, seed=541,
+             outside=((50, 0, 7), (300, 12)))
+    want = decode64(s)
+    assert_attention_close(run(s), want, "outside")
+    s.cu_groups, s.prefix_lens = s.cu_groups[:1], s.prefix_lens[:0]
+    assert_attention_close(run(s), want, "no groups")
+
+
+def test_group_bounds_that_do_not_ascend_or_lie_outside():
+    s = make([(64, [80, 81, 90, 70])], 8, 2, 128, 16, seed=542)
+    want = decode64(s)
+    for cu in ([-7, 3, 1, 900], [0, 4, 2, 4], [3, 3, 3, 3], [9, 9, 9, 9], [0, 1 << 30, -5, 4]):
+        s.cu_groups = torch.tensor(cu, dtype=torch.int32).cuda()
+        s.prefix_lens = torch.tensor([64, 64, 64], dtype=torch.int32).cuda()
+        assert_attention_close(run(s), want, str(cu))
+    s.cu_groups = torch.tensor([0, 4], dtype=torch.int32).cuda()
+    for p in (-1, -(1 << 31), (1 << 31) - 1):
+        s.prefix_lens = torch.tensor([p], dtype=torch.int32).cuda()  # (too long: nothing shared)
+        assert_attention_close(run(s), want, f"prefix {p}")
+
+
+def test_slots_behind_a_sequence_may_hold_anything():
+    s = make([(70, [75, 100, 81]), (40, [41, 64])], 8, 2, 128, 16, seed=543)
+    bt = s.bt.cpu()
+    for b, n in enumerate(s.lens):
+        for p in range(n, -(-n // 16) * 16):
+            s.k_cache[bt[b, p // 16], p % 16] = float("nan")
+            s.v_cache[bt[b, p // 16], p % 16] = float("inf")
+    assert_attention_close(run(s), decode64(s), "tails")
+
+
+@pytest.mark.parametrize("kv, D", [("bf16", 128), ("bf16", 64), ("fp8", 128), ("int8", 128)])
+def test_long_prefix_many_sequences(kv, D):
+    s = make([(20011, [20011 + 37 * i for i in range(1, 18)]), (700, [701 + i for i in range(30)])],
+             8, 2, D, 16, kv, seed=544, spread=2.0)
+    assert_attention_close(run(s), decode64(s), "long")
+
+
+@pytest.mark.parametrize("rows", [3, 60])
+def test_weight_on_few_keys(rows):
+    # a few keys of the prefix and of the sequences' own draw nearly all of the weight
+    s = make([(2000, [2001 + 5 * i for i in range(rows)])], 8, 1, 128, 16, seed=545, spread=2.0)
+    bt = s.bt.cpu()
+    for p in (0, 1, 130, 1999):
+        s.k_cache[bt[0, p // 16].item(), p % 16] *= 4
+    assert_attention_close(run(s), decode64(s), "few keys")
+
+
+def test_scores_far_apart_between_prefix_and_own_keys():
+    # whole parts of the softmax vanish against others, in either order
+    for big in (0, 1):
+        s = make([(256, [300, 280, 270])], 8, 2, 128, 16, seed=546 + big)
+        blocks = s.bt[:, :16] if big == 0 else s.bt[:, 16:]
+        blocks = blocks[blocks >= 0].long()
+        s.k_cache[blocks.unique()] *= 60
+        assert_attention_close(run(s), decode64(s), f"far {big}")
+
+
+def test_equal_keys_give_the_mean():
+    s = make([(512, [600] * 9)], 8, 2, 128, 16, seed=548)
+    s.k_cache[:] = s.k_cache[0, 0, 0]
+    assert_attention_close(run(s), decode64(s), "mean")
+
+
+def test_length_bound_cuts_sequences():
+    s = make([(200, [300, 250, 210])], 8, 2, 128, 16, seed=549)
+    out = run(s, max_context_len=230)
+    s.lens = [min(n, 230) for n in s.lens]
+    assert_attention_close(out, decode64(s), "bound")
+    out = run(s, max_context_len=100)  # below the prefix
+    s.lens = [100] * 3
+    assert_attention_close(out, decode64(s), "bound below the prefix")
+
+
+def test_repeats_other_streams_outputs_and_strided_inputs():
+    s = make([(1500, [1501 + 31 * i for i in range(25)]), (80, [81, 300])], 32, 8, 128, 16, seed=550)
+    a = run(s)
+    need = pa.decode_shared_workspace_size(s.k_cache, 27, 32, s.bt.shape[1], 2)
+    ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+    b = torch.zeros_like(a)
+    assert run(s, out=b, workspace=ws) is b
+    assert torch.equal(a, b)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        c = pa.decode_shared(s.q, s.k_cache, s.v_cache, s.bt, s.context_lens, s.cu_groups,
+                             s.prefix_lens, s.scale)
+    side.synchronize()
+    assert torch.equal(a, c)
+    wide = torch.cat([s.bt, s.bt], dim=1)[:, :s.bt.shape[1]]
+    q = s.q.transpose(0, 1).contiguous().transpose(0, 1)
+    lens = torch.stack([s.context_lens] * 2, dim=1)[:, 0]
+    d = pa.decode_shared(q, s.k_cache, s.v_cache, wide, lens, s.cu_groups, s.prefix_lens, s.scale)
+    assert torch.equal(a, d)
+
+
+@pytest.mark.parametrize("shift", [0, 16, 112])
+def test_the_workspace_and_what_lies_around_it(shift):
+    s = make([(300, [301, 310, 350]), (90, [91] * 40)], 8, 2, 128, 16, seed=551)
+    need = pa.decode_shared_workspace_size(s.k_cache, 43, 8, s.bt.shape[1], 2)
+    want = run(s)
+    ref = torch.arange(need + 512, device="cuda").to(torch.uint8)
+    big = ref.clone()
+    out = run(s, workspace=big[128 + shift:128 + shift + need])
+    assert torch.equal(out, want)
+    assert torch.equal(big[:128 + shift], ref[:128 + shift])
+    assert torch.equal(big[128 + shift + need:], ref[128 + shift + need:])
+    with pytest.raises(pa.PAError, match="WORKSPACE"):
+        run(s, workspace=big[128 + shift:128 + shift + need - 1])
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+def test_graph_replays_with_lengths_and_groups_rewritten(kv):
+    s = make([(320, [330, 340, 350, 360]), (64, [100, 90, 70])], 8, 2, 128, 16, kv, seed=552)
+    need = pa.decode_shared_workspace_size(s.k_cache, 7, 8, s.bt.shape[1], 2, k_scale=s.k_scale,
+                                           v_scale=s.v_scale)
+    ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+    outs = [torch.zeros_like(s.q) for _ in range(2)]
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    run(s, workspace=ws)
+    for k in range(2):  # two graphs that share the workspace
+        with torch.cuda.graph(graphs[k]):
+            pa.decode_shared(s.q, s.k_cache, s.v_cache, s.bt, s.context_lens, s.cu_groups,
+                             s.prefix_lens, s.scale, out=outs[k], workspace=ws, k_scale=s.k_scale,
+                             v_scale=s.v_scale)
+    gen = torch.Generator().manual_seed(1)
+    for step in range(4):
+        s.q.copy_(torch.randn(s.q.shape, generator=gen))
+        if step == 1:
+            s.context_lens.copy_(torch.tensor([321, 340, 0, 322, 70, 65, 0], dtype=torch.int32))
+        if step == 2:
+            s.prefix_lens.copy_(torch.tensor([160, 0], dtype=torch.int32))
+        if step == 3:
+            s.cu_groups.copy_(torch.tensor([1, 4, 4], dtype=torch.int32))
+        s.lens = s.context_lens.tolist()
+        for o, graph in zip(outs, graphs):
+            o.fill_(float("nan"))
+            graph.replay()
+        torch.cuda.synchronize()
+        assert pa.get_device_error() == 0
+        want = decode64(s)
+        assert_attention_close(outs[0], want, f"step {step}")
+        assert torch.equal(outs[0], outs[1])
+        assert torch.equal(outs[0], run(s))
+
+
+def test_bad_block_ids_are_flagged_and_spoil_their_group_only():
+    s = make([(320, [330, 340]), (64, [100, 90, 70])], 8, 2, 128, 16, seed=553)
+    want = decode64(s)
+    for bad in (-1, 1 << 30):
+        s.bt[0, 3] = bad
+        out = pa.decode_shared(s.q, s.k_cache, s.v_cache, s.bt, s.context_lens, s.cu_groups,
+                               s.prefix_lens, s.scale)
+        assert pa.get_device_error() == pa.PA_DEVERR_BLOCK_RANGE
+        assert_attention_close(out[2:], want[2:], "other group")
+
+
+def test_large_batches_of_few_heads_and_many_groups():
+    # 600 sequences in 150 groups of four
+    groups = [(48 + 16 * (i % 5), [50 + 16 * (i % 5) + j for j in range(4)]) for i in range(150)]
+    s = make(groups, 2, 1, 64, 16, seed=554)
+    assert_attention_close(run(s), decode64(s), "many groups")
+
+
+def test_batches_and_groups_above_the_limit_are_refused():
+    B = 16385
+    kc = torch.zeros((4, 16, 1, 64), dtype=torch.bfloat16, device="cuda")
+    q = torch.zeros((B, 1, 64), dtype=torch.bfloat16, device="cuda")
+    bt = torch.zeros((B, 1), dtype=torch.int32, device="cuda")
+    cu = torch.tensor([0, B], dtype=torch.int32, device="cuda")
+    one = torch.ones(1, dtype=torch.int32, device="cuda")
+    assert pa.decode_shared_workspace_size(kc, B, 1, 1, 1) == 0
+    with pytest.raises(pa.PAError, match="UNSUPPORTED"):
+        pa.decode_shared(q, kc, kc.clone(), bt, bt[:, 0].contiguous(), cu, one, 0.1)
+    assert pa.decode_shared_workspace_size(kc, 4, 1, 1, B) == 0
+    many = torch.zeros(B + 1, dtype=torch.int32, device="cuda")
+    with pytest.raises(pa.PAError, match="UNSUPPORTED"):
+        pa.decode_shared(q[:4], kc, kc.clone(), bt[:4], bt[:4, 0].contiguous(), many, many[1:], 0.1)
+
+
+def test_an_empty_batch():
+    s = make([(16, [20])], 8, 2, 128, 16, seed=555)
+    cu = torch.zeros(1, dtype=torch.int32, device="cuda")
+    out = pa.decode_shared(s.q[:0], s.k_cache, s.v_cache, s.bt[:0], s.context_lens[:0], cu,
+                           cu[:0], s.scale)
+    assert out.shape == (0, 8, 128)
+
+
+def test_seeded_random_batches():
+    r = np.random.default_rng(7)
+    for i in range(24):
+        kv, D = [("bf16", 128), ("bf16", 64), ("fp8", 128), ("int8", 128)][i % 4]
+        bs, Hkv, G = int(r.choice([16, 32])), int(r.choice([1, 2, 4])), int(r.integers(1, 9))
+        groups = []
+        for _ in range(int(r.integers(1, 5))):
+            p = int(r.integers(0, 900))
+            groups.append((p, [int(n) for n in p + r.integers(-p // 2, 300, int(r.integers(1, 40)))]))
+        groups = [(p, [max(n, 0) for n in ls]) for p, ls in groups]
+        s = make(groups, G * Hkv, Hkv, D, bs, kv, seed=600 + i, outside=((5,), ()) if i % 3 else ((), ()))
+        bound = max(s.lens) if i % 2 else 0
+        assert_attention_close(run(s, max_context_len=bound), decode64(s), f"case {i}: {groups}")

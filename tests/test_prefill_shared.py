@@ -1,0 +1,163 @@
+"""pa_prefill_shared against a plain 64-bit implementation (the library's attention tolerance)
+and against pa_prefill_varlen of the same batch."""
+import numpy as np
+import pytest
+import torch
+
+import paged_kv_cache_186_gb300 as pa
+from gpu_util import assert_attention_close
+from shared_util import make, prefill64
+
+pytestmark = pytest.mark.gpu
+
+
+def run(s, **kw):
+    kw.setdefault("max_q_len", max(s.new, default=0))
+    out = pa.prefill_shared(s.q, s.k_cache, s.v_cache, s.bt, s.cu_q, s.cu_k, s.cu_groups,
+                            s.prefix_lens, s.scale, **kw)
+    torch.cuda.synchronize()
+    assert pa.get_device_error() == 0
+    return out
+
+
+CASES = [
+    # groups [(prefix, kv lengths)], new tokens, H, Hkv, bs
+    ([(64, [70, 90, 65])], [6, 20, 1], 8, 2, 16),
+    ([(1, [1])], [1], 1, 1, 16),
+    ([(300, [310, 305, 400])], [10, 5, 100], 32, 8, 32),
+    ([(128, [140] * 20)], [3] * 20, 4, 1, 16),
+    ([(500, [501 + 3 * i for i in range(9)])], [1 + i for i in range(9)], 16, 2, 16),   # group 8
+    ([(333, [400, 350, 334])], [64, 17, 1], 16, 1, 32),                                 # group 16
+    ([(200, [300, 290]), (40, [41, 60, 50])], [70, 33, 1, 20, 10], 2, 2, 16),           # group 1
+    ([(1000, [1300, 1200])], [300, 129], 8, 4, 16),                                     # group 2
+]
+
+
+@pytest.mark.parametrize("bound", [True, False])
+@pytest.mark.parametrize("case", CASES, ids=lambda c: f"{len(c[0])}g{len(c[1])}H{c[2]}kv{c[3]}bs{c[4]}")
+def test_matches_64_bits_and_prefill_varlen(case, bound):
+    groups, new, H, Hkv, bs = case
+    s = make(groups, H, Hkv, 128, bs, seed=700 + H + bs, new=new)
+    want = prefill64(s)
+    assert_attention_close(run(s, max_q_len=max(new) if bound else 0), want, str(case))
+    ref = pa.prefill_varlen(s.q, s.k_cache, s.v_cache, s.bt, s.cu_q, s.cu_k, s.scale)
+    assert_attention_close(ref, want, "prefill_varlen")
+
+
+@pytest.mark.parametrize("prefix", [0, 1, 15, 16, 17, 127, 128, 129, 200, 256, 299, 1 << 20])
+@pytest.mark.parametrize("new", [[1, 1, 1], [5, 40, 64], [300, 290, 299]])
+def test_prefix_lengths_with_new_tokens_inside_and_behind(prefix, new):
+    # the last form has no cached keys: most of the new tokens lie within the prefix
+    s = make([(prefix, [300, 290, 299])], 8, 2, 128, 16, seed=720 + prefix % 89, new=new)
+    assert_attention_close(run(s), prefill64(s), f"prefix {prefix}")
+
+
+def test_sequences_without_new_tokens_short_ones_and_rows_behind_the_last():
+    s = make([(200, [0, 30, 205, 200, 144, 90]), (500, [40, 20]), (32, [])], 8, 2, 128, 16, seed=740,
+             new=[0, 3, 5, 1, 0, 9, 40, 2])
+    want = prefill64(s)
+    T = s.q.shape[0]
+    q = torch.cat([s.q, s.q[:7]])  # rows behind the last sequence
+    out = torch.full_like(q, 3.0)
+    pa.prefill_shared(q, s.k_cache, s.v_cache, s.bt, s.cu_q, s.cu_k, s.cu_groups, s.prefix_lens,
+                      s.scale, max_q_len=40, out=out)
+    torch.cuda.synchronize()
+    assert_attention_close(out[:T], want, "short")
+    assert (out[T:] == 3.0).all()
+
+
+def test_sequences_outside_the_groups():
+    s = make([(64, [80, 81]), (100, [120])], 8, 2, 128, 16, seed=741, new=[5, 7, 10, 2, 20, 12],
+             outside=((50, 7), (300,)))
+    want = prefill64(s)
+    assert_attention_close(run(s), want, "outside")
+    s.cu_groups, s.prefix_lens = s.cu_groups[:1], s.prefix_lens[:0]
+    assert_attention_close(run(s), want, "no groups")
+
+
+def test_more_new_tokens_than_keys():
+    # invalid input, as for prefill_varlen: the cached length is 0, keys are clamped
+    s = make([(32, [40, 20, 0])], 8, 2, 128, 16, seed=742, new=[60, 3, 4])
+    assert_attention_close(run(s), prefill64(s), "clamped")
+
+
+def test_long_prefix_and_long_questions():
+    s = make([(9001, [9001 + 200, 9001 + 77, 9400]), (3000, [3300, 3001])], 8, 2, 128, 32, seed=746,
+             new=[200, 77, 260, 300, 1], spread=2.0)
+    assert_attention_close(run(s), prefill64(s), "long")
+
+
+def test_repeats_streams_workspaces_and_graphs():
+    s = make([(700, [701 + 9 * i for i in range(12)]), (80, [90, 300])], 32, 8, 128, 16, seed=747,
+             new=[1 + i % 7 for i in range(12)] + [10, 150])
+    a = run(s)
+    assert_attention_close(a, prefill64(s), "first")
+    T = s.q.shape[0]
+    need = pa.prefill_shared_workspace_size(s.k_cache, T, 32, 2)
+    ref = torch.arange(need + 512, device="cuda").to(torch.uint8)
+    for shift in (0, 16, 112):
+        big = ref.clone()
+        ws = big[128 + shift:128 + shift + need]
+        assert torch.equal(run(s, workspace=ws), a)
+        assert torch.equal(big[:128 + shift], ref[:128 + shift])
+        assert torch.equal(big[128 + shift + need:], ref[128 + shift + need:])
+        with pytest.raises(pa.PAError, match="WORKSPACE"):
+            run(s, workspace=ws[:-1])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        c = pa.prefill_shared(s.q, s.k_cache, s.v_cache, s.bt, s.cu_q, s.cu_k, s.cu_groups,
+                              s.prefix_lens, s.scale, max_q_len=150)
+    side.synchronize()
+    assert torch.equal(a, c)
+    ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+    outs = [torch.zeros_like(s.q) for _ in range(2)]
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    for k in range(2):
+        with torch.cuda.graph(graphs[k]):
+            pa.prefill_shared(s.q, s.k_cache, s.v_cache, s.bt, s.cu_q, s.cu_k, s.cu_groups,
+                              s.prefix_lens, s.scale, max_q_len=150, out=outs[k], workspace=ws)
+    for _ in range(3):
+        graphs[0].replay()
+        graphs[1].replay()
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], a) and torch.equal(outs[1], a)
+
+
+def test_bad_block_ids_are_flagged_and_spoil_their_group_only():
+    s = make([(320, [330, 340]), (64, [100, 90])], 8, 2, 128, 16, seed=748, new=[4, 9, 30, 1])
+    want = prefill64(s)
+    for bad in (-1, 1 << 30):
+        s.bt[0, 3] = bad
+        out = pa.prefill_shared(s.q, s.k_cache, s.v_cache, s.bt, s.cu_q, s.cu_k, s.cu_groups,
+                                s.prefix_lens, s.scale, max_q_len=30)
+        assert pa.get_device_error() == pa.PA_DEVERR_BLOCK_RANGE
+        assert_attention_close(out[13:], want[13:], "other group")
+
+
+def test_a_decode_step_is_a_prefill_of_one_token_each():
+    s = make([(500, [501 + 17 * i for i in range(20)])], 8, 2, 128, 16, seed=749, new=[1] * 20)
+    dec = pa.decode_shared(s.q, s.k_cache, s.v_cache, s.bt, s.context_lens, s.cu_groups,
+                           s.prefix_lens, s.scale)
+    want = prefill64(s)
+    assert_attention_close(run(s), want, "prefill")
+    assert_attention_close(dec, want, "decode")
+
+
+def test_seeded_random_batches():
+    r = np.random.default_rng(8)
+    for i in range(20):
+        bs, Hkv, G = int(r.choice([16, 32])), int(r.choice([1, 2, 4])), int(r.choice([1, 2, 4, 8, 16]))
+        groups, new = [], []
+        for _ in range(int(r.integers(1, 4))):
+            p = int(r.integers(0, 700))
+            ls = [max(0, int(n)) for n in p + r.integers(-p // 2, 200, int(r.integers(1, 14)))]
+            groups.append((p, ls))
+            new += [min(n, int(r.integers(0, int(r.choice([3, 30, 150]))))) for n in ls]
+        if sum(new) == 0:
+            new[0] = 1 if groups[0][1][0] else 0
+        if sum(new) == 0:
+            continue
+        s = make(groups, G * Hkv, Hkv, 128, bs, seed=800 + i, new=new)
+        assert_attention_close(run(s, max_q_len=max(new) if i % 2 else 0), prefill64(s),
+                               f"case {i}: {groups} {new}")

@@ -328,6 +328,7 @@ pa_status pa_decode_scored(const void* q, const pa_kv_cache* cache, const int32_
  *   num_groups   >= 0; 0: nothing is shared, cu_groups and prefix_lens may be NULL.
  *   workspace    at least pa_decode_shared_workspace_size() bytes (0: the shape is
  *                not supported), contract as for pa_decode.
+ *   scale        > 0 (PA_ERR_SHAPE).
  *   other arguments as pa_decode. Batches and num_groups above 16384 return
  *   PA_ERR_UNSUPPORTED. K and V of shared keys past the context_len of a shorter
  *   sequence of the group must be finite: it gives them the weight 0.

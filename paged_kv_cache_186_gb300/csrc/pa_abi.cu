@@ -16,6 +16,7 @@
 #include "pa_launch.h"
 #include "pa_norm_rope.h"
 #include "pa_prefill.h"
+#include "pa_shared.h"
 
 namespace {
 
@@ -381,6 +382,60 @@ size_t pa_decode_workspace_size(const pa_kv_cache* cache, int32_t batch, int32_t
 
 namespace {
 
+// The groups and the workspace of a call over shared context.
+struct SharedCall {
+  const int32_t* cu_groups;
+  const int32_t* prefix_lens;
+  int32_t num_groups;
+  void* workspace;
+  size_t workspace_bytes;
+};
+
+// Q viewed as (head_dim, num_heads, rows), bf16: one box is the G heads of a kv
+// head for `tokens` consecutive rows, 64 dims (128 bytes) wide.
+pa_status encode_q_map(CUtensorMap* map, const void* q, int head_dim, int num_heads, int rows,
+                       int group, int tokens) {
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(head_dim), static_cast<cuuint64_t>(num_heads),
+                              static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[2] = {head_dim * static_cast<cuuint64_t>(2),
+                                 static_cast<cuuint64_t>(num_heads) * head_dim * 2};
+  const cuuint32_t box[3] = {64u, static_cast<cuuint32_t>(group), static_cast<cuuint32_t>(tokens)};
+  const cuuint32_t estr[3] = {1u, 1u, 1u};
+  return g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides, box,
+                  estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                  CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+                 CUDA_SUCCESS
+             ? PA_OK
+             : PA_ERR_CUDA;
+}
+
+// What the launches of a call over shared context have in common.
+pa::SharedArgs shared_args(const SharedCall& call, const pa::SharedLayout& layout,
+                           const pa_kv_cache* cache, const int32_t* block_tables, int32_t max_blocks,
+                           int32_t batch, int32_t rows, int32_t num_heads, int len_cap, float scale,
+                           void* out, uint32_t* err) {
+  pa::SharedArgs a{};
+  a.block_tables = block_tables;
+  a.cu_groups = call.cu_groups;
+  a.prefix_lens = call.prefix_lens;
+  a.out = out;
+  a.err = err;
+  a.batch = batch;
+  a.num_groups = call.num_groups;
+  a.rows = rows;
+  a.num_heads = num_heads;
+  a.num_kv_heads = cache->num_kv_heads;
+  a.group = num_heads / cache->num_kv_heads;
+  a.head_dim = cache->head_dim;
+  a.block_size = cache->block_size;
+  a.max_blocks = max_blocks;
+  a.num_blocks = cache->num_blocks;
+  a.len_cap = len_cap;
+  a.scale_log2 = scale * 1.4426950408889634f;
+  pa::shared_pointers(a, layout, call.workspace);
+  return a;
+}
+
 // The workspace of pa_decode_scored: pa_decode's, then (from ml on) the final
 // (max, 1 / sum) of every query head, then the scores of every key.
 struct ScoredWorkspace {
@@ -398,15 +453,15 @@ ScoredWorkspace scored_workspace(size_t decode_bytes, int32_t batch, int32_t num
   return w;
 }
 
-// Shared body of pa_decode and pa_decode_append (k_new == NULL: no append) and
-// pa_decode_scored (scores != NULL).
+// Shared body of pa_decode and pa_decode_append (k_new == NULL: no append),
+// pa_decode_scored (scores != NULL) and pa_decode_shared (shared != NULL).
 pa_status decode_common(const void* q, const pa_kv_cache* cache, const int32_t* block_tables,
                         int32_t max_blocks_per_seq, const int32_t* context_lens,
                         int32_t max_context_len, int32_t batch, int32_t num_heads, float scale,
                         void* out, void* workspace, size_t workspace_bytes, void* stream,
                         const void* k_new, const void* v_new, const float* k_scale_new,
                         const float* v_scale_new, int32_t window, int32_t sinks,
-                        float* scores = nullptr) {
+                        float* scores = nullptr, const SharedCall* shared = nullptr) {
   pa_status st = check_cache(cache);
   if (st != PA_OK) return st;
   if (sinks < 0) return PA_ERR_SHAPE;
@@ -431,7 +486,13 @@ pa_status decode_common(const void* q, const pa_kv_cache* cache, const int32_t* 
   if (scores != nullptr && plan.persistent_ctas == 0) return PA_ERR_UNSUPPORTED;
   const ScoredWorkspace sw =
       scored_workspace(plan.workspace_bytes, batch, num_heads, cap, cache->block_size);
-  const size_t need = scores != nullptr ? sw.bytes : plan.workspace_bytes;
+  pa::SharedLayout layout{};
+  if (shared != nullptr)
+    layout = pa::shared_layout(plan.workspace_bytes, batch, num_heads, cache->num_kv_heads,
+                               cache->head_dim, shared->num_groups, dev->num_sms);
+  const size_t need = scores != nullptr   ? sw.bytes
+                      : shared != nullptr ? layout.bytes
+                                          : plan.workspace_bytes;
   if (need > 0 && (workspace == nullptr || workspace_bytes < need || !aligned16(workspace)))
     return PA_ERR_WORKSPACE;
   if (window > 0 && plan.persistent_ctas == 0) return PA_ERR_UNSUPPORTED;
@@ -512,6 +573,26 @@ pa_status decode_common(const void* q, const pa_kv_cache* cache, const int32_t* 
     char* const ws = static_cast<char*>(workspace);
     a.head_ml = reinterpret_cast<float2*>(ws + sw.ml);
     a.raw_scores = reinterpret_cast<float*>(ws + sw.raw);
+  }
+  if (shared != nullptr) {
+    pa::SharedArgs h = shared_args(*shared, layout, cache, block_tables, max_blocks_per_seq, batch,
+                                   batch, num_heads, cap, scale, out, dev->err);
+    h.context_lens = context_lens;
+    a.own_start = h.plan.row_start;
+    a.own_o = h.own_o;
+    a.own_ml = reinterpret_cast<float*>(h.own_ml);
+    CUtensorMap qmap, ksub, vsub;
+    if ((st = encode_q_map(&qmap, q, cache->head_dim, num_heads, batch, group, h.tokens_per_tile)) !=
+            PA_OK ||
+        (st = cached_cache_map(&ksub, cache->k_cache, cache, kSubtileMap)) != PA_OK ||
+        (st = cached_cache_map(&vsub, cache->v_cache, cache, kSubtileMap)) != PA_OK)
+      return st;
+    return pa::launch_shared_plan(h, strm) == cudaSuccess &&
+                   pa::launch_decode(a, kmap, vmap, strm) == cudaSuccess &&
+                   pa::launch_shared_keys(h, qmap, ksub, vsub, strm) == cudaSuccess &&
+                   pa::launch_shared_merge(h, strm) == cudaSuccess
+               ? PA_OK
+               : PA_ERR_CUDA;
   }
   if (pa::launch_decode(a, kmap, vmap, strm) != cudaSuccess) return PA_ERR_CUDA;
   if (scores != nullptr && pa::launch_add_scores(a, scores, dev->num_sms, strm) != cudaSuccess)
@@ -644,14 +725,8 @@ pa_status pa_decode_window_append(const void* q, const void* k_new, const void* 
 
 namespace {
 
-// The groups and the workspace of a call over shared context.
-struct SharedCall {
-  const int32_t* cu_groups;
-  const int32_t* prefix_lens;
-  int32_t num_groups;
-  void* workspace;
-  size_t workspace_bytes;
-};
+// A window no key lies outside of, with room for the kernel's differences.
+constexpr int kNoWindow = 0x7ffffe00;
 
 // Shared body of pa_prefill_varlen (window 0), pa_prefill_window and
 // pa_prefill_shared.
@@ -683,28 +758,16 @@ pa_status prefill_common(const void* q, const pa_kv_cache* cache, const int32_t*
   const int qbound = max_q_len > 0 ? std::min(max_q_len, total_q) : total_q;
   // the grid's z extent is the number of query-tile pairs of the longest sequence
   if ((static_cast<long long>(qbound) + 2 * tpt - 1) / (2 * tpt) > 65535) return PA_ERR_UNSUPPORTED;
+  pa::SharedLayout layout{};
   if (shared != nullptr) {
-    const size_t need =
-        pa_prefill_shared_workspace_size(cache, num_heads, total_q, shared->num_groups);
-    if (shared->workspace == nullptr || shared->workspace_bytes < need ||
+    layout = pa::shared_layout(0, total_q, num_heads, cache->num_kv_heads, 128, shared->num_groups,
+                               dev->num_sms);
+    if (shared->workspace == nullptr || shared->workspace_bytes < layout.bytes ||
         !aligned16(shared->workspace))
       return PA_ERR_WORKSPACE;
   }
-  // Q viewed as (head_dim, num_heads, total_q); one box = the G heads of a kv
-  // head for tpt consecutive tokens, 64 dims (128 bytes) wide.
   CUtensorMap qmap, kmap, vmap;
-  {
-    const cuuint64_t dims[3] = {128u, static_cast<cuuint64_t>(num_heads),
-                                static_cast<cuuint64_t>(total_q)};
-    const cuuint64_t strides[2] = {128u * 2u, static_cast<cuuint64_t>(num_heads) * 128u * 2u};
-    const cuuint32_t box[3] = {64u, static_cast<cuuint32_t>(group), static_cast<cuuint32_t>(tpt)};
-    const cuuint32_t estr[3] = {1u, 1u, 1u};
-    if (g_encode(&qmap, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(q), dims, strides,
-                 box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-      return PA_ERR_CUDA;
-  }
+  if ((st = encode_q_map(&qmap, q, 128, num_heads, total_q, group, tpt)) != PA_OK) return st;
   if ((st = cached_cache_map(&kmap, cache->k_cache, cache, kSubtileMap)) != PA_OK) return st;
   if ((st = cached_cache_map(&vmap, cache->v_cache, cache, kSubtileMap)) != PA_OK) return st;
   pa::PrefillArgs a{};
@@ -725,8 +788,25 @@ pa_status prefill_common(const void* q, const pa_kv_cache* cache, const int32_t*
   a.num_qtiles = (qbound + tpt - 1) / tpt;
   a.scale_log2 = scale * 1.4426950408889634f;
   // (the kernel subtracts the window and a key's offset from a position)
-  a.window = std::min(window, 0x7ffffe00);
+  a.window = std::min(window, kNoWindow);
   a.sinks = sinks;
+  if (shared != nullptr) {
+    const cudaStream_t strm = static_cast<cudaStream_t>(stream);
+    pa::SharedArgs h = shared_args(*shared, layout, cache, block_tables, max_blocks_per_seq, batch,
+                                   total_q, num_heads, decode_len_cap(cache, max_blocks_per_seq, 0),
+                                   scale, out, dev->err);
+    h.cu_q = cu_seqlens_q;
+    h.cu_k = cu_seqlens_k;
+    a.own_start = h.plan.row_start;
+    a.own_o = h.own_o;
+    a.own_ml = h.own_ml;
+    return pa::launch_shared_plan(h, strm) == cudaSuccess &&
+                   pa::launch_prefill(a, qmap, kmap, vmap, strm) == cudaSuccess &&
+                   pa::launch_shared_keys(h, qmap, kmap, vmap, strm) == cudaSuccess &&
+                   pa::launch_shared_merge(h, strm) == cudaSuccess
+               ? PA_OK
+               : PA_ERR_CUDA;
+  }
   return pa::launch_prefill(a, qmap, kmap, vmap, static_cast<cudaStream_t>(stream)) == cudaSuccess
              ? PA_OK
              : PA_ERR_CUDA;
@@ -760,9 +840,17 @@ pa_status pa_prefill_window(const void* q, const pa_kv_cache* cache, const int32
 size_t pa_decode_shared_workspace_size(const pa_kv_cache* cache, int32_t batch, int32_t num_heads,
                                        int32_t max_blocks_per_seq, int32_t num_groups,
                                        int32_t max_context_len) {
-  if (num_groups < 0 || num_groups > pa::kMaxPersistentBatch || batch > pa::kMaxPersistentBatch)
+  const size_t decode_bytes =
+      pa_decode_workspace_size(cache, batch, num_heads, max_blocks_per_seq, max_context_len);
+  if (decode_bytes == 0 || batch > pa::kMaxPersistentBatch || num_groups < 0 ||
+      num_groups > pa::kMaxPersistentBatch || num_heads % cache->num_kv_heads != 0 ||
+      num_heads / cache->num_kv_heads > 8)
     return 0;
-  return pa_decode_workspace_size(cache, batch, num_heads, max_blocks_per_seq, max_context_len);
+  DeviceInfo* dev = nullptr;
+  if (device_info(&dev) != PA_OK) return 0;
+  return pa::shared_layout(decode_bytes, batch, num_heads, cache->num_kv_heads, cache->head_dim,
+                           num_groups, dev->num_sms)
+      .bytes;
 }
 
 pa_status pa_decode_shared(const void* q, const pa_kv_cache* cache, const int32_t* block_tables,
@@ -773,22 +861,29 @@ pa_status pa_decode_shared(const void* q, const pa_kv_cache* cache, const int32_
                            size_t workspace_bytes, void* stream) {
   const pa_status st = check_cache(cache);
   if (st != PA_OK) return st;
-  if (num_groups < 0) return PA_ERR_SHAPE;
+  if (num_groups < 0 || !(scale > 0.f)) return PA_ERR_SHAPE;
   if (batch > 0 && num_groups > 0 && (cu_groups == nullptr || prefix_lens == nullptr))
     return PA_ERR_NULL;
   if (batch > pa::kMaxPersistentBatch || num_groups > pa::kMaxPersistentBatch)
     return PA_ERR_UNSUPPORTED;
+  const SharedCall shared{cu_groups, prefix_lens, num_groups, workspace, workspace_bytes};
+  const bool share = num_groups > 0 && cache->dtype == PA_KV_BF16;
   return decode_common(q, cache, block_tables, max_blocks_per_seq, context_lens, max_context_len,
                        batch, num_heads, scale, out, workspace, workspace_bytes, stream, nullptr,
-                       nullptr, nullptr, nullptr, 0, 0);
+                       nullptr, nullptr, nullptr, 0, 0, nullptr, share ? &shared : nullptr);
 }
 
 size_t pa_prefill_shared_workspace_size(const pa_kv_cache* cache, int32_t num_heads,
                                         int32_t total_q, int32_t num_groups) {
-  return check_cache(cache) == PA_OK && num_heads > 0 && total_q > 0 && num_groups >= 0 &&
-                 num_groups <= pa::kMaxPersistentBatch
-             ? 16
-             : 0;
+  if (check_cache(cache) != PA_OK || cache->dtype != PA_KV_BF16 || cache->head_dim != 128 ||
+      num_heads <= 0 || num_heads % cache->num_kv_heads != 0 ||
+      num_heads / cache->num_kv_heads > 16 || total_q <= 0 || num_groups < 0 ||
+      num_groups > pa::kMaxPersistentBatch)
+    return 0;
+  DeviceInfo* dev = nullptr;
+  if (device_info(&dev) != PA_OK) return 0;
+  return pa::shared_layout(0, total_q, num_heads, cache->num_kv_heads, 128, num_groups, dev->num_sms)
+      .bytes;
 }
 
 pa_status pa_prefill_shared(const void* q, const pa_kv_cache* cache, const int32_t* block_tables,
@@ -805,8 +900,10 @@ pa_status pa_prefill_shared(const void* q, const pa_kv_cache* cache, const int32
   if (batch > pa::kMaxPersistentBatch || num_groups > pa::kMaxPersistentBatch)
     return PA_ERR_UNSUPPORTED;
   const SharedCall shared{cu_groups, prefix_lens, num_groups, workspace, workspace_bytes};
+  const bool share = num_groups > 0;
   return prefill_common(q, cache, block_tables, max_blocks_per_seq, cu_seqlens_q, cu_seqlens_k,
-                        batch, num_heads, total_q, max_q_len, scale, 0, 0, out, stream, &shared);
+                        batch, num_heads, total_q, max_q_len, scale, share ? kNoWindow : 0, 0, out,
+                        stream, share ? &shared : nullptr);
 }
 
 pa_status pa_debug_inject_wait_timeout(int32_t skip_copy, uint64_t wait_limit_ns) {

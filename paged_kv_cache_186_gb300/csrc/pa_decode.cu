@@ -40,6 +40,9 @@
 //     bf16 at 4; less what L2 keeps in between).
 //   * A sliding window with sinks (WIN) walks only the blocks that hold a
 //     visible key and masks the rest inside them.
+//   * The variant of pa_decode_shared (SH) walks each sequence's blocks behind
+//     those its group shares and leaves (max, sum, unnormalised O) in fp32 where
+//     the others write bf16 rows, for the merge (pa_shared.cu).
 //   * Batches above kMaxPersistentBatch use a grid of (kv head, sequence,
 //     split) CTAs instead, with the same per-block code.
 #include <algorithm>
@@ -582,11 +585,23 @@ __device__ __forceinline__ void piece_next(Piece& p, const int* prefix, int B, i
   p.hi = static_cast<int>(min(static_cast<long long>(p.nblk), r1 - p.g));
 }
 
+// pa_decode_shared: the blocks of a sequence of L keys from key `start` (a
+// block's first) on.
+template <int BS>
+__device__ __forceinline__ SeqWindow own_blocks(int L, int start) {
+  SeqWindow w;
+  w.sb = 0;
+  w.shift = start / BS;
+  w.nvis = max(0, (L + BS - 1) / BS - w.shift);
+  w.hole_lo = w.hole_hi = 0;
+  return w;
+}
+
 // Write the warp's result for segment (b, kvh): bf16 output rows if the
 // segment is entirely this warp's, else an fp32 partial (O unnormalised,
 // (max, sum) per head) in `slot`. Lane (r, q4) holds O^T for heads 2q4, 2q4+1
 // and the running max/sum of head r.
-template <int D, bool Q8, bool SC>
+template <int D, bool Q8, bool SC, bool SH>
 __device__ __forceinline__ void write_warp_result(const DecodeArgs& a, int b, int kvh,
                                                   bool final_out, long long slot, int lane,
                                                   float m_run, float l_run, float o_scale,
@@ -597,7 +612,7 @@ __device__ __forceinline__ void write_warp_result(const DecodeArgs& a, int b, in
   const int h0 = 2 * q4, h1 = 2 * q4 + 1;  // accumulator heads of this lane
   const float l0 = __shfl_sync(kFull, l_tot, 4 * h0);
   const float l1 = __shfl_sync(kFull, l_tot, 4 * h1);
-  if (final_out) {
+  if (!SH && final_out) {
     if constexpr (SC) {
       if (q4 == 0 && r < G)
         a.head_ml[static_cast<long long>(b) * a.num_heads + kvh * G + r] =
@@ -623,6 +638,12 @@ __device__ __forceinline__ void write_warp_result(const DecodeArgs& a, int b, in
     return;
   }
   float* po = a.part_o + slot * a.slot_rows * D;
+  float* ml = a.part_ml + slot * a.slot_rows * 2;
+  if (SH && final_out) {
+    const long long bh = static_cast<long long>(b) * a.num_heads + kvh * G;
+    po = a.own_o + bh * D;
+    ml = a.own_ml + bh * 2;
+  }
   if constexpr (Q8) {
 #pragma unroll
     for (int mt = 0; mt < D / 16; ++mt)
@@ -644,8 +665,8 @@ __device__ __forceinline__ void write_warp_result(const DecodeArgs& a, int b, in
     }
   }
   if (q4 == 0 && r < G) {
-    a.part_ml[(slot * a.slot_rows + r) * 2 + 0] = m_run;
-    a.part_ml[(slot * a.slot_rows + r) * 2 + 1] = l_tot;
+    ml[r * 2 + 0] = m_run;
+    ml[r * 2 + 1] = l_tot;
   }
 }
 
@@ -835,7 +856,7 @@ __device__ __forceinline__ bool arrive_last(unsigned long long* counter, uint32_
 // shuffles); then every part costs one round of independent loads (its max
 // and the lane's head_dim slice of O), two parts in flight at a time.
 // Partials are read through L2.
-template <int D, int GP, bool SC>
+template <int D, int GP, bool SC, bool SH>
 __device__ __forceinline__ void merge_segment_g(const DecodeArgs& a, const PartList& sp, int b,
                                                 int kvh, bool final_out, int lane) {
   // lanes per head (at least 8 dims each, so a slice is whole 16-byte bf16 stores)
@@ -893,11 +914,16 @@ __device__ __forceinline__ void merge_segment_g(const DecodeArgs& a, const PartL
   }
   __syncwarp();  // every lane has read the first part's slot before it is overwritten
   if (!g_ok) return;
-  if (!final_out) {
-    // one partial of the merged parts, in the slot of the first of them
-    const long long row = sp.slot(0) * GP + g;
-    if (sub == 0) *reinterpret_cast<float2*>(a.part_ml + row * 2) = make_float2(M, L);
-    float4* dst = reinterpret_cast<float4*>(a.part_o + row * D + sub * DL);
+  if (SH || !final_out) {
+    // one partial of the merged parts, in the slot of the first of them (SH: or
+    // the sequence's result, as one)
+    const bool own = SH && final_out;
+    const long long row = own ? static_cast<long long>(b) * a.num_heads + kvh * G + g
+                              : sp.slot(0) * GP + g;
+    float* const po = own ? a.own_o : a.part_o;
+    float* const ml = own ? a.own_ml : a.part_ml;
+    if (sub == 0) *reinterpret_cast<float2*>(ml + row * 2) = make_float2(M, L);
+    float4* dst = reinterpret_cast<float4*>(po + row * D + sub * DL);
 #pragma unroll
     for (int v = 0; v < V4; ++v)
       dst[v] = make_float4(acc[4 * v], acc[4 * v + 1], acc[4 * v + 2], acc[4 * v + 3]);
@@ -921,20 +947,20 @@ __device__ __forceinline__ void merge_segment_g(const DecodeArgs& a, const PartL
   }
 }
 
-template <int D, bool SC>
+template <int D, bool SC, bool SH>
 __device__ __forceinline__ void merge_segment(const DecodeArgs& a, const PartList& sp, int b,
                                               int kvh, bool final_out, int lane) {
-  if (a.group <= 1) merge_segment_g<D, 1, SC>(a, sp, b, kvh, final_out, lane);
-  else if (a.group <= 2) merge_segment_g<D, 2, SC>(a, sp, b, kvh, final_out, lane);
-  else if (a.group <= 4) merge_segment_g<D, 4, SC>(a, sp, b, kvh, final_out, lane);
-  else merge_segment_g<D, 8, SC>(a, sp, b, kvh, final_out, lane);
+  if (a.group <= 1) merge_segment_g<D, 1, SC, SH>(a, sp, b, kvh, final_out, lane);
+  else if (a.group <= 2) merge_segment_g<D, 2, SC, SH>(a, sp, b, kvh, final_out, lane);
+  else if (a.group <= 4) merge_segment_g<D, 4, SC, SH>(a, sp, b, kvh, final_out, lane);
+  else merge_segment_g<D, 8, SC, SH>(a, sp, b, kvh, final_out, lane);
 }
 
 // Arrival of one part of a segment of more than kGroupedAbove parts: this
 // part's group first (the group's last arriver merges it into the slot of the
 // group's first part), then the segment over the group results. Out of line:
 // it is rare and must not add registers to the block loop.
-template <int D, bool SC>
+template <int D, bool SC, bool SH>
 __device__ __noinline__ void finish_grouped(const DecodeArgs a, const SegParts sp, int b, int kvh,
                                             long long gw, int lane) {
   const int j = static_cast<int>(gw - sp.w0), g0 = j - j % kMergeGroup;
@@ -944,7 +970,7 @@ __device__ __noinline__ void finish_grouped(const DecodeArgs a, const SegParts s
     last = arrive_last(a.grp_counters + sp.slot(g0), a.epoch, static_cast<uint32_t>(ng), a.err);
   if (!__shfl_sync(kFull, last, 0)) return;
   __threadfence();
-  merge_segment<D, SC>(a, PartList{sp, g0, 1, ng}, b, kvh, false, lane);
+  merge_segment<D, SC, SH>(a, PartList{sp, g0, 1, ng}, b, kvh, false, lane);
   __threadfence();
   __syncwarp();
   const int ngroups = (sp.n + kMergeGroup - 1) / kMergeGroup;
@@ -953,7 +979,7 @@ __device__ __noinline__ void finish_grouped(const DecodeArgs a, const SegParts s
                        static_cast<uint32_t>(ngroups), a.err);
   if (!__shfl_sync(kFull, last, 0)) return;
   __threadfence();
-  merge_segment<D, SC>(a, PartList{sp, 0, kMergeGroup, ngroups}, b, kvh, true, lane);
+  merge_segment<D, SC, SH>(a, PartList{sp, 0, kMergeGroup, ngroups}, b, kvh, true, lane);
 }
 
 template <int D, int BS, int NW, int ST, bool Q8>
@@ -1007,7 +1033,7 @@ __device__ __noinline__ void append_row(uint8_t* tile, float* stage_scales, cons
   __syncwarp();
 }
 
-template <int D, int BS, int NW, int ST, int KV, bool WIN, bool SC>
+template <int D, int BS, int NW, int ST, int KV, bool WIN, bool SC, bool SH = false>
 __global__ void __launch_bounds__(NW * 32, 3)
     decode_persistent_kernel(const __grid_constant__ CUtensorMap kmap,
                              const __grid_constant__ CUtensorMap vmap, const DecodeArgs a) {
@@ -1037,16 +1063,22 @@ __global__ void __launch_bounds__(NW * 32, 3)
   // there would let this prologue read lengths not yet written). Everything
   // else (the cache, q, the new rows, the output and the workspace) is touched
   // only after grid_dependency_wait().
+  // SH: the start of each sequence's own keys comes from the launch before this
+  // one; the launch behind it, which works on the shared keys beside this one,
+  // needs that too and so may start only once it is there.
+  if constexpr (SH) grid_dependency_wait();
   grid_launch_dependents();
+  auto window_of = [&](int b, int L) {
+    if constexpr (SH) return own_blocks<BS>(L, a.own_start[b]);
+    else return seq_window<BS>(L, WIN ? a.window : 0, a.sinks);
+  };
 
   // ---- blocks per sequence and their exclusive prefix sum (whole CTA)
   int carry = 0, vmax = 0;
   for (int base_i = 0; base_i < B; base_i += NW * 32) {
     const int i = base_i + threadIdx.x;
     int v = 0;
-    if (i < B)
-      v = seq_window<BS>(min(max(a.context_lens[i], 0), a.len_cap), WIN ? a.window : 0, a.sinks)
-              .nvis;
+    if (i < B) v = window_of(i, min(max(a.context_lens[i], 0), a.len_cap)).nvis;
     vmax = max(vmax, v);
     int incl = v;
 #pragma unroll
@@ -1122,9 +1154,7 @@ __global__ void __launch_bounds__(NW * 32, 3)
       const long long off = r - static_cast<long long>(prefix[lo]) * Hkv;
       kvh_o = static_cast<int>(off / nb);
       int blk = static_cast<int>(off % nb);
-      if (WIN)
-        blk = seq_window<BS>(min(max(a.context_lens[lo], 0), a.len_cap), a.window, a.sinks)
-                  .logical(blk);
+      if (WIN || SH) blk = window_of(lo, min(max(a.context_lens[lo], 0), a.len_cap)).logical(blk);
       phys_o = a.block_tables[static_cast<long long>(lo) * a.max_blocks + blk];
     }
   };
@@ -1153,7 +1183,8 @@ __global__ void __launch_bounds__(NW * 32, 3)
   // sequences without keys: zero output rows (no warp owns any of their
   // blocks). Sequence b is checked by CTA b mod gridDim.x, so no CTA scans
   // more than ceil(B / gridDim.x) of them.
-  for (int b = blockIdx.x; b < B; b += gridDim.x) {
+  // (SH: the merge's rows)
+  for (int b = blockIdx.x; !SH && b < B; b += gridDim.x) {
     if (prefix[b + 1] != prefix[b]) continue;  // uniform over the CTA
     uint4* const row = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) +
                                                 static_cast<long long>(b) * a.num_heads * D);
@@ -1228,7 +1259,7 @@ __global__ void __launch_bounds__(NW * 32, 3)
     finish_q<D, Q8>(qraw, qa, q_inv);
     const float sl2p = sl2 * q_inv;
     const int L = min(max(a.context_lens[cp.b], 0), a.len_cap);
-    const SeqWindow sw = seq_window<BS>(L, WIN ? a.window : 0, a.sinks);
+    const SeqWindow sw = window_of(cp.b, L);
     float acc[D / 16][4];
 #pragma unroll
     for (int mt = 0; mt < D / 16; ++mt) acc[mt][0] = acc[mt][1] = acc[mt][2] = acc[mt][3] = 0.f;
@@ -1266,7 +1297,7 @@ __global__ void __launch_bounds__(NW * 32, 3)
     Piece nx = cp;
     piece_next(nx, prefix, B, Hkv, r1);
     if (nx.valid) fetch_q<D, Q8>(a, nx.b, nx.kvh, lane, qraw);
-    write_warp_result<D, Q8, SC>(a, cp.b, cp.kvh, whole, 2 * gw + (cp.lo == 0 ? 1 : 0), lane, m_run,
+    write_warp_result<D, Q8, SC, SH>(a, cp.b, cp.kvh, whole, 2 * gw + (cp.lo == 0 ? 1 : 0), lane, m_run,
                               l_run, 1.f / vfac, acc);
     if (!whole) {
       const SegParts sp = seg_parts(prefix, B, Hkv, cp.b, cp.kvh, W, cost);
@@ -1283,7 +1314,7 @@ __global__ void __launch_bounds__(NW * 32, 3)
         if (lane == 0) atomicExch(a.seg_counters + static_cast<long long>(cp.b) * Hkv + cp.kvh, 0ull);
         __threadfence();
         __syncwarp();
-        merge_segment<D, SC>(a, PartList{sp, 0, 1, sp.n}, cp.b, cp.kvh, true, lane);
+        merge_segment<D, SC, SH>(a, PartList{sp, 0, 1, sp.n}, cp.b, cp.kvh, true, lane);
         cp = nx;
         continue;
       }
@@ -1291,7 +1322,7 @@ __global__ void __launch_bounds__(NW * 32, 3)
       __threadfence();
       __syncwarp();
       if (sp.n > kGroupedAbove) {
-        finish_grouped<D, SC>(a, sp, cp.b, cp.kvh, gw, lane);
+        finish_grouped<D, SC, SH>(a, sp, cp.b, cp.kvh, gw, lane);
       } else {
         int last = 0;
         if (lane == 0)
@@ -1299,7 +1330,7 @@ __global__ void __launch_bounds__(NW * 32, 3)
                              static_cast<uint32_t>(sp.n), a.err);
         if (__shfl_sync(kFull, last, 0)) {
           __threadfence();
-          merge_segment<D, SC>(a, PartList{sp, 0, 1, sp.n}, cp.b, cp.kvh, true, lane);
+          merge_segment<D, SC, SH>(a, PartList{sp, 0, 1, sp.n}, cp.b, cp.kvh, true, lane);
         }
       }
     }
@@ -1507,6 +1538,7 @@ struct Inst {
     auto* k0 = decode_persistent_kernel<D, BS, kWarps, kStages, KV, false, false>;
     auto* k1 = decode_persistent_kernel<D, BS, kWarps, kStages, KV, true, false>;
     auto* k2 = decode_persistent_kernel<D, BS, kWarps, kStages, KV, false, true>;
+    auto* k3 = decode_persistent_kernel<D, BS, kWarps, kStages, KV, false, false, true>;
     const int smem_max = PC::smem_bytes(kMaxPersistentBatch);
     const int smem = PC::smem_bytes(bb);
     int n0 = 0, n1 = 0;
@@ -1515,6 +1547,8 @@ struct Inst {
         cudaFuncSetAttribute(k1, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_max) !=
             cudaSuccess ||
         cudaFuncSetAttribute(k2, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_max) !=
+            cudaSuccess ||
+        cudaFuncSetAttribute(k3, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_max) !=
             cudaSuccess ||
         cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n0, k0, kWarps * 32, smem) != cudaSuccess ||
         cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n1, k1, kWarps * 32, smem) != cudaSuccess)
@@ -1528,7 +1562,9 @@ struct Inst {
     cudaError_t e;
     const long long rows = static_cast<long long>(a.batch) * a.num_heads;
     if (a.persistent_ctas > 0) {
-      auto* k = a.raw_scores != nullptr
+      auto* k = a.own_o != nullptr
+                    ? decode_persistent_kernel<D, BS, kWarps, kStages, KV, false, false, true>
+                : a.raw_scores != nullptr
                     ? decode_persistent_kernel<D, BS, kWarps, kStages, KV, false, true>
                 : a.window > 0 ? decode_persistent_kernel<D, BS, kWarps, kStages, KV, true, false>
                                : decode_persistent_kernel<D, BS, kWarps, kStages, KV, false, false>;

@@ -74,6 +74,12 @@ struct DecodeArgs {
   // final (max, 1 / sum) of every query head (B, H); NULL otherwise
   float* raw_scores;
   float2* head_ml;
+  // pa_decode_shared: attend to each sequence's keys from own_start (B) on and
+  // leave (max, sum) (B, H, 2) and unnormalised O (B, H, D) in fp32 instead of
+  // bf16 rows; NULL otherwise
+  const int* own_start;
+  float* own_o;
+  float* own_ml;
   int persistent_ctas;        // > 0: persistent kernel with this many CTAs
   int blocks_per_split, num_splits;  // grid-split path
   int kv;                     // kKvBf16, kKvE4m3 or kKvInt8

@@ -63,6 +63,9 @@
 //     benchmark's lengths, window 1000 + 4 sinks: 109 us, 0.30 of the bf16 rate; 2
 //     prompts of 9001-16384 new tokens, window 4096: 3.68 ms, 0.52 of it (the
 //     chain S, softmax, P.V, next S of each key tile).
+//   * The variant of pa_prefill_shared (SH) is a window whose first key is where
+//     the group's shared keys end, for all rows alike; it leaves (max, sum,
+//     unnormalised O) in fp32 for the merge (pa_shared.cu).
 //   * TMEM: 512 columns (S0, S1, O0, O1, 128 each); shared memory: Q0, Q1,
 //     two K and two V stages (192 KB).
 #include <algorithm>
@@ -167,7 +170,7 @@ __device__ __forceinline__ PairKeys pair_keys(int first_pos, int kv_len, int win
   return k;
 }
 
-template <int BS, bool WIN, bool SPLIT>
+template <int BS, bool WIN, bool SPLIT, bool SH>
 __global__ void __launch_bounds__(kThreads, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap qmap,
                    const __grid_constant__ CUtensorMap kmap,
@@ -183,6 +186,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   // launched as a programmatic dependent of the store that wrote the new
   // tokens' K/V: wait for it before reading anything
   grid_dependency_wait();
+  // (the launch behind works on the shared keys beside this one)
+  if constexpr (SH) grid_launch_dependents();
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // grid (kv head, sequence, tile pair counted from each sequence's end): CTAs
@@ -203,7 +208,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   // K/V tiles each query tile needs (keys its last row can see)
   int Tq[2];
   PairKeys pk{};
-  if constexpr (WIN) pk = pair_keys<BS>(cached + t00, kv_len, a.window, a.sinks);
+  int own = 0;  // SH: first key (a block's)
+  if constexpr (SH) {
+    own = a.own_start[q0];
+    pk.lo = pk.wb = pk.shift = own;
+  } else if constexpr (WIN) {
+    pk = pair_keys<BS>(cached + t00, kv_len, a.window, a.sinks);
+  }
   auto tiles_to = [&](int end) {
     if constexpr (WIN) return pk.template tiles<BS>(end);
     else return (end + kBN - 1) / kBN;
@@ -228,11 +239,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   // every tile of a window of fewer than kBN keys
   const bool narrow = WIN && min(a.window, kBN) + min(a.sinks, kBN) < kBN;
   auto two_term = [&](int i, int n) {
-    return (n == 0 && (cached + t00 + i * TPT < kBN || (WIN && a.sinks > 0))) || narrow;
+    return (n == 0 && (cached + t00 + i * TPT - own < kBN || (WIN && a.sinks > 0))) || narrow;
   };
   __nv_bfloat16* const out = static_cast<__nv_bfloat16*>(a.out);
   const int H = a.num_heads;
 
+  if (SH && T == 0) return;  // the rows see no own key: the merge knows
   if (T == 0) {  // no keys at all (invalid q_len > kv_len = 0): zero rows
     const int rows = (min(t00 + 2 * TPT, q_len) - t00) * G;
     for (int e = threadIdx.x; e < rows * (kD / 8); e += kThreads) {
@@ -598,13 +610,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         f0 = m_used == -INFINITY ? 0.f : fast_exp2(m_used - m);
         f1 = o.x == -INFINITY ? 0.f : fast_exp2(o.x - m);
         l = l * f0 + o.y * f1;
+        if (SH) m_used = m;
       }
     }
     // (the half's last tile: Tn - 1 or, for the first of two, the last even one)
     if (ok && !(SPLIT && ti == 1) && Tn > 0 &&
         warp_wait(bar(BAR_O + ti), ((Tn - 1) / nstep) & 1, &abort_flag, a.err)) {
       tc::fence_after_sync();
-      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const float inv = SH ? 1.f : l > 0.f ? 1.f / l : 0.f;
+      const long long row = static_cast<long long>(q0 + tok) * H + kvh * G + g;
+      if (SH && row_valid) a.own_ml[row] = make_float2(m_used, l);
       __nv_bfloat16* orow = out + (static_cast<long long>(q0 + tok) * H + kvh * G + g) * kD;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
@@ -619,7 +634,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int j = 0; j < 32; ++j)
             w[j] = __float_as_uint(__uint_as_float(w[j]) * f0 + __uint_as_float(v[j]) * f1);
         }
-        if (row_valid) {
+        if (SH && row_valid) {
+          float4* dst = reinterpret_cast<float4*>(a.own_o + row * kD + 32 * c);
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            dst[j] = make_float4(__uint_as_float(w[4 * j]), __uint_as_float(w[4 * j + 1]),
+                                 __uint_as_float(w[4 * j + 2]), __uint_as_float(w[4 * j + 3]));
+        } else if (row_valid) {
           uint32_t pk[16];
 #pragma unroll
           for (int j = 0; j < 16; ++j)
@@ -641,7 +662,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
-template <int BS, bool WIN, bool SPLIT>
+template <int BS, bool WIN, bool SPLIT, bool SH = false>
 cudaError_t launch_bs(const PrefillArgs& a, const CUtensorMap& qmap, const CUtensorMap& kmap,
                       const CUtensorMap& vmap, cudaStream_t stream) {
   static bool attr_set[64] = {};
@@ -650,7 +671,7 @@ cudaError_t launch_bs(const PrefillArgs& a, const CUtensorMap& qmap, const CUten
   if (e != cudaSuccess) return e;
   if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
   if (!attr_set[dev]) {
-    e = cudaFuncSetAttribute(prefill_kernel<BS, WIN, SPLIT>,
+    e = cudaFuncSetAttribute(prefill_kernel<BS, WIN, SPLIT, SH>,
                              cudaFuncAttributeMaxDynamicSharedMemorySize, smem_bytes(SPLIT));
     if (e != cudaSuccess) return e;
     attr_set[dev] = true;
@@ -666,7 +687,7 @@ cudaError_t launch_bs(const PrefillArgs& a, const CUtensorMap& qmap, const CUten
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, prefill_kernel<BS, WIN, SPLIT>, qmap, kmap, vmap, a);
+  return cudaLaunchKernelEx(&cfg, prefill_kernel<BS, WIN, SPLIT, SH>, qmap, kmap, vmap, a);
 }
 
 }  // namespace
@@ -675,6 +696,13 @@ cudaError_t launch_prefill(const PrefillArgs& a, const CUtensorMap& qmap, const 
                            const CUtensorMap& vmap, cudaStream_t stream) {
   if (a.head_dim != kD || kBM % a.group != 0) return cudaErrorInvalidValue;
   if (a.block_size != 16 && a.block_size != 32) return cudaErrorInvalidValue;
+  if (a.own_o != nullptr) {  // as with a window, below
+    if (a.num_qtiles <= 1)
+      return a.block_size == 16 ? launch_bs<16, true, true, true>(a, qmap, kmap, vmap, stream)
+                                : launch_bs<32, true, true, true>(a, qmap, kmap, vmap, stream);
+    return a.block_size == 16 ? launch_bs<16, true, false, true>(a, qmap, kmap, vmap, stream)
+                              : launch_bs<32, true, false, true>(a, qmap, kmap, vmap, stream);
+  }
   if (a.window > 0) {
     // every sequence within one query tile (num_qtiles is of the longest): both
     // halves of a CTA share it. Measured on one GB300, 32 sequences of 1-16 new

@@ -19,6 +19,12 @@ struct PrefillArgs {
   int num_qtiles;       // tiles per sequence in the grid (from the max q_len bound)
   float scale_log2;
   int window, sinks;    // sliding window (> 0) with leading sink keys; 0 = all keys
+  // pa_prefill_shared: attend to each sequence's keys from own_start[its first
+  // row] (total_q) on and leave (max, sum) (total_q, H) and unnormalised O
+  // (total_q, H, D) in fp32 instead of bf16 rows; NULL otherwise
+  const int* own_start;
+  float* own_o;
+  float2* own_ml;
 };
 
 // Query tokens per 128-row tile for a head group of `group` query heads.

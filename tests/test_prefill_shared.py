@@ -81,6 +81,16 @@ def test_more_new_tokens_than_keys():
     assert_attention_close(run(s), prefill64(s), "clamped")
 
 
+@pytest.mark.parametrize("rows", [3, 60])
+def test_weight_on_few_keys(rows):
+    s = make([(2000, [2001 + 5 * i for i in range(rows)])], 8, 2, 128, 16, seed=745, spread=2.0,
+             new=[1 + i % 4 for i in range(rows)])
+    bt = s.bt.cpu()
+    for p in (0, 1, 100, 1999):
+        s.k_cache[bt[0, p // 16].item(), p % 16] *= 4
+    assert_attention_close(run(s), prefill64(s), "few keys")
+
+
 def test_long_prefix_and_long_questions():
     s = make([(9001, [9001 + 200, 9001 + 77, 9400]), (3000, [3300, 3001])], 8, 2, 128, 32, seed=746,
              new=[200, 77, 260, 300, 1], spread=2.0)

@@ -64,7 +64,8 @@ def decode(L, cache=None, q=P(0x10), bt=P(0x20), mb=4, cl=P(0x30), cu=P(0x40), p
     (dict(q=None), 1), (dict(bt=None), 1), (dict(cl=None), 1), (dict(out=None), 1),
     (dict(cu=None), 1), (dict(pl=None), 1), (dict(G=-1), 2), (dict(B=-1), 2), (dict(mb=0), 2),
     (dict(H=3), 2), (dict(H=18), 4), (dict(B=16385), 4), (dict(G=16385), 4),
-    (dict(scale=float("nan")), 2), (dict(q=P(0x18)), 7), (dict(out=P(0x68)), 7), (dict(B=0), 0),
+    (dict(scale=float("nan")), 2), (dict(scale=0.0), 2), (dict(scale=-0.1), 2),
+    (dict(q=P(0x18)), 7), (dict(out=P(0x68)), 7), (dict(B=0), 0),
     (dict(B=0, G=0, cu=None, pl=None), 0),
 ])
 def test_decode_shared_arguments(L, kw, want):

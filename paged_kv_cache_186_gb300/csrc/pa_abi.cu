@@ -431,6 +431,9 @@ pa::SharedArgs shared_args(const SharedCall& call, const pa::SharedLayout& layou
   a.max_blocks = max_blocks;
   a.num_blocks = cache->num_blocks;
   a.len_cap = len_cap;
+  a.k_scale = cache->k_scale;
+  a.v_scale = cache->v_scale;
+  a.kv = static_cast<int>(cache->dtype);
   a.scale_log2 = scale * 1.4426950408889634f;
   pa::shared_pointers(a, layout, call.workspace);
   return a;
@@ -867,10 +870,10 @@ pa_status pa_decode_shared(const void* q, const pa_kv_cache* cache, const int32_
   if (batch > pa::kMaxPersistentBatch || num_groups > pa::kMaxPersistentBatch)
     return PA_ERR_UNSUPPORTED;
   const SharedCall shared{cu_groups, prefix_lens, num_groups, workspace, workspace_bytes};
-  const bool share = num_groups > 0 && cache->dtype == PA_KV_BF16;
   return decode_common(q, cache, block_tables, max_blocks_per_seq, context_lens, max_context_len,
                        batch, num_heads, scale, out, workspace, workspace_bytes, stream, nullptr,
-                       nullptr, nullptr, nullptr, 0, 0, nullptr, share ? &shared : nullptr);
+                       nullptr, nullptr, nullptr, 0, 0, nullptr,
+                       num_groups > 0 ? &shared : nullptr);
 }
 
 size_t pa_prefill_shared_workspace_size(const pa_kv_cache* cache, int32_t num_heads,

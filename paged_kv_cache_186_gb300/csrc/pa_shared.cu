@@ -31,6 +31,7 @@
 // (1.28e-2 measured on rows with four dominant keys), and shared prompts begin
 // with such keys.
 #include <algorithm>
+#include <type_traits>
 
 #include "pa_device.cuh"
 #include "pa_launch.h"
@@ -44,6 +45,7 @@ namespace {
 constexpr unsigned kFull = 0xffffffffu;
 constexpr int kBM = 128;  // rows per query tile
 constexpr int kBN = 128;  // keys per tile
+constexpr int kSN = 64;   // keys per step: half a tile
 constexpr int kSub = 128 * kBM;  // bytes of a 64-dim (128-byte-wide) column of a 128-row tile
 
 // ============================================================ plan
@@ -244,75 +246,111 @@ struct PieceWalk {
   }
 };
 
-constexpr int kThreads = 384;  // 2 x 4 softmax warps, K, MMA, V and Q warps
-// Register split (setmaxnreg), as the prefill kernel's: 2*128*208 + 128*88 = 384*168.
-constexpr int kSoftmaxRegs = 208;
-constexpr int kControlRegs = 88;
-static_assert(2 * 128 * kSoftmaxRegs + 128 * kControlRegs <= kThreads * 168,
+constexpr int kThreads = 512;  // 2 x 4 softmax warps, K, MMA, V and Q warps, 4 converting warps
+// Register split (setmaxnreg) of the launch's 512 x 128.
+constexpr int kSoftmaxRegs = 160;
+constexpr int kControlRegs = 96;
+constexpr int kConvertRegs = 96;
+static_assert(2 * kSoftmaxRegs + kControlRegs + kConvertRegs <= 4 * 128,
               "register split exceeds the launch allocation");
-constexpr float kRescaleThreshold = 8.0f;  // log2 units
+constexpr float kRescaleThreshold = 8.0f;  // log2 units: P stays below 2^8 of its row's scale
 
-// K (and V) stages: what shared memory holds beside the query tiles.
-template <int D, bool PAIR>
+// Shared memory of a CTA. 8-bit codes (Q8) land as they are in raw stages of 128
+// keys and are widened into the 16-bit ones; with one row tile the room of the
+// second goes to deeper rings, since such calls are bound by the loads.
+template <int D, bool Q8, bool PAIR>
 struct Ring {
   static constexpr int kTile = (D / 64) * kSub;
+  static constexpr int kRawTile = kBN * 128;
   static constexpr int kQTiles = PAIR ? 2 : 1;
-  static constexpr int kStages = D == 64 ? (PAIR ? 4 : 6) : (PAIR ? 2 : 3);
-  static constexpr int kBytes = 1024 + (kQTiles + 2 * kStages) * kTile;
-  // (the static part: barriers and 1 KB of row sums)
-  static_assert(kBytes <= 225 * 1024 + 512, "shared memory over the per-CTA limit");
+  static constexpr int kK = Q8 ? (PAIR ? 2 : 1) : D == 64 ? (PAIR ? 4 : 6) : PAIR ? 2 : 3;
+  static constexpr int kV = Q8 ? 2 : D == 64 ? (PAIR ? 4 : 6) : 3;
+  static constexpr int kRaw = Q8 ? (PAIR ? 1 : 2) : 0;  // of K and of V each
+  static constexpr int kQ0 = 0;
+  static constexpr int kK0 = kQ0 + kQTiles * kTile;
+  static constexpr int kV0 = kK0 + kK * kTile;
+  static constexpr int kRawK0 = kV0 + kV * kTile;
+  static constexpr int kRawV0 = kRawK0 + kRaw * kRawTile;
+  static constexpr int kScale0 = kRawV0 + kRaw * kRawTile;   // (kV, 2, 128) fp32: K, V scales
+  static constexpr int kHalf0 = kScale0 + (Q8 ? kV * 2 * kBN * 4 : 0);  // (128) float2
+  static constexpr int kSmall0 = kHalf0 + (PAIR ? 0 : kBM * 8);
+  static constexpr int kBytes = kSmall0 + 640;
+  static_assert(kBytes <= 227 * 1024, "shared memory over the per-CTA limit");
 };
 constexpr int kMaxStages = 6;
+constexpr int kMaxRaw = 2;
 
 enum {
   BAR_QF = 0,                    // Q tiles landed
   BAR_QE,                        // the last S of the segment is done
-  BAR_KF,                        // + stage
-  BAR_KE = BAR_KF + kMaxStages,
-  BAR_VF = BAR_KE + kMaxStages,
-  BAR_VE = BAR_VF + kMaxStages,
-  BAR_S = BAR_VE + kMaxStages,   // + half: S ready
-  BAR_P = BAR_S + 2,             // + half: P written (4 warps)
-  BAR_O = BAR_P + 2,             // + half: P.V done
-  BAR_E = BAR_O + 2,             // + half: O of the piece has been read (4 warps)
+  BAR_KF,                        // + K stage: ready for the MMAs (landed, or widened by 4 warps)
+  BAR_KE = BAR_KF + kMaxStages,  // + K stage: free
+  BAR_VL = BAR_KE + kMaxStages,  // + V stage: landed (bf16)
+  BAR_VF = BAR_VL + kMaxStages,  // + V stage: in f16 (4 warps)
+  BAR_VE = BAR_VF + kMaxStages,  // + V stage: free
+  BAR_RKF = BAR_VE + kMaxStages,  // + raw stage: K codes landed
+  BAR_RKE = BAR_RKF + kMaxRaw,    // + raw stage: K codes read (4 warps)
+  BAR_RVF = BAR_RKE + kMaxRaw,
+  BAR_RVE = BAR_RVF + kMaxRaw,
+  BAR_S = BAR_RVE + kMaxRaw,     // + 2 half + buffer: S ready
+  BAR_P = BAR_S + 4,             // + 2 half + buffer: P written (4 warps)
+  BAR_O = BAR_P + 4,             // + 2 half + buffer: P.V done
+  BAR_E = BAR_O + 4,             // + half: O of the piece has been read (4 warps)
   BAR_ML = BAR_E + 2,            // second half's (max, sum) written (4 warps)
+  BAR_X,                         // converting warps' maxima written (4 warps)
   BAR_DRAIN,
   NBAR
 };
+static_assert(NBAR * 8 + kMaxStages * 4 + 8 * 4 + 8 <= 640, "barriers and small arrays");
 
-// Bounded wait that also gives up when another role of the CTA has aborted.
-__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+// Bounded wait that also gives up when another role of the CTA has aborted: by
+// one thread, and by a warp.
+__device__ __forceinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int* abort_flag,
                                           uint32_t* err) {
-  bool ok = mbar_try_wait(bar, parity);
-  if (!ok) {
-    const unsigned long long t0 = global_timer_ns();
-    while (!ok) {
+  const unsigned long long t0 = global_timer_ns();
+  while (true) {
 #pragma unroll 1
-      for (int i = 0; i < 64 && !ok; ++i) ok = mbar_try_wait(bar, parity);
-      if (ok || *abort_flag) break;
-      if (global_timer_ns() - t0 > kWaitLimitNs) {
-        *abort_flag = 1;
-        report_error(err, PA_DEVERR_WAIT_TIMEOUT);
-        break;
-      }
+    for (int i = 0; i < 64; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
+    if (*abort_flag) return false;
+    if (global_timer_ns() - t0 > kWaitLimitNs) {
+      *abort_flag = 1;
+      report_error(err, PA_DEVERR_WAIT_TIMEOUT);
+      return false;
     }
   }
-  return __all_sync(kFull, ok);
+}
+__device__ __forceinline__ bool thread_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                            uint32_t* err) {
+  return mbar_try_wait(bar, parity) || mbar_try_wait(bar, parity) ||
+         wait_slow(bar, parity, abort_flag, err);
+}
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                          uint32_t* err) {
+  return __all_sync(kFull, thread_wait(bar, parity, abort_flag, err));
 }
 
-template <int D, int BS, bool PAIR>
+__device__ __forceinline__ float pow2i(int k) {  // 2^k, k in [-126, 127]
+  return __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
+}
+
+// Two f16 -> two bf16 (of 8-bit codes: exact).
+__device__ __forceinline__ uint32_t f16x2_to_bf16x2(uint32_t w) {
+  const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+  return pack_bf16x2(f.x, f.y);
+}
+
+template <int D, int BS, int KV, bool PAIR>
 __global__ void __launch_bounds__(kThreads, 1)
     shared_keys_kernel(const __grid_constant__ CUtensorMap qmap,
                        const __grid_constant__ CUtensorMap kmap,
                        const __grid_constant__ CUtensorMap vmap, const SharedArgs a) {
-  using R = Ring<D, PAIR>;
-  constexpr int ST = R::kStages, kTile = R::kTile, kBlocks = kBN / BS;
+  constexpr bool Q8 = KV != kKvBf16;
+  using R = Ring<D, Q8, PAIR>;
+  constexpr int kTile = R::kTile, kBlocks = kBN / BS;
   constexpr int kCols = D / 32;  // 32-column chunks of O
-  extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t bars[NBAR];
-  __shared__ uint32_t tmem_slot;
-  __shared__ volatile int abort_flag;
-  __shared__ float2 half_ml[PAIR ? 1 : kBM];  // the second half's (max, sum) of each row
+  constexpr int kStep = PAIR ? 1 : 2;  // key tiles from one of a half's to its next
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = a.group, TPT = a.tokens_per_tile;
@@ -320,46 +358,193 @@ __global__ void __launch_bounds__(kThreads, 1)
   // after the plan was complete, and works beside it: its results are waited
   // for at the end, on behalf of the merge.
   PieceWalk walk(a);
-  if (walk.u >= walk.u1) {
+  const uint32_t base = smem_addr(smem_raw);
+  if (walk.u >= walk.u1 || (base & 1023u) != 0) {  // (swizzled tiles need the alignment asked for)
+    if (walk.u < walk.u1 && threadIdx.x == 0) report_error(a.err, PA_DEVERR_WAIT_TIMEOUT);
     grid_dependency_wait();
     return;
   }
-
-  const uint32_t raw = smem_addr(smem_raw);
-  const uint32_t base = (raw + 1023u) & ~1023u;
-  auto q_s = [&](int i) { return base + i * kTile; };
-  auto k_s = [&](int s) { return base + (R::kQTiles + s) * kTile; };
-  auto v_s = [&](int s) { return base + (R::kQTiles + ST + s) * kTile; };
-  const uint32_t bar0 = smem_addr(&bars[0]);
+  auto q_s = [&](int i) { return base + R::kQ0 + i * kTile; };
+  auto k_s = [&](int s) { return base + R::kK0 + s * kTile; };
+  auto v_s = [&](int s) { return base + R::kV0 + s * kTile; };
+  float* const scales = reinterpret_cast<float*>(smem_raw + R::kScale0);
+  float2* const half_ml = reinterpret_cast<float2*>(smem_raw + R::kHalf0);
+  uint64_t* const bars = reinterpret_cast<uint64_t*>(smem_raw + R::kSmall0);
+  int* const fac = reinterpret_cast<int*>(bars + NBAR);              // (kV) V's factor is 2^fac
+  uint32_t* const cmax = reinterpret_cast<uint32_t*>(fac + kMaxStages);  // (2, 4)
+  uint32_t* const tmem_slot = cmax + 8;
+  volatile int* const abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const uint32_t bar0 = smem_addr(bars);
   auto bar = [&](int i) { return bar0 + 8u * i; };
   if (threadIdx.x == 0) {
     for (int i = 0; i < NBAR; ++i) {
-      const bool warps4 = i == BAR_P || i == BAR_P + 1 || i == BAR_E || i == BAR_E + 1 || i == BAR_ML;
+      const bool warps4 = (i >= BAR_VF && i < BAR_VE) || (i >= BAR_P && i < BAR_O) ||
+                          (i >= BAR_E && i <= BAR_X) || (i >= BAR_RKE && i < BAR_RVF) ||
+                          (i >= BAR_RVE && i < BAR_S) || (Q8 && i >= BAR_KF && i < BAR_KE);
       mbar_init(bar(i), warps4 ? 4 : 1);
     }
-    abort_flag = 0;
+    *abort_flag = 0;
     fence_barrier_init();
     fence_proxy_async_smem();
   }
   if (warp == 9) {
-    tc::tmem_alloc(smem_addr(&tmem_slot), 512);
+    tc::tmem_alloc(smem_addr(tmem_slot), 512);
     tc::tmem_relinquish();
   }
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
-  const uint32_t tmem = tmem_slot;
-  auto tS = [&](int i) { return tmem + 128u * i; };  // S, then P (terms in columns 0-63, 64-127)
+  const uint32_t tmem = *tmem_slot;
+  // S of half i in two buffers of 64 columns, each then P in its first 32
+  auto tS = [&](int i, uint32_t b) { return tmem + 128u * i + 64u * b; };
   auto tO = [&](int i) { return tmem + 256u + 128u * i; };
-  auto wait = [&](int b, uint32_t parity) { return warp_wait(bar(b), parity, &abort_flag, a.err); };
+  auto wait = [&](int b, uint32_t parity) { return warp_wait(bar(b), parity, abort_flag, a.err); };
 
   Piece p;
-  if (warp >= 8) {
+  if (warp >= 12) {
+    // ------------------------------------------------------------ conversion
+    // V into f16 (times a power of two), where P as one f16 term is precise
+    // enough; 8-bit codes into bf16 (K) and f16 (V), exactly.
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kConvertRegs));
+    const int tid = threadIdx.x - 384;  // and, of 8-bit codes, the thread's key of the tile
+    uint32_t c = 0;  // key tiles so far
+    int k = 0;       // log2 of V's factor, or of the V scales'
+    bool ok = true;
+    // the largest of the four warps' values
+    auto all_max = [&](uint32_t v) {
+      v = __reduce_max_sync(kFull, v);
+      if (lane == 0) {
+        cmax[(c & 1) * 4 + (warp - 12)] = v;
+        mbar_arrive(bar(BAR_X));
+      }
+      ok = wait(BAR_X, c & 1);
+      const uint4 m = *reinterpret_cast<const uint4*>(cmax + (c & 1) * 4);
+      return max(max(m.x, m.y), max(m.z, m.w));
+    };
+    // keep the factor while it puts the tile's largest value (bits of a positive
+    // float) at 2^lo .. 2^(hi + 1), else move the value to 2^mid
+    auto move_factor = [&](uint32_t bits, int lo, int hi, int mid) {
+      if (bits == 0) return;
+      const int e = static_cast<int>(bits >> 23) - 127;
+      if (e + k < lo || e + k > hi) k = min(max(mid - e, -120), 90);
+    };
+    auto publish = [&](int b) {  // this warp's writes to a stage, to the MMAs
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(b));
+    };
+    while (ok && walk.next(a, p)) {
+      float ks = 0.f, vs = 0.f;  // Q8: scales of this thread's key
+      int phys1 = -1;            // its block in the next tile
+      const long long bt_row = static_cast<long long>(p.owner) * a.max_blocks;
+      auto block_of = [&](int t) {
+        const int key = t * kBN + tid;
+        return t < p.t1 && key < p.keys ? __ldg(a.block_tables + bt_row + key / BS) : -1;
+      };
+      auto load_scales = [&](int phys) {
+        ks = vs = 0.f;
+        if (phys >= 0 && phys < a.num_blocks) {
+          const long long i = (static_cast<long long>(phys) * a.num_kv_heads + p.kvh) * BS + tid % BS;
+          ks = a.k_scale[i];
+          vs = a.v_scale[i];
+        }
+      };
+      if constexpr (Q8) {
+        load_scales(block_of(p.t0));
+        phys1 = block_of(p.t0 + 1);
+      }
+      for (int t = p.t0; ok && t < p.t1; ++t, ++c) {
+        const int sv = c % R::kV;
+        if constexpr (!Q8) {
+          constexpr int N = kTile / 16 / 128;
+          ok = wait(BAR_VL + sv, (c / R::kV) & 1);
+          if (!ok) break;
+          uint4* const tile = reinterpret_cast<uint4*>(smem_raw + R::kV0 + sv * kTile) + tid;
+          uint4 x[N];
+          uint32_t m = 0;  // largest |V| so far, two bf16 side by side
+#pragma unroll
+          for (int i = 0; i < N; ++i) {
+            x[i] = tile[128 * i];
+            m = __vmaxu2(m, __vmaxu2(__vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu),
+                                     __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu)));
+          }
+          m = min(max(m >> 16, m & 0xffffu), 0x7f7fu);
+          m = all_max(m);
+          if (!ok) break;
+          move_factor(m << 16, 6, 14, 11);
+          const uint64_t f2 = tc::f32x2(pow2i(k), pow2i(k));
+          auto widen = [&](uint32_t w) {
+            float lo, hi;
+            tc::f32x2_split(tc::mul_f32x2(tc::f32x2(__uint_as_float(w << 16),
+                                                    __uint_as_float(w & 0xffff0000u)), f2), lo, hi);
+            return pack_f16x2(lo, hi);
+          };
+#pragma unroll
+          for (int i = 0; i < N; ++i)
+            tile[128 * i] = make_uint4(widen(x[i].x), widen(x[i].y), widen(x[i].z), widen(x[i].w));
+          if (tid == 0) fac[sv] = k;
+          publish(BAR_VF + sv);
+        } else {
+          // a thread's key: 128 codes, 16-byte chunk j of row tid at j ^ (tid & 7)
+          const int rs = c % R::kRaw, sk = c % R::kK;
+          auto read_raw = [&](int raw0, int full, int empty, uint4 (&x)[8]) {
+            ok = wait(full + rs, (c / R::kRaw) & 1);
+            const uint8_t* row = smem_raw + raw0 + rs * R::kRawTile + tid * 128;
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+              x[j] = *reinterpret_cast<const uint4*>(row + ((j ^ (tid & 7)) << 4));
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar(empty + rs));
+          };
+          auto write_row = [&](uint8_t* tile, const uint4 (&x)[8], auto&& widen) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {  // 16 dims: chunks 2 j, 2 j + 1 of the 16-bit row
+              uint8_t* row = tile + (j >> 2) * kSub + tid * 128;
+              uint4 lo, hi;
+              widen(x[j].x, lo.x, lo.y);
+              widen(x[j].y, lo.z, lo.w);
+              widen(x[j].z, hi.x, hi.y);
+              widen(x[j].w, hi.z, hi.w);
+              const int ch = 2 * (j & 3);
+              *reinterpret_cast<uint4*>(row + ((ch ^ (tid & 7)) << 4)) = lo;
+              *reinterpret_cast<uint4*>(row + (((ch + 1) ^ (tid & 7)) << 4)) = hi;
+            }
+          };
+          uint4 x[8];
+          read_raw(R::kRawK0, BAR_RKF, BAR_RKE, x);
+          ok = ok && (c < R::kK || wait(BAR_KE + sk, (c / R::kK - 1) & 1));
+          if (!ok) break;
+          write_row(smem_raw + R::kK0 + sk * kTile, x, [](uint32_t w, uint32_t& lo, uint32_t& hi) {
+            codes8x4_to_f16x2x2<KV>(w, lo, hi);
+            lo = f16x2_to_bf16x2(lo);
+            hi = f16x2_to_bf16x2(hi);
+          });
+          publish(BAR_KF + sk);
+          read_raw(R::kRawV0, BAR_RVF, BAR_RVE, x);
+          ok = ok && (c < R::kV || wait(BAR_VE + sv, (c / R::kV - 1) & 1));
+          if (!ok) break;
+          write_row(smem_raw + R::kV0 + sv * kTile, x, [](uint32_t w, uint32_t& lo, uint32_t& hi) {
+            codes8x4_to_f16x2x2<KV>(w, lo, hi);
+          });
+          // (a scale that is not finite spoils its rows, not the factor)
+          const uint32_t vb = __float_as_uint(vs) & 0x7fffffffu;
+          const uint32_t m = all_max(vb < 0x7f800000u ? vb : 0u);
+          if (!ok) break;
+          move_factor(m, 2, 6, 5);
+          scales[(2 * sv) * kBN + tid] = ks;
+          scales[(2 * sv + 1) * kBN + tid] = vs * pow2i(k);
+          if (tid == 0) fac[sv] = k;
+          publish(BAR_VF + sv);
+          load_scales(phys1);
+          phys1 = block_of(t + 2);
+        }
+      }
+    }
+  } else if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kControlRegs));
     if (warp == 11) {
       // ---------------------------------------------------------- Q producer
       uint32_t n = 0;
-      bool pending = false;
       for (; walk.next(a, p); ++n) {
         if (n > 0 && !wait(BAR_QE, (n - 1) & 1)) break;
         const int tiles = PAIR && p.tok0 + TPT < p.tok1 ? 2 : 1;
@@ -372,16 +557,20 @@ __global__ void __launch_bounds__(kThreads, 1)
                           p.tok0 + i * TPT);
         }
         __syncwarp();
-        pending = true;
       }
-      if (abort_flag && pending) (void)mbar_wait(bar(BAR_QF), (n - 1) & 1);
+      if (*abort_flag && n > 0) (void)mbar_wait(bar(BAR_QF), (n - 1) & 1);
     } else if (warp == 8 || warp == 10) {
       // ---------------------------------------------------------- K, V producers
       const bool is_k = warp == 8;
       const CUtensorMap* map = is_k ? &kmap : &vmap;
-      const int full0 = is_k ? BAR_KF : BAR_VF, empty0 = is_k ? BAR_KE : BAR_VE;
+      const int ST = Q8 ? R::kRaw : is_k ? R::kK : R::kV;
+      const int full0 = Q8 ? (is_k ? BAR_RKF : BAR_RVF) : is_k ? BAR_KF : BAR_VL;
+      const int empty0 = Q8 ? (is_k ? BAR_RKE : BAR_RVE) : is_k ? BAR_KE : BAR_VE;
+      const uint32_t dst0 = base + (Q8 ? (is_k ? R::kRawK0 : R::kRawV0) : is_k ? R::kK0 : R::kV0);
+      constexpr int kBytes = Q8 ? R::kRawTile : kTile;
+      constexpr int kSubs = Q8 ? 1 : D / 64;  // 128-byte columns of a row
       const int oob = a.num_blocks * BS;  // first row past the pool: TMA fills zeros
-      uint32_t c = 0;
+      uint32_t c = 0, s = 0, round = 0;   // tiles so far; stage and use of it
       bool ok = true;
       while (ok && walk.next(a, p)) {
         const long long bt_row = static_cast<long long>(p.owner) * a.max_blocks;
@@ -406,119 +595,135 @@ __global__ void __launch_bounds__(kThreads, 1)
             ids = nxt;
             nxt = load_ids(wb + 32);
           }
-          const int s = c % ST;
-          if (c >= ST && !wait(empty0 + s, (c / ST - 1) & 1)) {
+          if (round > 0 && !wait(empty0 + s, (round - 1) & 1)) {
             ok = false;
             break;
           }
-          const uint32_t dst = is_k ? k_s(s) : v_s(s);
-          if (lane == 0) mbar_arrive_expect_tx(bar(full0 + s), kTile);
+          const uint32_t dst = dst0 + s * kBytes;
+          if (lane == 0) mbar_arrive_expect_tx(bar(full0 + s), kBytes);
 #pragma unroll
           for (int i = 0; i < kBlocks; ++i) {
             const int rc = __shfl_sync(kFull, ids, t * kBlocks - wb + i);
             if (lane == 0) {
 #pragma unroll
-              for (int h = 0; h < D / 64; ++h)
+              for (int h = 0; h < kSubs; ++h)
                 tma_load_3d(dst + h * kSub + i * BS * 128, map, bar(full0 + s), 64 * h, p.kvh, rc);
             }
           }
+          if (++s == ST) {
+            s = 0;
+            ++round;
+          }
         }
       }
-      if (abort_flag) {
+      if (*abort_flag) {
         // let the copies already in flight land before shared memory is released
         for (uint32_t n = c > ST ? c - ST : 0; n < c; ++n)
           (void)mbar_wait(bar(full0 + n % ST), (n / ST) & 1);
       }
     } else {
       // ---------------------------------------------------------- MMA issue
-      constexpr uint32_t kIdescQK = tc::idesc_bf16_f32(kBM, kBN, false, false);
-      constexpr uint32_t kIdescPV = tc::idesc_bf16_f32(kBM, D, false, true);
-      auto issue_s = [&](int i, uint32_t c) {  // S_i = Q K(c)^T
-        const uint32_t q = q_s(PAIR ? i : 0), k = k_s(c % ST);
-        tc::fence_after_sync();
-        if (lane == 0) {
+      // By one thread from end to end: between two MMAs the tensor pipe only has
+      // what is queued, and every warp-wide step in between costs some of that.
+      if (tc::elect_one()) {
+        auto wait = [&](int b, uint32_t parity) {
+          return thread_wait(bar(b), parity, abort_flag, a.err);
+        };
+        constexpr uint32_t kIdescQK = tc::idesc_f32(kBM, kSN, tc::kBf16, false, false);
+        constexpr uint32_t kIdescPV = tc::idesc_f32(kBM, D, tc::kF16, false, true);
+        // Steps of each half so far, over all pieces: step x uses buffer x & 1 for
+        // the (x >> 1)-th time. (Indexed by constants only: they stay in registers.)
+        uint32_t next[2] = {0, 0};  // whose S is to be issued next
+        uint32_t done[2] = {0, 0};  // whose P.V is to be issued next
+        uint32_t ends[2] = {0, 0};  // pieces
+        // S = Q K^T of half i for the 64 keys of a K tile at `k`, once the P that
+        // was there has been used
+        auto issue_s = [&](auto half, uint64_t k) {
+          constexpr int i = decltype(half)::value;
+          const uint32_t x = next[i]++, b = 2 * i + (x & 1);
+          if (x >= 2 && !wait(BAR_O + b, ((x >> 1) - 1) & 1)) return false;
+          const uint64_t q = tc::smem_desc_sw128(q_s(PAIR ? i : 0), 16, 1024);
+          tc::fence_after_sync();
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
-            const uint32_t off = (kk >> 2) * kSub + (kk & 3) * 32;
-            tc::mma_ss(tS(i), tc::smem_desc_sw128(q + off, 16, 1024),
-                       tc::smem_desc_sw128(k + off, 16, 1024), kIdescQK, kk > 0 ? 1u : 0u);
+            // (a descriptor's low bits are the address in units of 16 bytes)
+            const int off = ((kk >> 2) * kSub + (kk & 3) * 32) >> 4;
+            tc::mma_ss(tS(i, x & 1), q + off, k + off, kIdescQK, kk > 0 ? 1u : 0u);
           }
-          tc::commit(bar(BAR_S + i));
-        }
-        __syncwarp();
-      };
-      auto issue_pv = [&](int i, uint32_t c, bool first) {  // O_i (+)= P_i V(c), both terms
-        const uint32_t v = v_s(c % ST);
-        tc::fence_after_sync();
-        if (lane == 0) {
-#pragma unroll 1
-          for (int t = 0; t < 2; ++t) {
+          tc::commit(bar(BAR_S + b));
+          return true;
+        };
+        // O (+)= P V for the 64 keys of a V tile at `v`
+        auto issue_pv = [&](auto half, uint64_t v, bool first) {
+          constexpr int i = decltype(half)::value;
+          const uint32_t x = done[i]++, b = 2 * i + (x & 1);
+          if (!wait(BAR_P + b, (x >> 1) & 1)) return false;
+          if (first && ends[i] > 0 && !wait(BAR_E + i, (ends[i] - 1) & 1)) return false;
+          tc::fence_after_sync();
 #pragma unroll
-            for (int kk = 0; kk < kBN / 16; ++kk)
-              tc::mma_ts(tO(i), tS(i) + 64 * t + kk * 8,
-                         tc::smem_desc_sw128(v + kk * 16 * 128, kSub, 1024), kIdescPV,
-                         !first || kk > 0 || t > 0 ? 1u : 0u);
-          }
-          tc::commit(bar(BAR_O + i));
-        }
-        __syncwarp();
-      };
-      auto commit = [&](int b) {
-        if (lane == 0) tc::commit(bar(b));
-        __syncwarp();
-      };
-      uint32_t c = 0;                // key tiles before the piece
-      uint32_t done0 = 0, done1 = 0;  // tiles of each half so far
-      uint32_t ends0 = 0, ends1 = 0;  // pieces of each half so far
-      auto done = [&](int i) -> uint32_t& { return i ? done1 : done0; };
-      auto ends = [&](int i) -> uint32_t& { return i ? ends1 : ends0; };
-      bool ok = true;
-      for (uint32_t n = 0; ok && walk.next(a, p); ++n) {
-        const int T = p.t1 - p.t0;
-        // halves: the two row tiles (each takes every key tile), or the two
-        // takers of one row tile's key tiles (half i: tiles i, i + 2, ...)
-        const int halves = PAIR ? (p.tok0 + TPT < p.tok1 ? 2 : 1) : min(T, 2);
-        constexpr int kStep = PAIR ? 1 : 2;
-        ok = wait(BAR_QF, n & 1);
-        // the first S of each half: its P of the piece before has been read
-        for (int i = 0; ok && i < halves; ++i) {
-          const int t = PAIR ? 0 : i;
-          ok = (t > 0 || i == 0 ? wait(BAR_KF + (c + t) % ST, ((c + t) / ST) & 1) : true) &&
-               (done(i) == 0 || wait(BAR_O + i, (done(i) - 1) & 1));
-          if (!ok) break;
-          issue_s(i, c + t);
-          if (!PAIR || i == halves - 1) commit(BAR_KE + (c + t) % ST);
-        }
-        if (ok && T <= kStep) commit(BAR_QE);
-        for (int t = 0; ok && t < T; ++t) {
-          const uint32_t ct = c + t, cn = ct + kStep;
-          const bool more = t + kStep < T;
-          ok = wait(BAR_VF + ct % ST, (ct / ST) & 1) &&
-               (!more || wait(BAR_KF + cn % ST, (cn / ST) & 1));
-          for (int i = PAIR ? 0 : t & 1; ok && i < (PAIR ? halves : (t & 1) + 1); ++i) {
-            ok = wait(BAR_P + i, done(i) & 1) &&
-                 (t >= kStep || ends(i) == 0 || wait(BAR_E + i, (ends(i) - 1) & 1));
-            if (!ok) break;
-            issue_pv(i, ct, t < kStep);
-            if (more) {
-              ok = wait(BAR_O + i, done(i) & 1);
-              if (!ok) break;
-              issue_s(i, cn);
+          for (int kk = 0; kk < kSN / 16; ++kk)
+            tc::mma_ts(tO(i), tS(i, x & 1) + kk * 8, v + kk * (16 * 128 >> 4), kIdescPV,
+                       !first || kk > 0 ? 1u : 0u);
+          tc::commit(bar(BAR_O + b));
+          return true;
+        };
+        constexpr std::integral_constant<int, 0> kH0{};
+        constexpr std::integral_constant<int, 1> kH1{};
+        constexpr int kStepDesc = kSN * 128 >> 4;  // from a tile's first 64 keys to its others
+        uint32_t c = 0;  // key tiles before the piece
+        bool ok = true;
+        for (uint32_t n = 0; ok && walk.next(a, p); ++n) {
+          const int T = p.t1 - p.t0;
+          // halves: the two row tiles (each takes every key tile), or the two
+          // takers of one row tile's key tiles (half i: tiles i, i + 2, ...)
+          const int halves = PAIR ? (p.tok0 + TPT < p.tok1 ? 2 : 1) : min(T, 2);
+          auto steps_of = [&](int t) { return p.keys - (p.t0 + t) * kBN > kSN ? 2 : 1; };
+          auto takes = [&](int i, int t) { return PAIR ? i < halves : (t & 1) == i; };
+          ok = wait(BAR_QF, n & 1);
+          for (int t = 0; ok && t < min(T, kStep); ++t) {
+            const uint32_t s = (c + t) % R::kK;
+            ok = wait(BAR_KF + s, ((c + t) / R::kK) & 1);
+            const uint64_t k = tc::smem_desc_sw128(k_s(s), 16, 1024);
+            for (int h = 0; ok && h < steps_of(t); ++h) {
+              if (takes(0, t)) ok = issue_s(kH0, k + h * kStepDesc);
+              if (ok && takes(1, t)) ok = issue_s(kH1, k + h * kStepDesc);
             }
-            ++done(i);
+            if (ok) tc::commit(bar(BAR_KE + s));
           }
-          if (!ok) break;
-          commit(BAR_VE + ct % ST);
-          if (more) commit(BAR_KE + cn % ST);
-          if (more && t + kStep == T - 1) commit(BAR_QE);
+          if (ok && T <= kStep) tc::commit(bar(BAR_QE));
+          for (int t = 0; ok && t < T; ++t) {
+            const uint32_t cn = c + t + kStep;
+            const uint32_t vs = (c + t) % R::kV, ks = cn % R::kK;
+            const int steps = steps_of(t), more = t + kStep < T ? steps_of(t + kStep) : 0;
+            ok = wait(BAR_VF + vs, ((c + t) / R::kV) & 1) &&
+                 (!more || wait(BAR_KF + ks, (cn / R::kK) & 1));
+            const uint64_t v = tc::smem_desc_sw128(v_s(vs), kSub, 1024);
+            const uint64_t k = tc::smem_desc_sw128(k_s(ks), 16, 1024);
+            // per step: P.V of every half, then the S that takes the buffer next.
+            // (A half's other buffer holds an S already: its softmax goes on.)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const bool first = t < kStep && h == 0;
+              if (ok && h < steps && takes(0, t)) ok = issue_pv(kH0, v + h * kStepDesc, first);
+              if (ok && h < steps && takes(1, t)) ok = issue_pv(kH1, v + h * kStepDesc, first);
+              if (ok && h == steps - 1) tc::commit(bar(BAR_VE + vs));
+              if (ok && h < more && takes(0, t)) ok = issue_s(kH0, k + h * kStepDesc);
+              if (ok && h < more && takes(1, t)) ok = issue_s(kH1, k + h * kStepDesc);
+            }
+            if (!ok) break;
+            if (more) tc::commit(bar(BAR_KE + ks));
+            if (more && t + kStep == T - 1) tc::commit(bar(BAR_QE));
+          }
+          c += T;
+          ++ends[0];
+          if (halves > 1) ++ends[1];
         }
-        c += T;
-        for (int i = 0; i < halves; ++i) ++ends(i);
+        if (*abort_flag) {  // no MMA may still run when TMEM is freed
+          tc::commit(bar(BAR_DRAIN));
+          (void)mbar_wait(bar(BAR_DRAIN), 0);
+        }
       }
-      if (abort_flag) {  // no MMA may still run when TMEM is freed
-        commit(BAR_DRAIN);
-        (void)mbar_wait(bar(BAR_DRAIN), 0);
-      }
+      __syncwarp();
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftmaxRegs));
@@ -527,31 +732,57 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int r = 32 * (warp & 3) + lane;  // row of the tile = TMEM lane
     const uint32_t trow = static_cast<uint32_t>(32 * (warp & 3)) << 16;
     const float sl2 = a.scale_log2;
-    constexpr int kStep = PAIR ? 1 : 2;
-    uint32_t done = 0;    // tiles of this half so far
-    uint32_t other = 0;   // first half, one row tile: tiles of the second half so far
+    // P's f16 holds 2^(score - max) times 2^7 (bf16) or times the V scale at up to
+    // 2^7: at most 2^15 with the threshold above, and nothing below 2^-31 of the
+    // row's largest is lost. The sum l takes the same 2^7.
+    constexpr float kLift = Q8 ? 0.f : 7.f;
+    uint32_t x = 0;       // steps of this half so far: buffer x & 1 for the (x >> 1)-th time
+    uint32_t other = 0;   // first half, one row tile: steps of the second half so far
     uint32_t merged = 0;  // pieces in which the second half had tiles
+    uint32_t c0 = 0;      // key tiles before the piece
     bool ok = true;
-    for (uint32_t n = 0; ok && walk.next(a, p); ++n) {
-      const int T = p.t1 - p.t0;
+    for (int T; ok && walk.next(a, p); c0 += T) {
+      T = p.t1 - p.t0;
       if (PAIR && hf == 1 && p.tok0 + TPT >= p.tok1) continue;  // one row tile in this segment
       const int tok = p.tok0 + (PAIR ? hf * TPT : 0) + r / G;
       const bool valid = r < TPT * G && tok < p.tok1;
       const int lim = valid ? min(p.keys, __ldcg(a.plan.row_vis + tok)) : p.keys;  // keys the row sees
       float m_used = -INFINITY, l = 0.f;
-      const int first = PAIR ? 0 : hf;
-      for (int t = first; t < T; t += kStep) {
-        ok = wait(BAR_S + hf, done & 1);
+      int k = 0;  // O holds the sum times 2^k
+      // steps (64 keys) of the piece; this half's: with one row tile, both of every other tile's
+      const int steps = (min(p.t1 * kBN, p.keys) - p.t0 * kBN + kSN - 1) / kSN;
+      const uint32_t x0 = x;
+      for (int st = PAIR ? 0 : 2 * hf; st < steps; st += !PAIR && (st & 1) ? 3 : 1, ++x) {
+        const uint32_t S = tS(hf, x & 1) + trow;
+        const bool begin = x == x0;
+        const uint32_t ct = c0 + (st >> 1);
+        const int sv = ct % R::kV;
+        // the tile's V is converted: its factor and scales are there
+        if ((st & 1) == 0) ok = wait(BAR_VF + sv, (ct / R::kV) & 1);
+        ok = ok && wait(BAR_S + 2 * hf + (x & 1), (x >> 1) & 1);
         if (!ok) break;
         tc::fence_after_sync();
-        uint32_t u[4][32];
+        uint32_t u[2][32];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tc::tmem_ld32(tS(hf) + trow + 32 * c, u[c]);
+        for (int c = 0; c < 2; ++c) tc::tmem_ld32(S + 32 * c, u[c]);
+        const int k_new = fac[sv];
+        const float* const sc = scales + (2 * sv) * kBN + (st & 1) * kSN;
         tc::tmem_wait_ld();
-        const int left = lim - (p.t0 + t) * kBN;  // keys of this tile the row sees
-        if (!__all_sync(kFull, left >= kBN)) {
+        if constexpr (Q8) {  // K scales
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
+          for (int j = 0; j < kSN; j += 4) {
+            const float4 f = *reinterpret_cast<const float4*>(sc + j);
+            uint32_t* w = &u[j >> 5][j & 31];
+            w[0] = __float_as_uint(__uint_as_float(w[0]) * f.x);
+            w[1] = __float_as_uint(__uint_as_float(w[1]) * f.y);
+            w[2] = __float_as_uint(__uint_as_float(w[2]) * f.z);
+            w[3] = __float_as_uint(__uint_as_float(w[3]) * f.w);
+          }
+        }
+        const int left = lim - p.t0 * kBN - st * kSN;  // keys of this step the row sees
+        if (!__all_sync(kFull, left >= kSN)) {
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
 #pragma unroll
             for (int j = 0; j < 32; ++j)
               if (32 * c + j >= left) u[c][j] = __float_as_uint(-INFINITY);
@@ -559,68 +790,70 @@ __global__ void __launch_bounds__(kThreads, 1)
         float mx = -INFINITY;
 #pragma unroll
         for (int j = 0; j < 32; ++j)
-          mx = fmaxf(mx, fmaxf(fmaxf(__uint_as_float(u[0][j]), __uint_as_float(u[1][j])),
-                               fmaxf(__uint_as_float(u[2][j]), __uint_as_float(u[3][j]))));
-        // (scores in base 2 grow with the raw ones, or fall where the scale is negative)
-        const float m_tile = mx * sl2;
-        if (t == first) {
-          m_used = m_tile;
-        } else if (__any_sync(kFull, m_tile > m_used + kRescaleThreshold)) {
-          // raise the maximum and rescale O: its last product must be done
-          ok = wait(BAR_O + hf, (done - 1) & 1);
+          mx = fmaxf(mx, fmaxf(__uint_as_float(u[0][j]), __uint_as_float(u[1][j])));
+        const float m_step = mx * sl2;  // (the scale is positive)
+        if (begin) {
+          m_used = m_step;
+          k = k_new;
+        } else if (k_new != k || __any_sync(kFull, m_step > m_used + kRescaleThreshold)) {
+          // raise the maximum, or follow V's factor: rescale O once its last product is done
+          ok = wait(BAR_O + 2 * hf + ((x - 1) & 1), ((x - 1) >> 1) & 1);
           if (!ok) break;
           tc::fence_after_sync();
-          const float m_new = fmaxf(m_used, m_tile);
+          const float m_new = fmaxf(m_used, m_step);
           // (a row that has seen no key yet has nothing to rescale)
           const float alpha = m_new == -INFINITY ? 1.f : fast_exp2(m_used - m_new);
+          const float beta = alpha * pow2i(min(max(k_new - k, -126), 126));
           uint32_t w[32];
 #pragma unroll
           for (int c = 0; c < kCols; ++c) {
             tc::tmem_ld32(tO(hf) + trow + 32 * c, w);
             tc::tmem_wait_ld();
 #pragma unroll
-            for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(__uint_as_float(w[j]) * alpha);
+            for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(__uint_as_float(w[j]) * beta);
             tc::tmem_st32(tO(hf) + trow + 32 * c, w);
           }
           tc::tmem_wait_st();
           l *= alpha;
           m_used = m_new;
+          k = k_new;
         }
-        // P = 2^(s * scale * log2(e) - m_used) as two bf16 terms; pairs of keys
-        // share one packed FMA and one packed add
-        const float nm = m_used == -INFINITY ? 0.f : -m_used;
+        // P = 2^(s * scale * log2(e) - m_used) in f16; pairs of keys share one
+        // packed FMA and one packed add
+        const float nm = m_used == -INFINITY ? 0.f : kLift - m_used;
         const uint64_t sl2x2 = tc::f32x2(sl2, sl2), nmx2 = tc::f32x2(nm, nm);
         uint64_t lsum = tc::f32x2(0.f, 0.f);
+        uint32_t w[32];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t hi[16], lo[16];
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const uint64_t x = tc::fma_f32x2(
-                tc::f32x2(__uint_as_float(u[c][2 * j]), __uint_as_float(u[c][2 * j + 1])), sl2x2,
-                nmx2);
-            float x0, x1;
-            tc::f32x2_split(x, x0, x1);
-            const float p0 = fast_exp2(x0), p1 = fast_exp2(x1);
-            lsum = tc::add_f32x2(lsum, tc::f32x2(p0, p1));
-            hi[j] = pack_bf16x2(p0, p1);
-            lo[j] = pack_bf16x2(p0 - __uint_as_float(hi[j] << 16),
-                                p1 - __uint_as_float(hi[j] & 0xffff0000u));
+        for (int j = 0; j < 32; ++j) {
+          const uint32_t* e = &u[j >> 4][2 * (j & 15)];
+          const uint64_t y = tc::fma_f32x2(
+              tc::f32x2(__uint_as_float(e[0]), __uint_as_float(e[1])), sl2x2, nmx2);
+          float y0, y1;
+          tc::f32x2_split(y, y0, y1);
+          float p0 = fast_exp2(y0), p1 = fast_exp2(y1);
+          lsum = tc::add_f32x2(lsum, tc::f32x2(p0, p1));
+          if constexpr (Q8) {  // V scales, times 2^k
+            const float2 f = *reinterpret_cast<const float2*>(sc + kBN + 2 * j);
+            p0 *= f.x;
+            p1 *= f.y;
           }
-          tc::tmem_st16(tS(hf) + trow + 16 * c, hi);
-          tc::tmem_st16(tS(hf) + trow + 64 + 16 * c, lo);
+          w[j] = pack_f16x2(p0, p1);
         }
+        tc::tmem_st32(S, w);
         float la, lb;
         tc::f32x2_split(lsum, la, lb);
         l += la + lb;
         tc::tmem_wait_st();
         tc::fence_before_sync();
         __syncwarp();
-        if (lane == 0) mbar_arrive(bar(BAR_P + hf));
-        ++done;
+        if (lane == 0) mbar_arrive(bar(BAR_P + 2 * hf + (x & 1)));
       }
       if (!ok) break;
-      // ---- the piece's partial: (max, sum) and O, unnormalised
+      // ---- the piece's partial: (max, sum) and O, unnormalised. O's factor 2^k
+      // goes into them: O 2^(m - k) stays what it is, and so does l 2^m.
+      m_used -= kLift + static_cast<float>(k);
+      l *= pow2i(k);
       float f0 = 1.f, f1 = 0.f;
       const bool both = !PAIR && T > 1;
       if constexpr (!PAIR) {
@@ -635,8 +868,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             ++merged;
             continue;  // the first half reads this half's O, in the same TMEM lanes
           }
-          other += T / 2;
-          ok = wait(BAR_ML, merged & 1) && wait(BAR_O + 1, (other - 1) & 1);
+          other += steps - static_cast<int>(x - x0);
+          ok = wait(BAR_ML, merged & 1) &&
+               wait(BAR_O + 2 + ((other - 1) & 1), ((other - 1) >> 1) & 1);
           if (!ok) break;
           const float2 o = half_ml[r];
           ++merged;
@@ -649,7 +883,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           continue;
         }
       }
-      ok = wait(BAR_O + hf, (done - 1) & 1);
+      ok = wait(BAR_O + 2 * hf + ((x - 1) & 1), ((x - 1) >> 1) & 1);
       if (!ok) break;
       tc::fence_after_sync();
       const long long row = p.slot * (kBM * a.row_tiles) + (PAIR ? hf * kBM : 0) + r;
@@ -791,11 +1025,11 @@ cudaLaunchConfig_t config(dim3 grid, int threads, size_t smem, cudaStream_t stre
   return cfg;
 }
 
-template <int D, int BS, bool PAIR>
-cudaError_t launch_keys(const SharedArgs& a, const CUtensorMap& qmap, const CUtensorMap& kmap,
+template <int D, int BS, int KV, bool PAIR>
+cudaError_t launch_keys_inst(const SharedArgs& a, const CUtensorMap& qmap, const CUtensorMap& kmap,
                         const CUtensorMap& vmap, cudaStream_t stream) {
-  auto* k = shared_keys_kernel<D, BS, PAIR>;
-  constexpr int smem = Ring<D, PAIR>::kBytes;
+  auto* k = shared_keys_kernel<D, BS, KV, PAIR>;
+  constexpr int smem = Ring<D, KV != kKvBf16, PAIR>::kBytes;
   static bool attr_set[64] = {};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
@@ -809,6 +1043,17 @@ cudaError_t launch_keys(const SharedArgs& a, const CUtensorMap& qmap, const CUte
   cudaLaunchAttribute attr[1];
   const cudaLaunchConfig_t cfg = config(dim3(a.ctas), kThreads, smem, stream, attr);
   return cudaLaunchKernelEx(&cfg, k, qmap, kmap, vmap, a);
+}
+
+template <int D, int KV>
+cudaError_t launch_keys(const SharedArgs& a, const CUtensorMap& qmap, const CUtensorMap& kmap,
+                        const CUtensorMap& vmap, cudaStream_t stream) {
+  const bool pair = a.row_tiles == 2;
+  if (a.block_size == 16)
+    return pair ? launch_keys_inst<D, 16, KV, true>(a, qmap, kmap, vmap, stream)
+                : launch_keys_inst<D, 16, KV, false>(a, qmap, kmap, vmap, stream);
+  return pair ? launch_keys_inst<D, 32, KV, true>(a, qmap, kmap, vmap, stream)
+              : launch_keys_inst<D, 32, KV, false>(a, qmap, kmap, vmap, stream);
 }
 
 }  // namespace
@@ -873,20 +1118,11 @@ cudaError_t launch_shared_plan(const SharedArgs& a, cudaStream_t stream) {
 cudaError_t launch_shared_keys(const SharedArgs& a, const CUtensorMap& qmap,
                                const CUtensorMap& kmap, const CUtensorMap& vmap,
                                cudaStream_t stream) {
-  const bool pair = a.row_tiles == 2;
-  if (a.head_dim == 128 && a.block_size == 16)
-    return pair ? launch_keys<128, 16, true>(a, qmap, kmap, vmap, stream)
-                : launch_keys<128, 16, false>(a, qmap, kmap, vmap, stream);
-  if (a.head_dim == 128 && a.block_size == 32)
-    return pair ? launch_keys<128, 32, true>(a, qmap, kmap, vmap, stream)
-                : launch_keys<128, 32, false>(a, qmap, kmap, vmap, stream);
-  if (a.head_dim == 64 && a.block_size == 16)
-    return pair ? launch_keys<64, 16, true>(a, qmap, kmap, vmap, stream)
-                : launch_keys<64, 16, false>(a, qmap, kmap, vmap, stream);
-  if (a.head_dim == 64 && a.block_size == 32)
-    return pair ? launch_keys<64, 32, true>(a, qmap, kmap, vmap, stream)
-                : launch_keys<64, 32, false>(a, qmap, kmap, vmap, stream);
-  return cudaErrorInvalidValue;
+  if (a.block_size != 16 && a.block_size != 32) return cudaErrorInvalidValue;
+  if (a.kv == kKvE4m3) return launch_keys<128, kKvE4m3>(a, qmap, kmap, vmap, stream);
+  if (a.kv == kKvInt8) return launch_keys<128, kKvInt8>(a, qmap, kmap, vmap, stream);
+  return a.head_dim == 64 ? launch_keys<64, kKvBf16>(a, qmap, kmap, vmap, stream)
+                          : launch_keys<128, kKvBf16>(a, qmap, kmap, vmap, stream);
 }
 
 cudaError_t launch_shared_merge(const SharedArgs& a, cudaStream_t stream) {

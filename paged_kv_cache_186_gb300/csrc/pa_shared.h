@@ -32,6 +32,8 @@ struct SharedArgs {
   const int32_t* prefix_lens;
   void* out;      // (rows, H, D) bf16
   uint32_t* err;
+  const float* k_scale;  // 8-bit caches: (NB, Hkv, bs)
+  const float* v_scale;
   SharedPlan plan;
   float* part_o;    // (slots, rows of a segment, D) fp32, of the shared keys
   float2* part_ml;  // (slots, rows of a segment): max, sum
@@ -44,6 +46,7 @@ struct SharedArgs {
   int row_tiles;        // tiles of a segment: 1 or 2
   int max_segments;     // segments the workspace has room for
   int ctas;             // grid of the launch over the shared keys
+  int kv;               // kKvBf16, kKvE4m3 or kKvInt8
   float scale_log2;
 };
 

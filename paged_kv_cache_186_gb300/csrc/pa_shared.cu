@@ -304,26 +304,24 @@ enum {
 static_assert(NBAR * 8 + kMaxStages * 4 + 8 * 4 + 8 <= 640, "barriers and small arrays");
 
 // Bounded wait that also gives up when another role of the CTA has aborted: by
-// one thread, and by a warp.
-__device__ __forceinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int* abort_flag,
-                                          uint32_t* err) {
-  const unsigned long long t0 = global_timer_ns();
-  while (true) {
+// one thread, and by a warp. (The timer is read and the flag looked at every 64
+// tries, each of which suspends the warp for a while.)
+__device__ __forceinline__ bool thread_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                            uint32_t* err) {
+  unsigned long long t0 = 0;
 #pragma unroll 1
-    for (int i = 0; i < 64; ++i)
-      if (mbar_try_wait(bar, parity)) return true;
+  for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i) {
+    if (i % 64 != 0) continue;
     if (*abort_flag) return false;
-    if (global_timer_ns() - t0 > kWaitLimitNs) {
+    const unsigned long long now = global_timer_ns();
+    if (t0 == 0) t0 = now;
+    if (now - t0 > kWaitLimitNs) {
       *abort_flag = 1;
       report_error(err, PA_DEVERR_WAIT_TIMEOUT);
       return false;
     }
   }
-}
-__device__ __forceinline__ bool thread_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag,
-                                            uint32_t* err) {
-  return mbar_try_wait(bar, parity) || mbar_try_wait(bar, parity) ||
-         wait_slow(bar, parity, abort_flag, err);
+  return true;
 }
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag,
                                           uint32_t* err) {
@@ -460,13 +458,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = wait(BAR_VL + sv, (c / R::kV) & 1);
           if (!ok) break;
           uint4* const tile = reinterpret_cast<uint4*>(smem_raw + R::kV0 + sv * kTile) + tid;
-          uint4 x[N];
           uint32_t m = 0;  // largest |V| so far, two bf16 side by side
-#pragma unroll
+#pragma unroll 8
           for (int i = 0; i < N; ++i) {
-            x[i] = tile[128 * i];
-            m = __vmaxu2(m, __vmaxu2(__vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu),
-                                     __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu)));
+            const uint4 x = tile[128 * i];
+            m = __vmaxu2(m, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
+                                     __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
           }
           m = min(max(m >> 16, m & 0xffffu), 0x7f7fu);
           m = all_max(m);
@@ -479,9 +476,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                     __uint_as_float(w & 0xffff0000u)), f2), lo, hi);
             return pack_f16x2(lo, hi);
           };
-#pragma unroll
-          for (int i = 0; i < N; ++i)
-            tile[128 * i] = make_uint4(widen(x[i].x), widen(x[i].y), widen(x[i].z), widen(x[i].w));
+#pragma unroll 8
+          for (int i = 0; i < N; ++i) {
+            const uint4 x = tile[128 * i];
+            tile[128 * i] = make_uint4(widen(x.x), widen(x.y), widen(x.z), widen(x.w));
+          }
           if (tid == 0) fac[sv] = k;
           publish(BAR_VF + sv);
         } else {
@@ -599,17 +598,19 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = false;
             break;
           }
-          const uint32_t dst = dst0 + s * kBytes;
-          if (lane == 0) mbar_arrive_expect_tx(bar(full0 + s), kBytes);
+          const uint32_t dst = dst0 + s * kBytes, full = bar(full0 + s);
+          int rc[kBlocks];
 #pragma unroll
-          for (int i = 0; i < kBlocks; ++i) {
-            const int rc = __shfl_sync(kFull, ids, t * kBlocks - wb + i);
-            if (lane == 0) {
+          for (int i = 0; i < kBlocks; ++i) rc[i] = __shfl_sync(kFull, ids, t * kBlocks - wb + i);
+          if (tc::elect_one()) {
+            mbar_arrive_expect_tx(full, kBytes);
+#pragma unroll
+            for (int i = 0; i < kBlocks; ++i)
 #pragma unroll
               for (int h = 0; h < kSubs; ++h)
-                tma_load_3d(dst + h * kSub + i * BS * 128, map, bar(full0 + s), 64 * h, p.kvh, rc);
-            }
+                tma_load_3d(dst + h * kSub + i * BS * 128, map, full, 64 * h, p.kvh, rc[i]);
           }
+          __syncwarp();
           if (++s == ST) {
             s = 0;
             ++round;
@@ -632,43 +633,46 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr uint32_t kIdescQK = tc::idesc_f32(kBM, kSN, tc::kBf16, false, false);
         constexpr uint32_t kIdescPV = tc::idesc_f32(kBM, D, tc::kF16, false, true);
         // Steps of each half so far, over all pieces: step x uses buffer x & 1 for
-        // the (x >> 1)-th time. (Indexed by constants only: they stay in registers.)
-        uint32_t next[2] = {0, 0};  // whose S is to be issued next
-        uint32_t done[2] = {0, 0};  // whose P.V is to be issued next
-        uint32_t ends[2] = {0, 0};  // pieces
+        // the (x >> 1)-th time. (The loops over halves and steps stay loops: code
+        // that fits the instruction cache beside the softmax warps' issues faster.)
+        uint32_t next0 = 0, next1 = 0;  // whose S is to be issued next
+        uint32_t done0 = 0, done1 = 0;  // whose P.V is to be issued next
+        uint32_t ends0 = 0, ends1 = 0;  // pieces
         // S = Q K^T of half i for the 64 keys of a K tile at `k`, once the P that
         // was there has been used
-        auto issue_s = [&](auto half, uint64_t k) {
-          constexpr int i = decltype(half)::value;
-          const uint32_t x = next[i]++, b = 2 * i + (x & 1);
+        auto issue_s = [&](int i, uint64_t k) {
+          const uint32_t x = i ? next1 : next0, b = 2 * i + (x & 1);
+          next0 += i ^ 1;
+          next1 += i;
           if (x >= 2 && !wait(BAR_O + b, ((x >> 1) - 1) & 1)) return false;
           const uint64_t q = tc::smem_desc_sw128(q_s(PAIR ? i : 0), 16, 1024);
+          const uint32_t d = tS(i, x & 1);
           tc::fence_after_sync();
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
             // (a descriptor's low bits are the address in units of 16 bytes)
             const int off = ((kk >> 2) * kSub + (kk & 3) * 32) >> 4;
-            tc::mma_ss(tS(i, x & 1), q + off, k + off, kIdescQK, kk > 0 ? 1u : 0u);
+            tc::mma_ss(d, q + off, k + off, kIdescQK, kk > 0 ? 1u : 0u);
           }
           tc::commit(bar(BAR_S + b));
           return true;
         };
         // O (+)= P V for the 64 keys of a V tile at `v`
-        auto issue_pv = [&](auto half, uint64_t v, bool first) {
-          constexpr int i = decltype(half)::value;
-          const uint32_t x = done[i]++, b = 2 * i + (x & 1);
+        auto issue_pv = [&](int i, uint64_t v, bool first) {
+          const uint32_t x = i ? done1 : done0, e = i ? ends1 : ends0, b = 2 * i + (x & 1);
+          done0 += i ^ 1;
+          done1 += i;
           if (!wait(BAR_P + b, (x >> 1) & 1)) return false;
-          if (first && ends[i] > 0 && !wait(BAR_E + i, (ends[i] - 1) & 1)) return false;
+          if (first && e > 0 && !wait(BAR_E + i, (e - 1) & 1)) return false;
+          const uint32_t d = tO(i), pa = tS(i, x & 1);
           tc::fence_after_sync();
 #pragma unroll
           for (int kk = 0; kk < kSN / 16; ++kk)
-            tc::mma_ts(tO(i), tS(i, x & 1) + kk * 8, v + kk * (16 * 128 >> 4), kIdescPV,
+            tc::mma_ts(d, pa + kk * 8, v + kk * (16 * 128 >> 4), kIdescPV,
                        !first || kk > 0 ? 1u : 0u);
           tc::commit(bar(BAR_O + b));
           return true;
         };
-        constexpr std::integral_constant<int, 0> kH0{};
-        constexpr std::integral_constant<int, 1> kH1{};
         constexpr int kStepDesc = kSN * 128 >> 4;  // from a tile's first 64 keys to its others
         uint32_t c = 0;  // key tiles before the piece
         bool ok = true;
@@ -678,16 +682,18 @@ __global__ void __launch_bounds__(kThreads, 1)
           // takers of one row tile's key tiles (half i: tiles i, i + 2, ...)
           const int halves = PAIR ? (p.tok0 + TPT < p.tok1 ? 2 : 1) : min(T, 2);
           auto steps_of = [&](int t) { return p.keys - (p.t0 + t) * kBN > kSN ? 2 : 1; };
-          auto takes = [&](int i, int t) { return PAIR ? i < halves : (t & 1) == i; };
+          auto first_half = [&](int t) { return PAIR ? 0 : t & 1; };
+          auto end_half = [&](int t) { return PAIR ? halves : (t & 1) + 1; };
           ok = wait(BAR_QF, n & 1);
           for (int t = 0; ok && t < min(T, kStep); ++t) {
             const uint32_t s = (c + t) % R::kK;
             ok = wait(BAR_KF + s, ((c + t) / R::kK) & 1);
             const uint64_t k = tc::smem_desc_sw128(k_s(s), 16, 1024);
-            for (int h = 0; ok && h < steps_of(t); ++h) {
-              if (takes(0, t)) ok = issue_s(kH0, k + h * kStepDesc);
-              if (ok && takes(1, t)) ok = issue_s(kH1, k + h * kStepDesc);
-            }
+#pragma unroll 1
+            for (int h = 0; ok && h < steps_of(t); ++h)
+#pragma unroll 1
+              for (int i = first_half(t); ok && i < end_half(t); ++i)
+                ok = issue_s(i, k + h * kStepDesc);
             if (ok) tc::commit(bar(BAR_KE + s));
           }
           if (ok && T <= kStep) tc::commit(bar(BAR_QE));
@@ -701,22 +707,24 @@ __global__ void __launch_bounds__(kThreads, 1)
             const uint64_t k = tc::smem_desc_sw128(k_s(ks), 16, 1024);
             // per step: P.V of every half, then the S that takes the buffer next.
             // (A half's other buffer holds an S already: its softmax goes on.)
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const bool first = t < kStep && h == 0;
-              if (ok && h < steps && takes(0, t)) ok = issue_pv(kH0, v + h * kStepDesc, first);
-              if (ok && h < steps && takes(1, t)) ok = issue_pv(kH1, v + h * kStepDesc, first);
+            const int i0 = first_half(t), i1 = end_half(t);
+#pragma unroll 1
+            for (int h = 0; ok && h < 2; ++h) {
+              const int d = h * kStepDesc;
+#pragma unroll 1
+              for (int i = i0; ok && h < steps && i < i1; ++i)
+                ok = issue_pv(i, v + d, t < kStep && h == 0);
               if (ok && h == steps - 1) tc::commit(bar(BAR_VE + vs));
-              if (ok && h < more && takes(0, t)) ok = issue_s(kH0, k + h * kStepDesc);
-              if (ok && h < more && takes(1, t)) ok = issue_s(kH1, k + h * kStepDesc);
+#pragma unroll 1
+              for (int i = i0; ok && h < more && i < i1; ++i) ok = issue_s(i, k + d);
             }
             if (!ok) break;
             if (more) tc::commit(bar(BAR_KE + ks));
             if (more && t + kStep == T - 1) tc::commit(bar(BAR_QE));
           }
           c += T;
-          ++ends[0];
-          if (halves > 1) ++ends[1];
+          ++ends0;
+          if (halves > 1) ++ends1;
         }
         if (*abort_flag) {  // no MMA may still run when TMEM is freed
           tc::commit(bar(BAR_DRAIN));

@@ -246,7 +246,7 @@ struct PieceWalk {
   }
 };
 
-constexpr int kThreads = 512;  // 2 x 4 softmax warps, K, MMA, V and Q warps, 4 converting warps
+constexpr int kThreads = 512;  // 2 x 4 softmax warps, Q and K, 2 MMA and V warps, 4 converting warps
 // Register split (setmaxnreg) of the launch's 512 x 128.
 constexpr int kSoftmaxRegs = 160;
 constexpr int kControlRegs = 96;
@@ -276,30 +276,32 @@ struct Ring {
   static constexpr int kSmall0 = kHalf0 + (PAIR ? 0 : kBM * 8);
   static constexpr int kBytes = kSmall0 + 640;
   static_assert(kBytes <= 227 * 1024, "shared memory over the per-CTA limit");
+  static_assert(kScale0 % 16 == 0 && kHalf0 % 16 == 0 && kSmall0 % 16 == 0, "16-byte accesses");
 };
 constexpr int kMaxStages = 6;
 constexpr int kMaxRaw = 2;
 
 enum {
   BAR_QF = 0,                    // Q tiles landed
-  BAR_QE,                        // the last S of the segment is done
+  BAR_QE,                        // each half's last S of the segment is done (2 arrivals)
   BAR_KF,                        // + K stage: ready for the MMAs (landed, or widened by 4 warps)
-  BAR_KE = BAR_KF + kMaxStages,  // + K stage: free
+  BAR_KE = BAR_KF + kMaxStages,  // + K stage: free (both halves' MMA threads)
   BAR_VL = BAR_KE + kMaxStages,  // + V stage: landed (bf16)
   BAR_VF = BAR_VL + kMaxStages,  // + V stage: in f16 (4 warps)
-  BAR_VE = BAR_VF + kMaxStages,  // + V stage: free
+  BAR_VE = BAR_VF + kMaxStages,  // + V stage: free (PAIR: 2 arrivals)
   BAR_RKF = BAR_VE + kMaxStages,  // + raw stage: K codes landed
   BAR_RKE = BAR_RKF + kMaxRaw,    // + raw stage: K codes read (4 warps)
   BAR_RVF = BAR_RKE + kMaxRaw,
   BAR_RVE = BAR_RVF + kMaxRaw,
-  BAR_S = BAR_RVE + kMaxRaw,     // + 2 half + buffer: S ready
-  BAR_P = BAR_S + 4,             // + 2 half + buffer: P written (4 warps)
+  BAR_S = BAR_RVE + kMaxRaw,     // + half: S ready
+  BAR_SR = BAR_S + 2,            // + half: S read (4 warps)
+  BAR_P = BAR_SR + 2,            // + 2 half + buffer: P written (4 warps)
   BAR_O = BAR_P + 4,             // + 2 half + buffer: P.V done
   BAR_E = BAR_O + 4,             // + half: O of the piece has been read (4 warps)
   BAR_ML = BAR_E + 2,            // second half's (max, sum) written (4 warps)
   BAR_X,                         // converting warps' maxima written (4 warps)
-  BAR_DRAIN,
-  NBAR
+  BAR_DRAIN,                     // + half
+  NBAR = BAR_DRAIN + 2
 };
 static_assert(NBAR * 8 + kMaxStages * 4 + 8 * 4 + 8 <= 640, "barriers and small arrays");
 
@@ -367,19 +369,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto v_s = [&](int s) { return base + R::kV0 + s * kTile; };
   float* const scales = reinterpret_cast<float*>(smem_raw + R::kScale0);
   float2* const half_ml = reinterpret_cast<float2*>(smem_raw + R::kHalf0);
-  uint64_t* const bars = reinterpret_cast<uint64_t*>(smem_raw + R::kSmall0);
-  int* const fac = reinterpret_cast<int*>(bars + NBAR);              // (kV) V's factor is 2^fac
-  uint32_t* const cmax = reinterpret_cast<uint32_t*>(fac + kMaxStages);  // (2, 4)
-  uint32_t* const tmem_slot = cmax + 8;
+  uint32_t* const cmax = reinterpret_cast<uint32_t*>(smem_raw + R::kSmall0);  // (2, 4), read by fours
+  uint64_t* const bars = reinterpret_cast<uint64_t*>(cmax + 8);
+  int* const fac = reinterpret_cast<int*>(bars + NBAR);  // (kV) V's factor is 2^fac
+  uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(fac + kMaxStages);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
   const uint32_t bar0 = smem_addr(bars);
   auto bar = [&](int i) { return bar0 + 8u * i; };
   if (threadIdx.x == 0) {
     for (int i = 0; i < NBAR; ++i) {
-      const bool warps4 = (i >= BAR_VF && i < BAR_VE) || (i >= BAR_P && i < BAR_O) ||
+      const bool warps4 = (i >= BAR_VF && i < BAR_VE) || (i >= BAR_SR && i < BAR_O) ||
                           (i >= BAR_E && i <= BAR_X) || (i >= BAR_RKE && i < BAR_RVF) ||
                           (i >= BAR_RVE && i < BAR_S) || (Q8 && i >= BAR_KF && i < BAR_KE);
-      mbar_init(bar(i), warps4 ? 4 : 1);
+      const bool both = i == BAR_QE || (i >= BAR_KE && i < BAR_VL) ||
+                        (PAIR && i >= BAR_VE && i < BAR_RKF);
+      mbar_init(bar(i), warps4 ? 4 : both ? 2 : 1);
     }
     *abort_flag = 0;
     fence_barrier_init();
@@ -393,8 +397,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc::fence_after_sync();
   const uint32_t tmem = *tmem_slot;
-  // S of half i in two buffers of 64 columns, each then P in its first 32
-  auto tS = [&](int i, uint32_t b) { return tmem + 128u * i + 64u * b; };
+  // of half i: S (64 columns), two buffers of P (32 each), O. S is free as soon as
+  // the softmax warps have read it, so the next S is made while they work on it.
+  auto tS = [&](int i) { return tmem + 128u * i; };
+  auto tP = [&](int i, uint32_t b) { return tmem + 128u * i + 64u + 32u * b; };
   auto tO = [&](int i) { return tmem + 256u + 128u * i; };
   auto wait = [&](int b, uint32_t parity) { return warp_wait(bar(b), parity, abort_flag, a.err); };
 
@@ -541,25 +547,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   } else if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kControlRegs));
-    if (warp == 11) {
-      // ---------------------------------------------------------- Q producer
-      uint32_t n = 0;
-      for (; walk.next(a, p); ++n) {
-        if (n > 0 && !wait(BAR_QE, (n - 1) & 1)) break;
-        const int tiles = PAIR && p.tok0 + TPT < p.tok1 ? 2 : 1;
-        if (lane == 0) {
-          // a box is G heads of TPT tokens: TPT * G rows of 128 bytes
-          mbar_arrive_expect_tx(bar(BAR_QF), tiles * (D / 64) * TPT * G * 128);
-          for (int i = 0; i < tiles; ++i)
-            for (int c = 0; c < D / 64; ++c)
-              tma_load_3d(q_s(i) + c * kSub, &qmap, bar(BAR_QF), 64 * c, p.kvh * G,
-                          p.tok0 + i * TPT);
-        }
-        __syncwarp();
-      }
-      if (*abort_flag && n > 0) (void)mbar_wait(bar(BAR_QF), (n - 1) & 1);
-    } else if (warp == 8 || warp == 10) {
-      // ---------------------------------------------------------- K, V producers
+    if (warp == 8 || warp == 10) {
+      // ---------------------------------------------------------- Q and K, V producers
       const bool is_k = warp == 8;
       const CUtensorMap* map = is_k ? &kmap : &vmap;
       const int ST = Q8 ? R::kRaw : is_k ? R::kK : R::kV;
@@ -570,8 +559,23 @@ __global__ void __launch_bounds__(kThreads, 1)
       constexpr int kSubs = Q8 ? 1 : D / 64;  // 128-byte columns of a row
       const int oob = a.num_blocks * BS;  // first row past the pool: TMA fills zeros
       uint32_t c = 0, s = 0, round = 0;   // tiles so far; stage and use of it
+      uint32_t n = 0;                     // Q loads so far
       bool ok = true;
       while (ok && walk.next(a, p)) {
+        if (is_k) {
+          if (n > 0 && !wait(BAR_QE, (n - 1) & 1)) break;
+          const int tiles = PAIR && p.tok0 + TPT < p.tok1 ? 2 : 1;
+          if (tc::elect_one()) {
+            // a box is G heads of TPT tokens: TPT * G rows of 128 bytes
+            mbar_arrive_expect_tx(bar(BAR_QF), tiles * (D / 64) * TPT * G * 128);
+            for (int i = 0; i < tiles; ++i)
+              for (int h = 0; h < D / 64; ++h)
+                tma_load_3d(q_s(i) + h * kSub, &qmap, bar(BAR_QF), 64 * h, p.kvh * G,
+                            p.tok0 + i * TPT);
+          }
+          __syncwarp();
+          ++n;
+        }
         const long long bt_row = static_cast<long long>(p.owner) * a.max_blocks;
         const int nblk = p.keys / BS;
         // block ids 32 at a time (lane l: block wb + l, as the pool row of its
@@ -619,116 +623,118 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (*abort_flag) {
         // let the copies already in flight land before shared memory is released
-        for (uint32_t n = c > ST ? c - ST : 0; n < c; ++n)
-          (void)mbar_wait(bar(full0 + n % ST), (n / ST) & 1);
+        if (n > 0) (void)mbar_wait(bar(BAR_QF), (n - 1) & 1);
+        for (uint32_t j = c > ST ? c - ST : 0; j < c; ++j)
+          (void)mbar_wait(bar(full0 + j % ST), (j / ST) & 1);
       }
     } else {
       // ---------------------------------------------------------- MMA issue
-      // By one thread from end to end: between two MMAs the tensor pipe only has
-      // what is queued, and every warp-wide step in between costs some of that.
+      // One warp a half, one thread of it from end to end: between two MMAs the
+      // tensor pipe only has what is queued, and every warp-wide step in between,
+      // or a wait for the other half, costs some of that.
       if (tc::elect_one()) {
+        const int i = warp == 9 ? 0 : 1;
         auto wait = [&](int b, uint32_t parity) {
           return thread_wait(bar(b), parity, abort_flag, a.err);
         };
         constexpr uint32_t kIdescQK = tc::idesc_f32(kBM, kSN, tc::kBf16, false, false);
         constexpr uint32_t kIdescPV = tc::idesc_f32(kBM, D, tc::kF16, false, true);
-        // Steps of each half so far, over all pieces: step x uses buffer x & 1 for
-        // the (x >> 1)-th time. (The loops over halves and steps stay loops: code
-        // that fits the instruction cache beside the softmax warps' issues faster.)
-        uint32_t next0 = 0, next1 = 0;  // whose S is to be issued next
-        uint32_t done0 = 0, done1 = 0;  // whose P.V is to be issued next
-        uint32_t ends0 = 0, ends1 = 0;  // pieces
-        // S = Q K^T of half i for the 64 keys of a K tile at `k`, once the P that
-        // was there has been used
-        auto issue_s = [&](int i, uint64_t k) {
-          const uint32_t x = i ? next1 : next0, b = 2 * i + (x & 1);
-          next0 += i ^ 1;
-          next1 += i;
-          if (x >= 2 && !wait(BAR_O + b, ((x >> 1) - 1) & 1)) return false;
-          const uint64_t q = tc::smem_desc_sw128(q_s(PAIR ? i : 0), 16, 1024);
-          const uint32_t d = tS(i, x & 1);
-          tc::fence_after_sync();
-#pragma unroll
-          for (int kk = 0; kk < D / 16; ++kk) {
-            // (a descriptor's low bits are the address in units of 16 bytes)
-            const int off = ((kk >> 2) * kSub + (kk & 3) * 32) >> 4;
-            tc::mma_ss(d, q + off, k + off, kIdescQK, kk > 0 ? 1u : 0u);
-          }
-          tc::commit(bar(BAR_S + b));
-          return true;
-        };
-        // O (+)= P V for the 64 keys of a V tile at `v`
-        auto issue_pv = [&](int i, uint64_t v, bool first) {
-          const uint32_t x = i ? done1 : done0, e = i ? ends1 : ends0, b = 2 * i + (x & 1);
-          done0 += i ^ 1;
-          done1 += i;
-          if (!wait(BAR_P + b, (x >> 1) & 1)) return false;
-          if (first && e > 0 && !wait(BAR_E + i, (e - 1) & 1)) return false;
-          const uint32_t d = tO(i), pa = tS(i, x & 1);
-          tc::fence_after_sync();
-#pragma unroll
-          for (int kk = 0; kk < kSN / 16; ++kk)
-            tc::mma_ts(d, pa + kk * 8, v + kk * (16 * 128 >> 4), kIdescPV,
-                       !first || kk > 0 ? 1u : 0u);
-          tc::commit(bar(BAR_O + b));
-          return true;
-        };
         constexpr int kStepDesc = kSN * 128 >> 4;  // from a tile's first 64 keys to its others
-        uint32_t c = 0;  // key tiles before the piece
+        const uint64_t q = tc::smem_desc_sw128(q_s(PAIR ? i : 0), 16, 1024);
+        uint32_t xs = 0, xp = 0;  // steps of this half so far: S issued, P.V issued
+        uint32_t pieces = 0;      // of this half, so far
+        uint32_t c = 0;           // key tiles before the piece
+        // A barrier is asked for its phases one after the other, and none may pass
+        // unseen (the parity would be that of another). So K tiles are waited for in
+        // turn, also those the other half takes (the copies may land in any order),
+        // and every stage is given back by both threads. V tiles are converted in
+        // turn, and a half's own are never more than three apart; with two V stages
+        // (8-bit codes) S of a tile implies that V of the tile before is there.
+        uint32_t kw = 0;
+        auto wait_k = [&](uint32_t tile) {
+          for (; kw <= tile; ++kw) {
+            const uint32_t s = kw % R::kK;
+            if (!wait(BAR_KF + s, (kw / R::kK) & 1)) return false;
+            if (kw < tile) mbar_arrive(bar(BAR_KE + s));  // the other half's
+          }
+          return true;
+        };
         bool ok = true;
         for (uint32_t n = 0; ok && walk.next(a, p); ++n) {
           const int T = p.t1 - p.t0;
-          // halves: the two row tiles (each takes every key tile), or the two
-          // takers of one row tile's key tiles (half i: tiles i, i + 2, ...)
-          const int halves = PAIR ? (p.tok0 + TPT < p.tok1 ? 2 : 1) : min(T, 2);
+          const bool mine = i == 0 || (PAIR ? p.tok0 + TPT < p.tok1 : T > 1);
           auto steps_of = [&](int t) { return p.keys - (p.t0 + t) * kBN > kSN ? 2 : 1; };
-          auto first_half = [&](int t) { return PAIR ? 0 : t & 1; };
-          auto end_half = [&](int t) { return PAIR ? halves : (t & 1) + 1; };
           ok = wait(BAR_QF, n & 1);
-          for (int t = 0; ok && t < min(T, kStep); ++t) {
-            const uint32_t s = (c + t) % R::kK;
-            ok = wait(BAR_KF + s, ((c + t) / R::kK) & 1);
-            const uint64_t k = tc::smem_desc_sw128(k_s(s), 16, 1024);
-#pragma unroll 1
-            for (int h = 0; ok && h < steps_of(t); ++h)
-#pragma unroll 1
-              for (int i = first_half(t); ok && i < end_half(t); ++i)
-                ok = issue_s(i, k + h * kStepDesc);
-            if (ok) tc::commit(bar(BAR_KE + s));
-          }
-          if (ok && T <= kStep) tc::commit(bar(BAR_QE));
-          for (int t = 0; ok && t < T; ++t) {
-            const uint32_t cn = c + t + kStep;
-            const uint32_t vs = (c + t) % R::kV, ks = cn % R::kK;
-            const int steps = steps_of(t), more = t + kStep < T ? steps_of(t + kStep) : 0;
-            ok = wait(BAR_VF + vs, ((c + t) / R::kV) & 1) &&
-                 (!more || wait(BAR_KF + ks, (cn / R::kK) & 1));
-            const uint64_t v = tc::smem_desc_sw128(v_s(vs), kSub, 1024);
-            const uint64_t k = tc::smem_desc_sw128(k_s(ks), 16, 1024);
-            // per step: P.V of every half, then the S that takes the buffer next.
-            // (A half's other buffer holds an S already: its softmax goes on.)
-            const int i0 = first_half(t), i1 = end_half(t);
-#pragma unroll 1
-            for (int h = 0; ok && h < 2; ++h) {
-              const int d = h * kStepDesc;
-#pragma unroll 1
-              for (int i = i0; ok && h < steps && i < i1; ++i)
-                ok = issue_pv(i, v + d, t < kStep && h == 0);
-              if (ok && h == steps - 1) tc::commit(bar(BAR_VE + vs));
-#pragma unroll 1
-              for (int i = i0; ok && h < more && i < i1; ++i) ok = issue_s(i, k + d);
+          if (!mine) {  // stages need this half's arrivals all the same
+            for (int t = 0; ok && t < T; ++t) {
+              const uint32_t vs = (c + t) % R::kV;
+              ok = wait_k(c + t);
+              if (ok) mbar_arrive(bar(BAR_KE + (c + t) % R::kK));
+              ok = ok && wait(BAR_VF + vs, ((c + t) / R::kV) & 1);
+              if (ok && PAIR) mbar_arrive(bar(BAR_VE + vs));
             }
-            if (!ok) break;
-            if (more) tc::commit(bar(BAR_KE + ks));
-            if (more && t + kStep == T - 1) tc::commit(bar(BAR_QE));
+            if (ok) mbar_arrive(bar(BAR_QE));
+            c += T;
+            continue;
+          }
+          // The next S in the order of this half's key tiles t (PAIR: all; else i,
+          // i + 2, ...) and their steps h, once the one before has been read.
+          int st = PAIR ? 0 : i, sh = 0;
+          auto issue_s = [&]() {
+            const uint32_t cs = c + st, s = cs % R::kK;
+            if (!wait_k(cs)) return false;
+            if (xs > 0 && !wait(BAR_SR + i, (xs - 1) & 1)) return false;
+            ++xs;
+            const uint64_t k = tc::smem_desc_sw128(k_s(s), 16, 1024) + sh * kStepDesc;
+            const uint32_t d = tS(i);
+            tc::fence_after_sync();
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              // (a descriptor's low bits are the address in units of 16 bytes)
+              const int off = ((kk >> 2) * kSub + (kk & 3) * 32) >> 4;
+              tc::mma_ss(d, q + off, k + off, kIdescQK, kk > 0 ? 1u : 0u);
+            }
+            tc::commit(bar(BAR_S + i));
+            if (++sh == steps_of(st)) {
+              tc::commit(bar(BAR_KE + s));
+              sh = 0;
+              st += kStep;
+              if (st >= T) tc::commit(bar(BAR_QE));
+            }
+            return true;
+          };
+          ok = ok && issue_s();
+          for (int t = PAIR ? 0 : i; ok && t < T; t += kStep) {
+            const uint32_t cv = c + t, s = cv % R::kV;
+            const int steps = steps_of(t);
+#pragma unroll 1
+            for (int h = 0; ok && h < steps; ++h) {
+              if (st < T) ok = issue_s();
+              ok = ok && (h > 0 || wait(BAR_VF + s, (cv / R::kV) & 1));
+              // O (+)= P V for 64 keys
+              const uint32_t b = 2 * i + (xp & 1);
+              const bool first = t < kStep && h == 0;
+              ok = ok && wait(BAR_P + b, (xp >> 1) & 1) &&
+                   (!first || pieces == 0 || wait(BAR_E + i, (pieces - 1) & 1));
+              if (!ok) break;
+              const uint64_t v = tc::smem_desc_sw128(v_s(s), kSub, 1024) + h * kStepDesc;
+              const uint32_t d = tO(i), pa = tP(i, xp & 1);
+              ++xp;
+              tc::fence_after_sync();
+#pragma unroll
+              for (int kk = 0; kk < kSN / 16; ++kk)
+                tc::mma_ts(d, pa + kk * 8, v + kk * (16 * 128 >> 4), kIdescPV,
+                           !first || kk > 0 ? 1u : 0u);
+              tc::commit(bar(BAR_O + b));
+            }
+            if (ok) tc::commit(bar(BAR_VE + s));
           }
           c += T;
-          ++ends0;
-          if (halves > 1) ++ends1;
+          ++pieces;
         }
         if (*abort_flag) {  // no MMA may still run when TMEM is freed
-          tc::commit(bar(BAR_DRAIN));
-          (void)mbar_wait(bar(BAR_DRAIN), 0);
+          tc::commit(bar(BAR_DRAIN + i));
+          (void)mbar_wait(bar(BAR_DRAIN + i), 0);
         }
       }
       __syncwarp();
@@ -744,7 +750,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // 2^7: at most 2^15 with the threshold above, and nothing below 2^-31 of the
     // row's largest is lost. The sum l takes the same 2^7.
     constexpr float kLift = Q8 ? 0.f : 7.f;
-    uint32_t x = 0;       // steps of this half so far: buffer x & 1 for the (x >> 1)-th time
+    uint32_t x = 0;       // steps of this half so far: P buffer x & 1 for the (x >> 1)-th time
     uint32_t other = 0;   // first half, one row tile: steps of the second half so far
     uint32_t merged = 0;  // pieces in which the second half had tiles
     uint32_t c0 = 0;      // key tiles before the piece
@@ -761,13 +767,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int steps = (min(p.t1 * kBN, p.keys) - p.t0 * kBN + kSN - 1) / kSN;
       const uint32_t x0 = x;
       for (int st = PAIR ? 0 : 2 * hf; st < steps; st += !PAIR && (st & 1) ? 3 : 1, ++x) {
-        const uint32_t S = tS(hf, x & 1) + trow;
+        const uint32_t S = tS(hf) + trow;
         const bool begin = x == x0;
         const uint32_t ct = c0 + (st >> 1);
         const int sv = ct % R::kV;
-        // the tile's V is converted: its factor and scales are there
-        if ((st & 1) == 0) ok = wait(BAR_VF + sv, (ct / R::kV) & 1);
-        ok = ok && wait(BAR_S + 2 * hf + (x & 1), (x >> 1) & 1);
+        ok = wait(BAR_S + hf, x & 1);
+        // the tile's V is converted: its factor and scales are there (asked for only
+        // after S: V of the tiles before is then known to be)
+        if ((st & 1) == 0) ok = ok && wait(BAR_VF + sv, (ct / R::kV) & 1);
         if (!ok) break;
         tc::fence_after_sync();
         uint32_t u[2][32];
@@ -776,6 +783,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int k_new = fac[sv];
         const float* const sc = scales + (2 * sv) * kBN + (st & 1) * kSN;
         tc::tmem_wait_ld();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(BAR_SR + hf));
         if constexpr (Q8) {  // K scales
 #pragma unroll
           for (int j = 0; j < kSN; j += 4) {
@@ -848,7 +858,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           w[j] = pack_f16x2(p0, p1);
         }
-        tc::tmem_st32(S, w);
+        // (the buffer's P of two steps ago has been used)
+        ok = x < 2 || wait(BAR_O + 2 * hf + (x & 1), ((x >> 1) - 1) & 1);
+        if (!ok) break;
+        tc::fence_after_sync();
+        tc::tmem_st32(tP(hf, x & 1) + trow, w);
         float la, lb;
         tc::f32x2_split(lsum, la, lb);
         l += la + lb;

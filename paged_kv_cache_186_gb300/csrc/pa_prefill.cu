@@ -335,15 +335,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int id0 = n * kBlocksPerTile - wbase;
       if (n >= NS && !warp_wait(bar(empty0 + s), ((n - NS) / NS) & 1, &abort_flag, a.err)) break;
       const uint32_t dst = is_k ? k_s(s) : v_s(s);
-      if (lane == 0) mbar_arrive_expect_tx(bar(full0 + s), kTileBytes);
+      int c[kBlocksPerTile];
 #pragma unroll
-      for (int i = 0; i < kBlocksPerTile; ++i) {
-        const int c = __shfl_sync(0xffffffffu, cur_ids, id0 + i);
-        if (lane == 0) {
-          tma_load_3d(dst + i * BS * 128, map, bar(full0 + s), 0, kvh, c);
-          tma_load_3d(dst + kSub + i * BS * 128, map, bar(full0 + s), 64, kvh, c);
+      for (int i = 0; i < kBlocksPerTile; ++i) c[i] = __shfl_sync(0xffffffffu, cur_ids, id0 + i);
+      if (tc::elect_one()) {
+        mbar_arrive_expect_tx(bar(full0 + s), kTileBytes);
+#pragma unroll
+        for (int i = 0; i < kBlocksPerTile; ++i) {
+          tma_load_3d(dst + i * BS * 128, map, bar(full0 + s), 0, kvh, c[i]);
+          tma_load_3d(dst + kSub + i * BS * 128, map, bar(full0 + s), 64, kvh, c[i]);
         }
       }
+      __syncwarp();
       ++issued;
     }
     if (abort_flag) {
@@ -357,13 +360,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     constexpr uint32_t kIdescPV = tc::idesc_bf16_f32(kBM, kD, false, true);
     auto issue_s = [&](int i, int n) {  // S_i = Q_i K(n)^T
       const int ks = n % kStages;
+      const uint64_t qd = tc::smem_desc_sw128(q_s(SPLIT ? 0 : i), 16, 1024);
+      const uint64_t kd = tc::smem_desc_sw128(k_s(ks), 16, 1024);
       tc::fence_after_sync();
-      if (lane == 0) {
+      if (tc::elect_one()) {
 #pragma unroll
         for (int kk = 0; kk < kD / 16; ++kk) {
-          const uint32_t off = (kk >> 2) * kSub + (kk & 3) * 32;
-          tc::mma_ss(tS(i), tc::smem_desc_sw128(q_s(SPLIT ? 0 : i) + off, 16, 1024),
-                     tc::smem_desc_sw128(k_s(ks) + off, 16, 1024), kIdescQK, kk > 0 ? 1u : 0u);
+          // (a descriptor's low bits are the address in units of 16 bytes)
+          const int off = ((kk >> 2) * kSub + (kk & 3) * 32) >> 4;
+          tc::mma_ss(tS(i), qd + off, kd + off, kIdescQK, kk > 0 ? 1u : 0u);
         }
         tc::commit(bar(BAR_S + i));
       }
@@ -372,14 +377,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto issue_pv = [&](int i, int n) {  // O_i += P_i V(n)
       const int vs = n % kStages;
       const int terms = two_term(SPLIT ? 0 : i, n) ? 2 : 1;
+      const uint64_t vd = tc::smem_desc_sw128(v_s(vs), kSub, 1024);
       tc::fence_after_sync();
-      if (lane == 0) {
+      if (tc::elect_one()) {
 #pragma unroll 1
         for (int t = 0; t < terms; ++t) {  // P = hi (columns 0..63) + lo (64..127)
 #pragma unroll
           for (int kk = 0; kk < kBN / 16; ++kk)
-            tc::mma_ts(tO(i), tS(i) + 64 * t + kk * 8,
-                       tc::smem_desc_sw128(v_s(vs) + kk * 16 * 128, kSub, 1024), kIdescPV,
+            tc::mma_ts(tO(i), tS(i) + 64 * t + kk * 8, vd + kk * (16 * 128 >> 4), kIdescPV,
                        (n >= nstep || kk > 0 || t > 0) ? 1u : 0u);
         }
         tc::commit(bar(BAR_O + i));
@@ -391,14 +396,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (ok) {
       for (int i = 0; i < (SPLIT ? 1 : 2); ++i)
         if (Tq[i] > 0) issue_s(i, 0);
-      if (lane == 0) tc::commit(bar(BAR_KE + 0));
+      if (tc::elect_one()) tc::commit(bar(BAR_KE + 0));
       __syncwarp();
     }
     if (SPLIT && ok && T > 1) {  // the second half's first tile
       ok = warp_wait(bar(BAR_KF + 1), 0, &abort_flag, a.err);
       if (ok) {
         issue_s(1, 1);
-        if (lane == 0) tc::commit(bar(BAR_KE + 1));
+        if (tc::elect_one()) tc::commit(bar(BAR_KE + 1));
         __syncwarp();
       }
     }
@@ -461,14 +466,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       if (!ok) break;
-      if (lane == 0) {
+      if (tc::elect_one()) {
         tc::commit(bar(BAR_VE + s));
         if (more) tc::commit(bar(BAR_KE + s1));
       }
       __syncwarp();
     }
     if (abort_flag) {  // make sure no MMA is still running before TMEM is freed
-      if (lane == 0) tc::commit(bar(BAR_DRAIN));
+      if (tc::elect_one()) tc::commit(bar(BAR_DRAIN));
       __syncwarp();
       (void)mbar_wait(bar(BAR_DRAIN), 0);
     }

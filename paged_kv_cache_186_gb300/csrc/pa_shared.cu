@@ -77,15 +77,24 @@ __device__ __forceinline__ T block_scan(T v, T* warp_part, Op op) {
   return v;
 }
 
+// Groups whose bounds and keys the plan keeps in shared memory; more are read
+// back from the workspace.
+constexpr int kPlanGroups = 512;
+
 __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedArgs a) {
   __shared__ long long part[32];
-  // everything this launch writes may still be read by the call before it
-  grid_dependency_wait();
-  grid_launch_dependents();
+  __shared__ int s_cu[kPlanGroups + 1], s_keys[kPlanGroups];
   const SharedPlan& p = a.plan;
   const int G = a.num_groups, B = a.batch, tid = threadIdx.x;
   const int warp = tid >> 5, lane = tid & 31;
   const bool decode = a.context_lens != nullptr;
+  const bool few = G <= kPlanGroups;
+  int* const cu = few ? s_cu : p.cu;
+  int* const keys = few ? s_keys : p.keys;
+  // what this launch writes may still be read by the call before it, and its
+  // inputs written by the launch before it
+  grid_dependency_wait();
+  grid_launch_dependents();
   auto kv_len = [&](int b) {
     return decode ? min(max(a.context_lens[b], 0), a.len_cap)
                   : min(max(a.cu_k[b + 1] - a.cu_k[b], 0), a.len_cap);
@@ -98,15 +107,20 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedA
     long long v = i <= G ? min(max(a.cu_groups[i], 0), B) : 0;
     v = block_scan<long long>(v, part, [](long long x, long long y) { return max(x, y); });
     v = max(v, carry);
-    if (i <= G) p.cu[i] = static_cast<int>(v);
+    if (i <= G) cu[i] = static_cast<int>(v);
     carry = max(carry, part[31]);
     __syncthreads();
   }
 
   // ---- shared keys of each group, and the first of its sequences that has them all
   for (int g = warp; g < G; g += kPlanThreads / 32) {
-    const int b0 = p.cu[g], b1 = p.cu[g + 1];
+    const int b0 = cu[g], b1 = cu[g + 1];
     const int want = min(max(a.prefix_lens[g], 0), a.len_cap) / a.block_size * a.block_size;
+    int t0 = b0, t1 = b1;
+    if (!decode) {
+      t0 = min(max(a.cu_q[b0], 0), a.rows);
+      t1 = min(max(a.cu_q[b1], t0), a.rows);
+    }
     int owner = -1;
     for (int base = b0; want > 0 && base < b1 && owner < 0; base += 32) {
       const int b = base + lane;
@@ -114,15 +128,12 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedA
       if (has) owner = base + __ffs(has) - 1;
     }
     if (lane == 0) {
-      int t0 = b0, t1 = b1;
-      if (!decode) {
-        t0 = min(max(a.cu_q[b0], 0), a.rows);
-        t1 = min(max(a.cu_q[b1], t0), a.rows);
-      }
+      const int k = owner >= 0 && t1 > t0 ? want : 0;
+      keys[g] = k;
+      if (few) p.keys[g] = k;
       p.tok[2 * g] = t0;
       p.tok[2 * g + 1] = t1;
       p.owner[g] = max(owner, 0);
-      p.keys[g] = owner >= 0 && t1 > t0 ? want : 0;
     }
   }
   __syncthreads();
@@ -133,10 +144,10 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedA
   for (int base = 0; base < G; base += kPlanThreads) {
     const int g = base + tid;
     long long s = 0, u = 0;
-    if (g < G && p.keys[g] > 0) {
+    if (g < G && keys[g] > 0) {
       s = static_cast<long long>((p.tok[2 * g + 1] - p.tok[2 * g] + per_seg - 1) / per_seg) *
           a.num_kv_heads;
-      u = s * ((p.keys[g] + kBN - 1) / kBN);
+      u = s * ((keys[g] + kBN - 1) / kBN);
     }
     auto add = [](long long x, long long y) { return x + y; };
     const long long si = block_scan<long long>(s, part, add);
@@ -164,16 +175,16 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedA
     int lo = 0, hi = G;  // last g with cu[g] <= b
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (p.cu[mid] <= b) lo = mid; else hi = mid;
+      if (cu[mid] <= b) lo = mid; else hi = mid;
     }
-    return fits && p.cu[lo] <= b && b < p.cu[lo + 1] && p.keys[lo] > 0 ? lo : -1;
+    return fits && cu[lo] <= b && b < cu[lo + 1] && keys[lo] > 0 ? lo : -1;
   };
   if (decode) {
     for (int b = tid; b < B; b += kPlanThreads) {
       const int g = group_of(b);
       p.row_vis[b] = kv_len(b);
       p.row_grp[b] = g;
-      p.row_start[b] = g >= 0 ? p.keys[g] : 0;
+      p.row_start[b] = g >= 0 ? keys[g] : 0;
     }
     return;
   }
@@ -183,7 +194,7 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedA
   for (int b = warp; b < B; b += kPlanThreads / 32) {
     const int q0 = a.cu_q[b], q1 = min(a.cu_q[b + 1], a.rows);
     const int kv = kv_len(b), cached = max(kv - (a.cu_q[b + 1] - q0), 0);
-    const int g = group_of(b), start = g >= 0 ? p.keys[g] : 0;
+    const int g = group_of(b), start = g >= 0 ? keys[g] : 0;
     for (int t = max(q0, 0) + lane; t < q1; t += 32) {
       p.row_vis[t] = min(cached + (t - q0) + 1, kv);
       p.row_grp[t] = g;
@@ -357,6 +368,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   // The launch before this one (each sequence's own keys) let it start only
   // after the plan was complete, and works beside it: its results are waited
   // for at the end, on behalf of the merge.
+  // (The merge waits for all of this launch: it may be launched at any time.)
+  grid_launch_dependents();
   PieceWalk walk(a);
   const uint32_t base = smem_addr(smem_raw);
   if (walk.u >= walk.u1 || (base & 1023u) != 0) {  // (swizzled tiles need the alignment asked for)
@@ -952,84 +965,111 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ============================================================ merge
 constexpr int kMergeWarps = 4;
 
-// One row and head on D/4 lanes, 16 bytes of O each: its parts of the shared
-// keys in order, then its own keys' result.
-template <int D>
+// Every query head of a row and kv head: the parts of the shared keys and the
+// row's own keys' result, folded into a running (max, sum, O). O of a head is on
+// D/4 lanes, 16 bytes each; such a team of lanes takes four heads at a time, so
+// that the look-up of the parts is shared and their reads are under way together.
+// WIDE: all teams of the CTA share a row's parts, team s taking the parts s, s +
+// teams, ..., and fold each other's results through shared memory; otherwise
+// every team has a row of its own.
+template <int D, bool WIDE>
 __global__ void __launch_bounds__(kMergeWarps * 32) shared_merge_kernel(const SharedArgs a) {
-  constexpr int LPR = D / 4, RPW = 32 / LPR;
+  constexpr int LPR = D / 4, kTeams = kMergeWarps * 32 / LPR;
+  constexpr int kHeads = 4;  // at a time
+  __shared__ float2 team_ml[WIDE ? kTeams : 1][kHeads];
+  __shared__ float4 team_o[WIDE ? kTeams : 1][kHeads][WIDE ? LPR : 1];
   grid_dependency_wait();
   grid_launch_dependents();
-  const int lane = threadIdx.x & 31, sub = lane % LPR;
-  const long long rh = (static_cast<long long>(blockIdx.x) * kMergeWarps + (threadIdx.x >> 5)) * RPW +
-                       lane / LPR;
-  const bool in = rh < static_cast<long long>(a.rows) * a.num_heads;
-  const int t = in ? static_cast<int>(rh / a.num_heads) : 0;
-  const int h = in ? static_cast<int>(rh % a.num_heads) : 0;
-  const int vis = in ? a.plan.row_vis[t] : -1;
-  const int g = in ? a.plan.row_grp[t] : -1;
-  const bool own = vis > (in ? a.plan.row_start[t] : 0);
+  const int team = threadIdx.x / LPR, sub = threadIdx.x % LPR;
+  const long long w = WIDE ? blockIdx.x : static_cast<long long>(blockIdx.x) * kTeams + team;
+  if (w >= static_cast<long long>(a.rows) * a.num_kv_heads) return;
+  const int t = static_cast<int>(w / a.num_kv_heads), kvh = static_cast<int>(w % a.num_kv_heads);
+  const int vis = a.plan.row_vis[t], g = a.plan.row_grp[t], start = a.plan.row_start[t];
+  if (vis < 0) return;
+  const bool own = vis > start;
 
   // ---- the row's parts: slots seg + c of the CTAs c that own units of its segment
-  long long first = 0;
-  int n = 0, r = 0;
+  long long first = 0;  // row of the first part
+  int n = 0;
+  const long long step = kBM * a.row_tiles;
   if (g >= 0) {
-    const int per_seg = a.tokens_per_tile * a.row_tiles, kvh = h / a.group;
+    const int per_seg = a.tokens_per_tile * a.row_tiles;
     const int i = t - a.plan.tok[2 * g], rows = a.plan.tok[2 * g + 1] - a.plan.tok[2 * g];
-    const int R = (rows + per_seg - 1) / per_seg, KT = (a.plan.keys[g] + kBN - 1) / kBN;
+    const int R = (rows + per_seg - 1) / per_seg, KT = (start + kBN - 1) / kBN;
     const int s = kvh * R + i / per_seg, q = i % per_seg;
-    r = q / a.tokens_per_tile * kBM + q % a.tokens_per_tile * a.group + h % a.group;
     const long long N = a.plan.unit[a.num_groups], W = working_ctas(N, a.ctas);
     const long long u0 = a.plan.unit[g] + static_cast<long long>(s) * KT;
     const long long c0 = ((u0 + 1) * W - 1) / N, c1 = ((u0 + KT) * W - 1) / N;
-    first = a.plan.seg[g] + s + c0;
+    first = (a.plan.seg[g] + s + c0) * step + q / a.tokens_per_tile * kBM +
+            q % a.tokens_per_tile * a.group;
     n = static_cast<int>(c1 - c0 + 1);
   }
-  auto part = [&](int j) { return (first + j) * (kBM * a.row_tiles) + r; };
-
-  // ---- (max, sum): a lane takes every LPR-th part, then the row's lanes combine
-  float M = -INFINITY, L = 0.f;
-  auto fold = [&](float m, float l) {
-    const float m2 = fmaxf(M, m);
-    if (m2 != -INFINITY) {
-      L = L * fast_exp2(M - m2) + l * fast_exp2(m - m2);
-      M = m2;
-    }
-  };
-  for (int j = sub; j < n; j += LPR) {
-    const float2 ml = __ldcg(a.part_ml + part(j));
-    fold(ml.x, ml.y);
-  }
-  float2 mine = make_float2(-INFINITY, 0.f);
-  if (own) mine = __ldcg(a.own_ml + rh);
-  if (own && sub == 0) fold(mine.x, mine.y);
+  const long long rh = static_cast<long long>(t) * a.num_heads + kvh * a.group;
+  for (int h0 = 0; h0 < a.group; h0 += kHeads) {
+    float M[kHeads], L[kHeads];
+    float4 acc[kHeads];
 #pragma unroll
-  for (int o = LPR / 2; o >= 1; o >>= 1) {
-    const float m = __shfl_xor_sync(kFull, M, o), l = __shfl_xor_sync(kFull, L, o);
-    fold(m, l);
+    for (int h = 0; h < kHeads; ++h) {
+      M[h] = -INFINITY;
+      L[h] = 0.f;
+      acc[h] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    auto fold = [&](int h, const float2& ml, const float4& x) {
+      const float m = fmaxf(M[h], ml.x);
+      // (nothing so far, or nothing in this part: a factor of 0, not of 2^(inf - inf))
+      const float f0 = M[h] == -INFINITY ? 0.f : fast_exp2(M[h] - m);
+      const float f1 = ml.x == -INFINITY ? 0.f : fast_exp2(ml.x - m);
+      M[h] = m;
+      L[h] = L[h] * f0 + ml.y * f1;
+      acc[h].x = acc[h].x * f0 + x.x * f1;
+      acc[h].y = acc[h].y * f0 + x.y * f1;
+      acc[h].z = acc[h].z * f0 + x.z * f1;
+      acc[h].w = acc[h].w * f0 + x.w * f1;
+    };
+#pragma unroll 2
+    for (int j = WIDE ? team : 0; j < n; j += WIDE ? kTeams : 1) {
+      const long long row = first + j * step + h0;
+      float2 ml[kHeads];
+      float4 x[kHeads];
+#pragma unroll
+      for (int h = 0; h < kHeads; ++h)
+        if (h0 + h < a.group) {
+          ml[h] = __ldcg(a.part_ml + row + h);
+          x[h] = __ldcg(reinterpret_cast<const float4*>(a.part_o + (row + h) * D) + sub);
+        }
+#pragma unroll
+      for (int h = 0; h < kHeads; ++h)
+        if (h0 + h < a.group) fold(h, ml[h], x[h]);
+    }
+    if constexpr (WIDE) {
+      if (h0 > 0) __syncthreads();  // the heads before have been read
+#pragma unroll
+      for (int h = 0; h < kHeads; ++h) {
+        if (sub == 0) team_ml[team][h] = make_float2(M[h], L[h]);
+        team_o[team][h][sub] = acc[h];
+      }
+      __syncthreads();
+    }
+#pragma unroll
+    for (int h = 0; h < kHeads; ++h) {
+      if (h0 + h >= a.group) break;
+      if (WIDE && h != team) continue;  // (there are at least four teams)
+      if constexpr (WIDE) {
+        for (int s = 0; s < kTeams; ++s)
+          if (s != team) fold(h, team_ml[s][h], team_o[s][h][sub]);
+      }
+      const long long row = rh + h0 + h;
+      if (own)
+        fold(h, __ldcg(a.own_ml + row),
+             __ldcg(reinterpret_cast<const float4*>(a.own_o + row * D) + sub));
+      // no keys: zeros; a NaN stays
+      const float inv = L[h] > 0.f ? 1.f / L[h] : L[h];
+      uint2 o;
+      o.x = pack_bf16x2(acc[h].x * inv, acc[h].y * inv);
+      o.y = pack_bf16x2(acc[h].z * inv, acc[h].w * inv);
+      reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + row * D)[sub] = o;
+    }
   }
-
-  // ---- O
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  auto add = [&](float m, const float4& x) {
-    const float f = m == -INFINITY ? 0.f : fast_exp2(m - M);
-    acc.x += f * x.x;
-    acc.y += f * x.y;
-    acc.z += f * x.z;
-    acc.w += f * x.w;
-  };
-#pragma unroll 4
-  for (int j = 0; j < n; ++j) {
-    const long long row = part(j);
-    const float m = __ldcg(&a.part_ml[row].x);
-    add(m, __ldcg(reinterpret_cast<const float4*>(a.part_o + row * D) + sub));
-  }
-  if (own) add(mine.x, __ldcg(reinterpret_cast<const float4*>(a.own_o + rh * D) + sub));
-  if (vis < 0) return;
-  const float inv = L > 0.f ? 1.f / L : (L == 0.f ? 0.f : L);  // no keys: zeros; NaN stays
-  uint2 w;
-  w.x = pack_bf16x2(acc.x * inv, acc.y * inv);
-  w.y = pack_bf16x2(acc.z * inv, acc.w * inv);
-  reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + rh * D)[sub] = w;
 }
 
 // ============================================================ host side
@@ -1147,16 +1187,22 @@ cudaError_t launch_shared_keys(const SharedArgs& a, const CUtensorMap& qmap,
                           : launch_keys<128, kKvBf16>(a, qmap, kmap, vmap, stream);
 }
 
+// A row to a team needs enough rows to hide the chain of look-ups and reads of
+// one: below 16 warps an SM, a row to a CTA.
 cudaError_t launch_shared_merge(const SharedArgs& a, cudaStream_t stream) {
-  const long long rh = static_cast<long long>(a.rows) * a.num_heads;
-  const long long per_cta = kMergeWarps * (128 / a.head_dim);
-  const long long grid = (rh + per_cta - 1) / per_cta;
+  const long long rows = static_cast<long long>(a.rows) * a.num_kv_heads;
+  const long long teams = kMergeWarps * (128 / a.head_dim);
+  const bool wide = rows < 16LL * a.ctas * (128 / a.head_dim);
+  const long long grid = wide ? rows : (rows + teams - 1) / teams;
   if (grid > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   cudaLaunchAttribute attr[1];
   const cudaLaunchConfig_t cfg =
       config(dim3(static_cast<unsigned>(grid)), kMergeWarps * 32, 0, stream, attr);
-  return a.head_dim == 64 ? cudaLaunchKernelEx(&cfg, shared_merge_kernel<64>, a)
-                          : cudaLaunchKernelEx(&cfg, shared_merge_kernel<128>, a);
+  if (a.head_dim == 64)
+    return wide ? cudaLaunchKernelEx(&cfg, shared_merge_kernel<64, true>, a)
+                : cudaLaunchKernelEx(&cfg, shared_merge_kernel<64, false>, a);
+  return wide ? cudaLaunchKernelEx(&cfg, shared_merge_kernel<128, true>, a)
+              : cudaLaunchKernelEx(&cfg, shared_merge_kernel<128, false>, a);
 }
 
 }  // namespace pa

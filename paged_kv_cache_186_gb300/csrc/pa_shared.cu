@@ -316,29 +316,35 @@ enum {
 };
 static_assert(NBAR * 8 + kMaxStages * 4 + 8 * 4 + 8 <= 640, "barriers and small arrays");
 
-// Bounded wait that also gives up when another role of the CTA has aborted: by
+// Bounded waits that also give up when another role of the CTA has aborted: by
 // one thread, and by a warp. (The timer is read and the flag looked at every 64
 // tries, each of which suspends the warp for a while.)
+__device__ __forceinline__ bool give_up(uint32_t i, unsigned long long& t0, volatile int* abort_flag,
+                                        uint32_t* err) {
+  if (i % 64 != 0) return false;
+  if (*abort_flag) return true;
+  const unsigned long long now = global_timer_ns();
+  if (t0 == 0) t0 = now;
+  if (now - t0 <= kWaitLimitNs) return false;
+  *abort_flag = 1;
+  report_error(err, PA_DEVERR_WAIT_TIMEOUT);
+  return true;
+}
 __device__ __forceinline__ bool thread_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag,
                                             uint32_t* err) {
   unsigned long long t0 = 0;
 #pragma unroll 1
-  for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i) {
-    if (i % 64 != 0) continue;
-    if (*abort_flag) return false;
-    const unsigned long long now = global_timer_ns();
-    if (t0 == 0) t0 = now;
-    if (now - t0 > kWaitLimitNs) {
-      *abort_flag = 1;
-      report_error(err, PA_DEVERR_WAIT_TIMEOUT);
-      return false;
-    }
-  }
+  for (uint32_t i = 1; !mbar_try_wait(bar, parity); ++i)
+    if (give_up(i, t0, abort_flag, err)) return false;
   return true;
 }
 __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatile int* abort_flag,
                                           uint32_t* err) {
-  return __all_sync(kFull, thread_wait(bar, parity, abort_flag, err));
+  unsigned long long t0 = 0;
+#pragma unroll 1
+  for (uint32_t i = 1; !__all_sync(kFull, mbar_try_wait(bar, parity)); ++i)
+    if (__any_sync(kFull, give_up(i, t0, abort_flag, err))) return false;
+  return true;
 }
 
 __device__ __forceinline__ float pow2i(int k) {  // 2^k, k in [-126, 127]
@@ -477,12 +483,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           ok = wait(BAR_VL + sv, (c / R::kV) & 1);
           if (!ok) break;
           uint4* const tile = reinterpret_cast<uint4*>(smem_raw + R::kV0 + sv * kTile) + tid;
+          // (read once: the MMAs leave shared memory little room, see above)
+          uint4 x[N];
           uint32_t m = 0;  // largest |V| so far, two bf16 side by side
-#pragma unroll 8
+#pragma unroll
           for (int i = 0; i < N; ++i) {
-            const uint4 x = tile[128 * i];
-            m = __vmaxu2(m, __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu),
-                                     __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu)));
+            x[i] = tile[128 * i];
+            m = __vmaxu2(m, __vmaxu2(__vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu),
+                                     __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu)));
           }
           m = min(max(m >> 16, m & 0xffffu), 0x7f7fu);
           m = all_max(m);
@@ -495,11 +503,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                                                     __uint_as_float(w & 0xffff0000u)), f2), lo, hi);
             return pack_f16x2(lo, hi);
           };
-#pragma unroll 8
-          for (int i = 0; i < N; ++i) {
-            const uint4 x = tile[128 * i];
-            tile[128 * i] = make_uint4(widen(x.x), widen(x.y), widen(x.z), widen(x.w));
-          }
+#pragma unroll
+          for (int i = 0; i < N; ++i)
+            tile[128 * i] = make_uint4(widen(x[i].x), widen(x[i].y), widen(x[i].z), widen(x[i].w));
           if (tid == 0) fac[sv] = k;
           publish(BAR_VF + sv);
         } else {
@@ -804,10 +810,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int j = 0; j < kSN; j += 4) {
             const float4 f = *reinterpret_cast<const float4*>(sc + j);
             uint32_t* w = &u[j >> 5][j & 31];
-            w[0] = __float_as_uint(__uint_as_float(w[0]) * f.x);
-            w[1] = __float_as_uint(__uint_as_float(w[1]) * f.y);
-            w[2] = __float_as_uint(__uint_as_float(w[2]) * f.z);
-            w[3] = __float_as_uint(__uint_as_float(w[3]) * f.w);
+            auto mul2 = [&](int e, float f0, float f1) {
+              float x0, x1;
+              tc::f32x2_split(tc::mul_f32x2(tc::f32x2(__uint_as_float(w[e]), __uint_as_float(w[e + 1])),
+                                            tc::f32x2(f0, f1)), x0, x1);
+              w[e] = __float_as_uint(x0);
+              w[e + 1] = __float_as_uint(x1);
+            };
+            mul2(0, f.x, f.y);
+            mul2(2, f.z, f.w);
           }
         }
         const int left = lim - p.t0 * kBN - st * kSN;  // keys of this step the row sees
@@ -818,11 +829,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = 0; j < 32; ++j)
               if (32 * c + j >= left) u[c][j] = __float_as_uint(-INFINITY);
         }
-        float mx = -INFINITY;
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
         for (int j = 0; j < 32; ++j)
-          mx = fmaxf(mx, fmaxf(__uint_as_float(u[0][j]), __uint_as_float(u[1][j])));
-        const float m_step = mx * sl2;  // (the scale is positive)
+          mx[j & 3] = fmaxf(mx[j & 3], fmaxf(__uint_as_float(u[0][j]), __uint_as_float(u[1][j])));
+        // (the scale is positive)
+        const float m_step = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;
         if (begin) {
           m_used = m_step;
           k = k_new;
@@ -853,31 +865,33 @@ __global__ void __launch_bounds__(kThreads, 1)
         // packed FMA and one packed add
         const float nm = m_used == -INFINITY ? 0.f : kLift - m_used;
         const uint64_t sl2x2 = tc::f32x2(sl2, sl2), nmx2 = tc::f32x2(nm, nm);
-        uint64_t lsum = tc::f32x2(0.f, 0.f);
+        uint64_t lsum[2] = {tc::f32x2(0.f, 0.f), tc::f32x2(0.f, 0.f)};
         uint32_t w[32];
 #pragma unroll
-        for (int j = 0; j < 32; ++j) {
-          const uint32_t* e = &u[j >> 4][2 * (j & 15)];
-          const uint64_t y = tc::fma_f32x2(
-              tc::f32x2(__uint_as_float(e[0]), __uint_as_float(e[1])), sl2x2, nmx2);
-          float y0, y1;
-          tc::f32x2_split(y, y0, y1);
-          float p0 = fast_exp2(y0), p1 = fast_exp2(y1);
-          lsum = tc::add_f32x2(lsum, tc::f32x2(p0, p1));
-          if constexpr (Q8) {  // V scales, times 2^k
-            const float2 f = *reinterpret_cast<const float2*>(sc + kBN + 2 * j);
-            p0 *= f.x;
-            p1 *= f.y;
+        for (int j = 0; j < 32; j += 2) {
+          float4 f;
+          if constexpr (Q8) f = *reinterpret_cast<const float4*>(sc + kBN + 2 * j);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t* e = &u[j >> 4][2 * ((j + i) & 15)];
+            const uint64_t y = tc::fma_f32x2(
+                tc::f32x2(__uint_as_float(e[0]), __uint_as_float(e[1])), sl2x2, nmx2);
+            float p0, p1;
+            tc::f32x2_split(y, p0, p1);
+            p0 = fast_exp2(p0);
+            p1 = fast_exp2(p1);
+            const uint64_t pp = tc::f32x2(p0, p1);
+            lsum[i] = tc::add_f32x2(lsum[i], pp);
+            if constexpr (Q8)  // V scales, times 2^k
+              tc::f32x2_split(tc::mul_f32x2(pp, i ? tc::f32x2(f.z, f.w) : tc::f32x2(f.x, f.y)), p0, p1);
+            w[j + i] = pack_f16x2(p0, p1);
           }
-          w[j] = pack_f16x2(p0, p1);
         }
-        // (the buffer's P of two steps ago has been used)
-        ok = x < 2 || wait(BAR_O + 2 * hf + (x & 1), ((x >> 1) - 1) & 1);
-        if (!ok) break;
-        tc::fence_after_sync();
+        // (The buffer's P of two steps ago has been used: its product was issued
+        // before this step's S by the same thread, whose commit of S covers it.)
         tc::tmem_st32(tP(hf, x & 1) + trow, w);
         float la, lb;
-        tc::f32x2_split(lsum, la, lb);
+        tc::f32x2_split(tc::add_f32x2(lsum[0], lsum[1]), la, lb);
         l += la + lb;
         tc::tmem_wait_st();
         tc::fence_before_sync();

@@ -413,8 +413,9 @@ pa_status encode_q_map(CUtensorMap* map, const void* q, int head_dim, int num_he
 pa::SharedArgs shared_args(const SharedCall& call, const pa::SharedLayout& layout,
                            const pa_kv_cache* cache, const int32_t* block_tables, int32_t max_blocks,
                            int32_t batch, int32_t rows, int32_t num_heads, int len_cap, float scale,
-                           void* out, uint32_t* err) {
+                           void* out, uint32_t* err, const int32_t* context_lens) {
   pa::SharedArgs a{};
+  a.context_lens = context_lens;
   a.block_tables = block_tables;
   a.cu_groups = call.cu_groups;
   a.prefix_lens = call.prefix_lens;
@@ -579,9 +580,12 @@ pa_status decode_common(const void* q, const pa_kv_cache* cache, const int32_t* 
   }
   if (shared != nullptr) {
     pa::SharedArgs h = shared_args(*shared, layout, cache, block_tables, max_blocks_per_seq, batch,
-                                   batch, num_heads, cap, scale, out, dev->err);
-    h.context_lens = context_lens;
+                                   batch, num_heads, cap, scale, out, dev->err, context_lens);
+    h.slot_o = a.part_o;
+    h.slot_ml = reinterpret_cast<const float2*>(a.part_ml);
+    h.slot_rows = a.slot_rows;
     a.own_start = h.plan.row_start;
+    a.own_parts = h.own_parts;
     a.own_o = h.own_o;
     a.own_ml = reinterpret_cast<float*>(h.own_ml);
     CUtensorMap qmap, ksub, vsub;
@@ -797,7 +801,7 @@ pa_status prefill_common(const void* q, const pa_kv_cache* cache, const int32_t*
     const cudaStream_t strm = static_cast<cudaStream_t>(stream);
     pa::SharedArgs h = shared_args(*shared, layout, cache, block_tables, max_blocks_per_seq, batch,
                                    total_q, num_heads, decode_len_cap(cache, max_blocks_per_seq, 0),
-                                   scale, out, dev->err);
+                                   scale, out, dev->err, nullptr);
     h.cu_q = cu_seqlens_q;
     h.cu_k = cu_seqlens_k;
     a.own_start = h.plan.row_start;

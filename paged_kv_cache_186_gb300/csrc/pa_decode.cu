@@ -731,6 +731,9 @@ struct SegParts {
 // against 60.0 us with groups, 57-64 parts 111-112 us against 102-103 us.
 constexpr int kMergeGroup = 16;
 constexpr int kGroupedAbove = 32;
+// pa_decode_shared: segments of up to this many parts are merged by the launch
+// that merges them with the shared keys' (no arrivals, no last arriver here)
+constexpr int kLeaveParts = 8;
 
 // Parts j0, j0 + stride, ... (n of them) of a segment, for a merge.
 struct PartList {
@@ -1299,8 +1302,16 @@ __global__ void __launch_bounds__(NW * 32, 3)
     if (nx.valid) fetch_q<D, Q8>(a, nx.b, nx.kvh, lane, qraw);
     write_warp_result<D, Q8, SC, SH>(a, cp.b, cp.kvh, whole, 2 * gw + (cp.lo == 0 ? 1 : 0), lane, m_run,
                               l_run, 1.f / vfac, acc);
-    if (!whole) {
-      const SegParts sp = seg_parts(prefix, B, Hkv, cp.b, cp.kvh, W, cost);
+    bool merge = !whole;
+    SegParts sp{gw, 1};
+    if (!whole) sp = seg_parts(prefix, B, Hkv, cp.b, cp.kvh, W, cost);
+    if constexpr (SH) {
+      merge = sp.n > kLeaveParts;
+      if (cp.lo == 0 && lane == 0)
+        a.own_parts[static_cast<long long>(cp.b) * Hkv + cp.kvh] =
+            whole || merge ? make_int2(-1, 1) : make_int2(static_cast<int>(sp.w0), sp.n);
+    }
+    if (merge) {
       // Every other part already arrived (counted after publishing its
       // partial): this warp is the segment's last. Its own partial is read
       // only by its own lanes, so it needs neither a fence nor an arrival:

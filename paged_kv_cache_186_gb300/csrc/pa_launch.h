@@ -76,10 +76,12 @@ struct DecodeArgs {
   float2* head_ml;
   // pa_decode_shared: attend to each sequence's keys from own_start (B) on and
   // leave (max, sum) (B, H, 2) and unnormalised O (B, H, D) in fp32 instead of
-  // bf16 rows; NULL otherwise
+  // bf16 rows; NULL otherwise. A segment of few parts is left in the partial slots,
+  // for the merge behind it: own_parts (B, Hkv) says where a result is.
   const int* own_start;
   float* own_o;
   float* own_ml;
+  int2* own_parts;
   int persistent_ctas;        // > 0: persistent kernel with this many CTAs
   int blocks_per_split, num_splits;  // grid-split path
   int kv;                     // kKvBf16, kKvE4m3 or kKvInt8

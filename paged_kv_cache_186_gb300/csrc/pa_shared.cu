@@ -49,6 +49,13 @@ constexpr int kSN = 64;   // keys per step: half a tile
 constexpr int kSub = 128 * kBM;  // bytes of a 64-dim (128-byte-wide) column of a 128-row tile
 
 // ============================================================ plan
+// CTA c of the W that work owns units [c N / W, (c+1) N / W). A unit is dearer
+// than a CTA's start only where there are very few of them, so as many CTAs as
+// there are units work.
+__device__ __forceinline__ long long working_ctas(long long units, int ctas) {
+  return max(1LL, min(units, static_cast<long long>(ctas)));
+}
+
 constexpr int kPlanThreads = 1024;
 
 // Inclusive scan of one value per thread of the CTA (op associative).
@@ -170,6 +177,22 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedA
     p.unit[G] = fits ? units : 0;
   }
 
+  __syncthreads();
+
+  // ---- the partials of each segment: one of every CTA that owns units of it
+  const long long W = working_ctas(units, a.ctas);
+  for (int i = tid; fits && i < segs; i += kPlanThreads) {
+    int lo = 0, hi = G;  // last g with seg[g] <= i (groups without segments come before it)
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (p.seg[mid] <= i) lo = mid; else hi = mid;
+    }
+    const long long KT = (keys[lo] + kBN - 1) / kBN;
+    const long long u0 = p.unit[lo] + (i - p.seg[lo]) * KT;
+    const long long c0 = ((u0 + 1) * W - 1) / units, c1 = ((u0 + KT) * W - 1) / units;
+    p.parts[i] = make_int2(static_cast<int>(i + c0), static_cast<int>(c1 - c0 + 1));
+  }
+
   // ---- rows
   auto group_of = [&](int b) {  // the group that holds sequence b, if it shares keys
     int lo = 0, hi = G;  // last g with cu[g] <= b
@@ -204,13 +227,6 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedA
 }
 
 // ============================================================ shared keys
-// CTA c of the W that work owns units [c N / W, (c+1) N / W). A unit is dearer
-// than a CTA's start only where there are very few of them, so as many CTAs as
-// there are units work.
-__device__ __forceinline__ long long working_ctas(long long units, int ctas) {
-  return max(1LL, min(units, static_cast<long long>(ctas)));
-}
-
 // One CTA's run of key tiles within one segment.
 struct Piece {
   int kvh, tok0, tok1;  // kv head; rows: first of the segment, past the group's last
@@ -981,15 +997,16 @@ constexpr int kMergeWarps = 4;
 
 // Every query head of a row and kv head: the parts of the shared keys and the
 // row's own keys' result, folded into a running (max, sum, O). O of a head is on
-// D/4 lanes, 16 bytes each; such a team of lanes takes four heads at a time, so
+// D/4 lanes, 16 bytes each; such a team of lanes takes some heads at a time, so
 // that the look-up of the parts is shared and their reads are under way together.
 // WIDE: all teams of the CTA share a row's parts, team s taking the parts s, s +
 // teams, ..., and fold each other's results through shared memory; otherwise
 // every team has a row of its own.
 template <int D, bool WIDE>
-__global__ void __launch_bounds__(kMergeWarps * 32) shared_merge_kernel(const SharedArgs a) {
+__global__ void __launch_bounds__(kMergeWarps * 32, WIDE ? 4 : 8)
+    shared_merge_kernel(const SharedArgs a) {
   constexpr int LPR = D / 4, kTeams = kMergeWarps * 32 / LPR;
-  constexpr int kHeads = 4;  // at a time
+  constexpr int kHeads = WIDE ? 4 : 2;  // at a time
   __shared__ float2 team_ml[WIDE ? kTeams : 1][kHeads];
   __shared__ float4 team_o[WIDE ? kTeams : 1][kHeads][WIDE ? LPR : 1];
   grid_dependency_wait();
@@ -999,26 +1016,37 @@ __global__ void __launch_bounds__(kMergeWarps * 32) shared_merge_kernel(const Sh
   if (w >= static_cast<long long>(a.rows) * a.num_kv_heads) return;
   const int t = static_cast<int>(w / a.num_kv_heads), kvh = static_cast<int>(w % a.num_kv_heads);
   const int vis = a.plan.row_vis[t], g = a.plan.row_grp[t], start = a.plan.row_start[t];
+  // (no own keys: what is left here from another call is not used)
+  int2 mine = make_int2(-1, 1);
+  if (a.own_parts != nullptr) mine = a.own_parts[w];
   if (vis < 0) return;
   const bool own = vis > start;
 
-  // ---- the row's parts: slots seg + c of the CTAs c that own units of its segment
-  long long first = 0;  // row of the first part
+  // ---- the row's parts of the shared keys, then those of its own
+  long long first = 0;  // row of the first
   int n = 0;
   const long long step = kBM * a.row_tiles;
   if (g >= 0) {
     const int per_seg = a.tokens_per_tile * a.row_tiles;
     const int i = t - a.plan.tok[2 * g], rows = a.plan.tok[2 * g + 1] - a.plan.tok[2 * g];
-    const int R = (rows + per_seg - 1) / per_seg, KT = (start + kBN - 1) / kBN;
-    const int s = kvh * R + i / per_seg, q = i % per_seg;
-    const long long N = a.plan.unit[a.num_groups], W = working_ctas(N, a.ctas);
-    const long long u0 = a.plan.unit[g] + static_cast<long long>(s) * KT;
-    const long long c0 = ((u0 + 1) * W - 1) / N, c1 = ((u0 + KT) * W - 1) / N;
-    first = (a.plan.seg[g] + s + c0) * step + q / a.tokens_per_tile * kBM +
-            q % a.tokens_per_tile * a.group;
-    n = static_cast<int>(c1 - c0 + 1);
+    const int R = (rows + per_seg - 1) / per_seg, q = i % per_seg;
+    const int2 parts = a.plan.parts[a.plan.seg[g] + kvh * R + i / per_seg];
+    first = parts.x * step + q / a.tokens_per_tile * kBM + q % a.tokens_per_tile * a.group;
+    n = parts.y;
   }
   const long long rh = static_cast<long long>(t) * a.num_heads + kvh * a.group;
+  // own part j: in own_o, or in the decode kernel's slots (the segment's first
+  // part is in its warp's odd one)
+  const float2* own_ml = a.own_ml + rh;
+  const float* own_o = a.own_o + rh * D;
+  if (own && mine.x >= 0) {
+    own_ml = a.slot_ml + (2LL * mine.x + 1) * a.slot_rows;
+    own_o = a.slot_o + (2LL * mine.x + 1) * a.slot_rows * D;
+  }
+  const int n_own = own ? mine.y : 0;
+  // Part 0 is read ahead of the shared keys' parts (WIDE: by the team that has the
+  // fewest of those); parts j > 0 lie 2 j - 1 slots further.
+  const int own_team = WIDE ? n % kTeams : 0;
   for (int h0 = 0; h0 < a.group; h0 += kHeads) {
     float M[kHeads], L[kHeads];
     float4 acc[kHeads];
@@ -1040,20 +1068,40 @@ __global__ void __launch_bounds__(kMergeWarps * 32) shared_merge_kernel(const Sh
       acc[h].z = acc[h].z * f0 + x.z * f1;
       acc[h].w = acc[h].w * f0 + x.w * f1;
     };
-#pragma unroll 2
-    for (int j = WIDE ? team : 0; j < n; j += WIDE ? kTeams : 1) {
-      const long long row = first + j * step + h0;
-      float2 ml[kHeads];
-      float4 x[kHeads];
+    auto read = [&](const float2* ml, const float* o, float2 (&m)[kHeads], float4 (&x)[kHeads]) {
 #pragma unroll
       for (int h = 0; h < kHeads; ++h)
         if (h0 + h < a.group) {
-          ml[h] = __ldcg(a.part_ml + row + h);
-          x[h] = __ldcg(reinterpret_cast<const float4*>(a.part_o + (row + h) * D) + sub);
+          m[h] = __ldcg(ml + h0 + h);
+          x[h] = __ldcg(reinterpret_cast<const float4*>(o + static_cast<long long>(h0 + h) * D) + sub);
         }
+    };
+    auto fold_all = [&](const float2 (&m)[kHeads], const float4 (&x)[kHeads]) {
 #pragma unroll
       for (int h = 0; h < kHeads; ++h)
-        if (h0 + h < a.group) fold(h, ml[h], x[h]);
+        if (h0 + h < a.group) fold(h, m[h], x[h]);
+    };
+    const bool have_own = n_own > 0 && (!WIDE || team == own_team);
+    float2 om[kHeads];
+    float4 ox[kHeads];
+    if (have_own) read(own_ml, own_o, om, ox);
+#pragma unroll 2
+    for (int j = WIDE ? team : 0; j < n; j += WIDE ? kTeams : 1) {
+      const long long row = first + j * step;
+      float2 m[kHeads];
+      float4 x[kHeads];
+      read(a.part_ml + row, a.part_o + row * D, m, x);
+      fold_all(m, x);
+    }
+    if (have_own) fold_all(om, ox);
+#pragma unroll 1
+    for (int j = 1; j < n_own; ++j) {
+      if (WIDE && (j + own_team) % kTeams != team) continue;
+      const long long row = (2LL * j - 1) * a.slot_rows;
+      float2 m[kHeads];
+      float4 x[kHeads];
+      read(own_ml + row, own_o + row * D, m, x);
+      fold_all(m, x);
     }
     if constexpr (WIDE) {
       if (h0 > 0) __syncthreads();  // the heads before have been read
@@ -1072,16 +1120,12 @@ __global__ void __launch_bounds__(kMergeWarps * 32) shared_merge_kernel(const Sh
         for (int s = 0; s < kTeams; ++s)
           if (s != team) fold(h, team_ml[s][h], team_o[s][h][sub]);
       }
-      const long long row = rh + h0 + h;
-      if (own)
-        fold(h, __ldcg(a.own_ml + row),
-             __ldcg(reinterpret_cast<const float4*>(a.own_o + row * D) + sub));
       // no keys: zeros; a NaN stays
       const float inv = L[h] > 0.f ? 1.f / L[h] : L[h];
       uint2 o;
       o.x = pack_bf16x2(acc[h].x * inv, acc[h].y * inv);
       o.y = pack_bf16x2(acc[h].z * inv, acc[h].w * inv);
-      reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + row * D)[sub] = o;
+      reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + (rh + h0 + h) * D)[sub] = o;
     }
   }
 }
@@ -1154,10 +1198,12 @@ SharedLayout shared_layout(size_t base, int rows, int num_heads, int num_kv_head
   const size_t rh = static_cast<size_t>(rows) * num_heads;
   l.plan = up(base);
   const size_t plan_bytes = (static_cast<size_t>(num_groups) + 1) * (sizeof(long long) + 6 * sizeof(int)) +
+                            static_cast<size_t>(l.max_segments) * sizeof(int2) +
                             3 * static_cast<size_t>(rows) * sizeof(int);
   l.part_ml = up(l.plan + plan_bytes);
   l.part_o = up(l.part_ml + part_rows * sizeof(float2));
-  l.own_ml = up(l.part_o + part_rows * head_dim * sizeof(float));
+  l.own_parts = up(l.part_o + part_rows * head_dim * sizeof(float));
+  l.own_ml = up(l.own_parts + static_cast<size_t>(rows) * num_kv_heads * sizeof(int2));
   l.own_o = up(l.own_ml + rh * sizeof(float2));
   l.bytes = l.own_o + rh * head_dim * sizeof(float);
   return l;
@@ -1167,7 +1213,8 @@ void shared_pointers(SharedArgs& a, const SharedLayout& l, void* workspace) {
   char* const ws = static_cast<char*>(workspace);
   const int g1 = a.num_groups + 1;
   a.plan.unit = reinterpret_cast<long long*>(ws + l.plan);
-  a.plan.cu = reinterpret_cast<int*>(a.plan.unit + g1);
+  a.plan.parts = reinterpret_cast<int2*>(a.plan.unit + g1);
+  a.plan.cu = reinterpret_cast<int*>(a.plan.parts + l.max_segments);
   a.plan.keys = a.plan.cu + g1;
   a.plan.owner = a.plan.keys + g1;
   a.plan.seg = a.plan.owner + g1;
@@ -1177,6 +1224,7 @@ void shared_pointers(SharedArgs& a, const SharedLayout& l, void* workspace) {
   a.plan.row_start = a.plan.row_grp + a.rows;
   a.part_ml = reinterpret_cast<float2*>(ws + l.part_ml);
   a.part_o = reinterpret_cast<float*>(ws + l.part_o);
+  a.own_parts = a.context_lens != nullptr ? reinterpret_cast<int2*>(ws + l.own_parts) : nullptr;
   a.own_ml = reinterpret_cast<float2*>(ws + l.own_ml);
   a.own_o = reinterpret_cast<float*>(ws + l.own_o);
   a.tokens_per_tile = l.tokens_per_tile;

@@ -18,6 +18,7 @@ struct SharedPlan {
   int* tok;         // (groups, 2) the group's rows: first, past the last
   int* seg;         // (groups+1) segments (kv head, row tile) before the group
   long long* unit;  // (groups+1) units (a segment's 128-key tiles) before the group
+  int2* parts;      // (segments) slot of the segment's first partial, partials
   int* row_vis;     // (rows) keys the row sees; -1: the row belongs to no sequence
   int* row_grp;     // (rows) the row's group, -1 if that shares nothing
   int* row_start;   // (rows) keys of the row's sequence that its group attends to
@@ -39,6 +40,12 @@ struct SharedArgs {
   float2* part_ml;  // (slots, rows of a segment): max, sum
   float* own_o;     // (rows, H, D) fp32, of each row's own keys
   float2* own_ml;   // (rows, H)
+  // decode: where a sequence and kv head's own result is: (-1, 1) in own_o, else
+  // (first warp, parts) in the decode kernel's partial slots
+  int2* own_parts;         // (rows, Hkv), NULL for prefill
+  const float* slot_o;     // (slots, slot_rows, D)
+  const float2* slot_ml;   // (slots, slot_rows)
+  int slot_rows;
   int batch, num_groups, rows;
   int num_heads, num_kv_heads, group, head_dim, block_size, max_blocks, num_blocks;
   int len_cap;          // keys a sequence may have
@@ -53,7 +60,7 @@ struct SharedArgs {
 // Sizes of a call: grid, segment form and the workspace's parts (byte offsets).
 struct SharedLayout {
   int tokens_per_tile, row_tiles, max_segments, ctas;
-  size_t plan, part_ml, part_o, own_ml, own_o, bytes;
+  size_t plan, part_ml, part_o, own_parts, own_ml, own_o, bytes;
 };
 SharedLayout shared_layout(size_t base, int rows, int num_heads, int num_kv_heads, int head_dim,
                            int num_groups, int num_sms);

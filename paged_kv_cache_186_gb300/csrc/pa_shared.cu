@@ -290,9 +290,9 @@ struct Ring {
   static constexpr int kTile = (D / 64) * kSub;
   static constexpr int kRawTile = kBN * 128;
   static constexpr int kQTiles = PAIR ? 2 : 1;
-  static constexpr int kK = Q8 ? (PAIR ? 2 : 1) : D == 64 ? (PAIR ? 4 : 6) : PAIR ? 2 : 3;
+  static constexpr int kK = Q8 ? 1 : D == 64 ? (PAIR ? 4 : 6) : PAIR ? 2 : 3;
   static constexpr int kV = Q8 ? 2 : D == 64 ? (PAIR ? 4 : 6) : 3;
-  static constexpr int kRaw = Q8 ? (PAIR ? 1 : 2) : 0;  // of K and of V each
+  static constexpr int kRaw = Q8 ? 2 : 0;  // of K and of V each
   static constexpr int kQ0 = 0;
   static constexpr int kK0 = kQ0 + kQTiles * kTile;
   static constexpr int kV0 = kK0 + kK * kTile;

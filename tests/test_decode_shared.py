@@ -6,7 +6,7 @@ import torch
 
 import paged_kv_cache_186_gb300 as pa
 from gpu_util import assert_attention_close
-from shared_util import decode64, make
+from shared_util import decode64, make, n64
 
 pytestmark = pytest.mark.gpu
 
@@ -277,3 +277,74 @@ def test_seeded_random_batches():
         s = make(groups, G * Hkv, Hkv, D, bs, kv, seed=600 + i, outside=((5,), ()) if i % 3 else ((), ()))
         bound = max(s.lens) if i % 2 else 0
         assert_attention_close(run(s, max_context_len=bound), decode64(s), f"case {i}: {groups}")
+
+
+@pytest.mark.parametrize("kv, D, bs", [("bf16", 64, 16), ("bf16", 64, 32), ("bf16", 128, 16),
+                                       ("fp8", 128, 32), ("int8", 128, 16)])
+@pytest.mark.parametrize("seqs", [1, 3, 40])
+def test_many_groups_of_a_few_key_tiles_over_and_over(kv, D, bs, seqs):
+    # segments of one to twenty key tiles: every CTA walks many pieces, and the stages of its rings
+    # are handed from one half to the other in every order; repeated, since a wait that could
+    # be passed early or never would depend on timing
+    r = np.random.default_rng(D + bs + seqs)
+    groups = []
+    for _ in range(24):
+        p = int(r.integers(1, 2600))
+        groups.append((p, [p + int(r.integers(1, 60)) for _ in range(seqs)]))
+    s = make(groups, 8, 4, D, bs, kv, seed=560 + seqs)
+    first = run(s)
+    assert_attention_close(first, plain(s).double().cpu().numpy(), "against decode")
+    for _ in range(60):
+        out = pa.decode_shared(s.q, s.k_cache, s.v_cache, s.bt, s.context_lens, s.cu_groups,
+                               s.prefix_lens, s.scale, k_scale=s.k_scale, v_scale=s.v_scale)
+    torch.cuda.synchronize()
+    assert pa.get_device_error() == 0
+    assert torch.equal(out, first)
+
+
+@pytest.mark.parametrize("kv", ["bf16", "fp8"])
+def test_values_of_any_magnitude(kv):
+    # V (or its scales) from 2^-30 to 2^40 between tiles and heads: the factor that brings V into
+    # f16 moves with them; zeros leave it where it is
+    s = make([(1200, [1201, 1300, 1250])], 8, 2, 128, 16, kv, seed=570)
+    blocks = s.bt[0, :75].long()
+    t = s.v_cache if kv == "bf16" else s.v_scale
+    ref = t.clone()
+    for shifts in ([0, -30, 40, 5], [40, 0, -30, 12], [-30, -30, -30, -30]):
+        t.copy_(ref)
+        for i, e in enumerate(shifts):
+            part = blocks[i * 19:(i + 1) * 19]
+            t[part] = t[part] * 2.0 ** e
+        t[blocks[20:30]] = 0
+        want = decode64(s)
+        got = n64(run(s))
+        # relative to the largest value a row could have from the keys it weighs
+        top = np.abs(want).max(axis=-1, keepdims=True)
+        assert (np.abs(got - want) <= top * 2.0 ** -6).all()
+        assert np.linalg.norm(got - want) <= 5e-3 * np.linalg.norm(want)
+
+
+def test_an_infinite_value_spoils_its_heads_only():
+    s = make([(300, [310, 305])], 8, 2, 128, 16, seed=571)
+    ref = run(s)
+    s.v_cache[s.bt[0, 5].item(), 3, 1, 7] = float("inf")
+    out = run(s)
+    assert torch.equal(out[:, :4], ref[:, :4])
+    assert torch.isinf(out[:, 4:, 7].float()).all()
+    assert torch.isfinite(out[:, 4:, 8:].float()).all()
+
+
+def test_blocks_beyond_2_to_the_32_elements():
+    # the same shared and own blocks at the front of a small pool and at the end of a large one
+    s = make([(200, [210, 230, 201]), (64, [70])], 8, 8, 128, 32, seed=572)
+    small = run(s)
+    per = 32 * 8 * 128
+    nb = (1 << 32) // per + 64
+    need = s.k_cache.shape[0]
+    big_k, big_v = (torch.empty((nb, 32, 8, 128), dtype=torch.bfloat16, device="cuda")
+                    for _ in range(2))
+    big_k[nb - need:], big_v[nb - need:] = s.k_cache, s.v_cache
+    bt = torch.where(s.bt >= 0, s.bt + (nb - need), s.bt)
+    out = pa.decode_shared(s.q, big_k, big_v, bt, s.context_lens, s.cu_groups, s.prefix_lens, s.scale)
+    torch.cuda.synchronize()
+    assert torch.equal(out, small)

@@ -326,6 +326,9 @@ pa_status pa_decode_scored(const void* q, const pa_kv_cache* cache, const int32_
  *                (context_len 0) may stand in any group, its row of the table may
  *                hold anything.
  *   num_groups   >= 0; 0: nothing is shared, cu_groups and prefix_lens may be NULL.
+ *   always       0: shared keys are attended to once where that is expected to pay
+ *                (by the batch, the groups and the length bound), else the call is
+ *                pa_decode; other values: whether or not it pays.
  *   workspace    at least pa_decode_shared_workspace_size() bytes (0: the shape is
  *                not supported), contract as for pa_decode.
  *   scale        > 0 (PA_ERR_SHAPE).
@@ -339,8 +342,8 @@ size_t pa_decode_shared_workspace_size(const pa_kv_cache* cache, int32_t batch, 
 pa_status pa_decode_shared(const void* q, const pa_kv_cache* cache, const int32_t* block_tables,
                            int32_t max_blocks_per_seq, const int32_t* context_lens,
                            int32_t max_context_len, const int32_t* cu_groups,
-                           const int32_t* prefix_lens, int32_t num_groups, int32_t batch,
-                           int32_t num_heads, float scale, void* out, void* workspace,
+                           const int32_t* prefix_lens, int32_t num_groups, int32_t always,
+                           int32_t batch, int32_t num_heads, float scale, void* out, void* workspace,
                            size_t workspace_bytes, void* stream);
 
 /*
@@ -490,6 +493,8 @@ pa_status pa_prefill_window(const void* q, const pa_kv_cache* cache, const int32
  *                being its kv_len): the block tables of a group begin with the same
  *                blocks. New tokens may lie within the prefix; they see the keys up
  *                to their own.
+ *   always       as pa_decode_shared; whether sharing pays is seen on the device,
+ *                from the lengths.
  *   workspace    at least pa_prefill_shared_workspace_size() bytes (0: the shape is
  *                not supported): about 8 * head_dim bytes per query row. Contents on
  *                entry are ignored; calls sharing one workspace must not overlap.
@@ -503,9 +508,10 @@ size_t pa_prefill_shared_workspace_size(const pa_kv_cache* cache, int32_t num_he
 pa_status pa_prefill_shared(const void* q, const pa_kv_cache* cache, const int32_t* block_tables,
                             int32_t max_blocks_per_seq, const int32_t* cu_seqlens_q,
                             const int32_t* cu_seqlens_k, const int32_t* cu_groups,
-                            const int32_t* prefix_lens, int32_t num_groups, int32_t batch,
-                            int32_t num_heads, int32_t total_q, int32_t max_q_len, float scale,
-                            void* out, void* workspace, size_t workspace_bytes, void* stream);
+                            const int32_t* prefix_lens, int32_t num_groups, int32_t always,
+                            int32_t batch, int32_t num_heads, int32_t total_q, int32_t max_q_len,
+                            float scale, void* out, void* workspace, size_t workspace_bytes,
+                            void* stream);
 
 /*
  * pa_decode_noalloc - pa_decode for callers that cannot allocate device memory.

@@ -137,12 +137,12 @@ def lib() -> ctypes.CDLL:
     L.pa_decode_shared_workspace_size.restype = ctypes.c_size_t
     L.pa_decode_shared_workspace_size.argtypes = [cache, i32, i32, i32, i32, i32]
     L.pa_decode_shared.restype = ctypes.c_int
-    L.pa_decode_shared.argtypes = [P, cache, P, i32, P, i32, P, P, i32, i32, i32, ctypes.c_float,
-                                   P, P, ctypes.c_size_t, P]
+    L.pa_decode_shared.argtypes = [P, cache, P, i32, P, i32, P, P, i32, i32, i32, i32,
+                                   ctypes.c_float, P, P, ctypes.c_size_t, P]
     L.pa_prefill_shared_workspace_size.restype = ctypes.c_size_t
     L.pa_prefill_shared_workspace_size.argtypes = [cache, i32, i32, i32]
     L.pa_prefill_shared.restype = ctypes.c_int
-    L.pa_prefill_shared.argtypes = [P, cache, P, i32, P, P, P, P, i32, i32, i32, i32, i32,
+    L.pa_prefill_shared.argtypes = [P, cache, P, i32, P, P, P, P, i32, i32, i32, i32, i32, i32,
                                     ctypes.c_float, P, P, ctypes.c_size_t, P]
     _lib = L
     return L
@@ -608,13 +608,14 @@ def decode_shared_workspace_size(k_cache, batch: int, num_heads: int, max_blocks
 
 
 def decode_shared(q, k_cache, v_cache, block_tables, context_lens, cu_groups, prefix_lens,
-                  scale: float, *, max_context_len: int = 0, out=None, workspace=None,
-                  k_scale=None, v_scale=None) -> torch.Tensor:
+                  scale: float, *, max_context_len: int = 0, always: bool = False, out=None,
+                  workspace=None, k_scale=None, v_scale=None) -> torch.Tensor:
     """pa_decode_shared: decode where the sequences cu_groups[g] .. cu_groups[g+1]-1 (int32
     (groups + 1,)) share their first prefix_lens[g] keys (int32 (groups,)): their block table rows
     begin with the same prefix_lens[g] // block_size blocks, which are read and attended to once
-    for the whole group. A workspace (uint8 tensor of decode_shared_workspace_size bytes) is
-    allocated in every call that gives none."""
+    for the whole group (where that is expected to pay, by the batch, the groups and
+    max_context_len; always: in any case). A workspace (uint8 tensor of
+    decode_shared_workspace_size bytes) is allocated in every call that gives none."""
     if q.dim() != 3:
         raise ValueError("q must be (batch, num_heads, head_dim)")
     max_context_len = int(max_context_len)
@@ -646,7 +647,7 @@ def decode_shared(q, k_cache, v_cache, block_tables, context_lens, cu_groups, pr
         ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     _run(dev, "pa_decode_shared", (_lib or lib()).pa_decode_shared, q.data_ptr(),
          ctypes.byref(cache), bt.data_ptr(), width, cl.data_ptr(), max_context_len, cg.data_ptr(),
-         pl.data_ptr(), n, B, H, scale, out.data_ptr(), ws or None, ws_bytes)
+         pl.data_ptr(), n, 1 if always else 0, B, H, scale, out.data_ptr(), ws or None, ws_bytes)
     return out
 
 
@@ -659,10 +660,10 @@ def prefill_shared_workspace_size(k_cache, total_q: int, num_heads: int, num_gro
 
 
 def prefill_shared(q, k_cache, v_cache, block_tables, cu_seqlens_q, cu_seqlens_k, cu_groups,
-                   prefix_lens, scale: float, *, max_q_len: int = 0, out=None,
-                   workspace=None) -> torch.Tensor:
+                   prefix_lens, scale: float, *, max_q_len: int = 0, always: bool = False,
+                   out=None, workspace=None) -> torch.Tensor:
     """pa_prefill_shared: prefill_varlen of sequences that share their first keys in groups
-    (cu_groups, prefix_lens: as decode_shared). bf16 caches of head_dim 128. max_q_len (a bound of
+    (cu_groups, prefix_lens, always: as decode_shared). bf16 caches of head_dim 128. max_q_len (a bound of
     every sequence's new tokens) sizes the grid and lets short questions take their own variant. A
     workspace (uint8 tensor of prefill_shared_workspace_size bytes, about 8 * head_dim per query
     row) is allocated in every call that gives none."""
@@ -698,8 +699,8 @@ def prefill_shared(q, k_cache, v_cache, block_tables, cu_seqlens_q, cu_seqlens_k
         ws, ws_bytes = workspace.data_ptr(), workspace.numel() * workspace.element_size()
     _run(dev, "pa_prefill_shared", (_lib or lib()).pa_prefill_shared, q.data_ptr(),
          ctypes.byref(cache), bt.data_ptr(), width, cu_q.data_ptr(), cu_k.data_ptr(),
-         cg.data_ptr(), pl.data_ptr(), groups, n - 1, H, T, max_q_len, scale, out.data_ptr(),
-         ws or None, ws_bytes)
+         cg.data_ptr(), pl.data_ptr(), groups, 1 if always else 0, n - 1, H, T, max_q_len, scale,
+         out.data_ptr(), ws or None, ws_bytes)
     return out
 
 

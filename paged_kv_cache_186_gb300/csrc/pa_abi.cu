@@ -387,6 +387,8 @@ struct SharedCall {
   const int32_t* cu_groups;
   const int32_t* prefix_lens;
   int32_t num_groups;
+  bool share;   // decode: attend to the shared keys once
+  bool always;  // prefill: likewise, whether or not it pays
   void* workspace;
   size_t workspace_bytes;
 };
@@ -578,7 +580,7 @@ pa_status decode_common(const void* q, const pa_kv_cache* cache, const int32_t* 
     a.head_ml = reinterpret_cast<float2*>(ws + sw.ml);
     a.raw_scores = reinterpret_cast<float*>(ws + sw.raw);
   }
-  if (shared != nullptr) {
+  if (shared != nullptr && shared->share) {
     pa::SharedArgs h = shared_args(*shared, layout, cache, block_tables, max_blocks_per_seq, batch,
                                    batch, num_heads, cap, scale, out, dev->err, context_lens);
     h.slot_o = a.part_o;
@@ -804,7 +806,10 @@ pa_status prefill_common(const void* q, const pa_kv_cache* cache, const int32_t*
                                    scale, out, dev->err, nullptr);
     h.cu_q = cu_seqlens_q;
     h.cu_k = cu_seqlens_k;
+    h.always = shared->always;
+    h.own_tokens = pa::prefill_shared_tokens(tpt, a.num_qtiles);
     a.own_start = h.plan.row_start;
+    a.own_group = h.plan.row_grp;
     a.own_o = h.own_o;
     a.own_ml = h.own_ml;
     return pa::launch_shared_plan(h, strm) == cudaSuccess &&
@@ -863,8 +868,8 @@ size_t pa_decode_shared_workspace_size(const pa_kv_cache* cache, int32_t batch, 
 pa_status pa_decode_shared(const void* q, const pa_kv_cache* cache, const int32_t* block_tables,
                            int32_t max_blocks_per_seq, const int32_t* context_lens,
                            int32_t max_context_len, const int32_t* cu_groups,
-                           const int32_t* prefix_lens, int32_t num_groups, int32_t batch,
-                           int32_t num_heads, float scale, void* out, void* workspace,
+                           const int32_t* prefix_lens, int32_t num_groups, int32_t always,
+                           int32_t batch, int32_t num_heads, float scale, void* out, void* workspace,
                            size_t workspace_bytes, void* stream) {
   const pa_status st = check_cache(cache);
   if (st != PA_OK) return st;
@@ -873,7 +878,19 @@ pa_status pa_decode_shared(const void* q, const pa_kv_cache* cache, const int32_
     return PA_ERR_NULL;
   if (batch > pa::kMaxPersistentBatch || num_groups > pa::kMaxPersistentBatch)
     return PA_ERR_UNSUPPORTED;
-  const SharedCall shared{cu_groups, prefix_lens, num_groups, workspace, workspace_bytes};
+  // Sharing costs two more launches and a merge (about 6 us) and spares at most
+  // this many bytes of K and V (by the host's bound of the lengths). Measured on
+  // one GB300, shared / unshared us: bf16, 8 kv heads of 128, 4 sequences behind
+  // 16384 keys (201 MB) 36 / 35, 8 behind 8192 (235 MB) 30 / 34, 16 behind 2048 (126
+  // MB) 27 / 23 and 4096 (252 MB) 29 / 31, 64 behind 1024 (264 MB) 32 / 30 and 2048
+  // (529 MB) 35 / 46. The decode of 8-bit codes is slower a byte: 8 sequences
+  // behind 2048 keys (29 MB) 31 / 33, 64 behind 2048 (264 MB) 42 / 59.
+  const double saved = static_cast<double>(std::max(0, batch - num_groups)) * 2.0 *
+                       decode_len_cap(cache, std::max(max_blocks_per_seq, 0), max_context_len) *
+                       cache->num_kv_heads * cache->head_dim * elem_bytes(cache);
+  const bool pays = saved >= (cache->dtype == PA_KV_BF16 ? 240e6 : 28e6);
+  const SharedCall shared{cu_groups, prefix_lens, num_groups, always != 0 || pays, false,
+                          workspace, workspace_bytes};
   return decode_common(q, cache, block_tables, max_blocks_per_seq, context_lens, max_context_len,
                        batch, num_heads, scale, out, workspace, workspace_bytes, stream, nullptr,
                        nullptr, nullptr, nullptr, 0, 0, nullptr,
@@ -896,9 +913,10 @@ size_t pa_prefill_shared_workspace_size(const pa_kv_cache* cache, int32_t num_he
 pa_status pa_prefill_shared(const void* q, const pa_kv_cache* cache, const int32_t* block_tables,
                             int32_t max_blocks_per_seq, const int32_t* cu_seqlens_q,
                             const int32_t* cu_seqlens_k, const int32_t* cu_groups,
-                            const int32_t* prefix_lens, int32_t num_groups, int32_t batch,
-                            int32_t num_heads, int32_t total_q, int32_t max_q_len, float scale,
-                            void* out, void* workspace, size_t workspace_bytes, void* stream) {
+                            const int32_t* prefix_lens, int32_t num_groups, int32_t always,
+                            int32_t batch, int32_t num_heads, int32_t total_q, int32_t max_q_len,
+                            float scale, void* out, void* workspace, size_t workspace_bytes,
+                            void* stream) {
   const pa_status st = check_cache(cache);
   if (st != PA_OK) return st;
   if (num_groups < 0) return PA_ERR_SHAPE;
@@ -906,7 +924,8 @@ pa_status pa_prefill_shared(const void* q, const pa_kv_cache* cache, const int32
     return PA_ERR_NULL;
   if (batch > pa::kMaxPersistentBatch || num_groups > pa::kMaxPersistentBatch)
     return PA_ERR_UNSUPPORTED;
-  const SharedCall shared{cu_groups, prefix_lens, num_groups, workspace, workspace_bytes};
+  const SharedCall shared{cu_groups, prefix_lens, num_groups, true, always != 0, workspace,
+                          workspace_bytes};
   const bool share = num_groups > 0;
   return prefill_common(q, cache, block_tables, max_blocks_per_seq, cu_seqlens_q, cu_seqlens_k,
                         batch, num_heads, total_q, max_q_len, scale, share ? kNoWindow : 0, 0, out,

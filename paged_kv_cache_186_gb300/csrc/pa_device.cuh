@@ -104,6 +104,13 @@ __device__ __forceinline__ void st_keep(float* p, float x, float y, float z, flo
                : "memory");
 }
 
+// 32-byte store (a whole L2 sector; the address must be aligned to it).
+__device__ __forceinline__ void st_global_32(float* p, const uint32_t* w) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
+               "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
 // 4-D tiled tensor load with an L2 cache policy, completing on `bar`.
 __device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, uint32_t bar,
                                             int c0, int c1, int c2, int c3, uint64_t policy) {

@@ -209,8 +209,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   int Tq[2];
   PairKeys pk{};
   int own = 0;  // SH: first key (a block's)
+  bool part = false;  // SH: the rows' result is merged with the shared keys'
   if constexpr (SH) {
     own = a.own_start[q0];
+    part = a.own_group[q0] >= 0;
     pk.lo = pk.wb = pk.shift = own;
   } else if constexpr (WIN) {
     pk = pair_keys<BS>(cached + t00, kv_len, a.window, a.sinks);
@@ -244,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __nv_bfloat16* const out = static_cast<__nv_bfloat16*>(a.out);
   const int H = a.num_heads;
 
-  if (SH && T == 0) return;  // the rows see no own key: the merge knows
+  if (SH && part && T == 0) return;  // the rows see no own key: the merge knows
   if (T == 0) {  // no keys at all (invalid q_len > kv_len = 0): zero rows
     const int rows = (min(t00 + 2 * TPT, q_len) - t00) * G;
     for (int e = threadIdx.x; e < rows * (kD / 8); e += kThreads) {
@@ -622,9 +624,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (ok && !(SPLIT && ti == 1) && Tn > 0 &&
         warp_wait(bar(BAR_O + ti), ((Tn - 1) / nstep) & 1, &abort_flag, a.err)) {
       tc::fence_after_sync();
-      const float inv = SH ? 1.f : l > 0.f ? 1.f / l : 0.f;
+      const float inv = SH && part ? 1.f : l > 0.f ? 1.f / l : 0.f;
       const long long row = static_cast<long long>(q0 + tok) * H + kvh * G + g;
-      if (SH && row_valid) a.own_ml[row] = make_float2(m_used, l);
+      if (SH && part && row_valid) a.own_ml[row] = make_float2(m_used, l);
       __nv_bfloat16* orow = out + (static_cast<long long>(q0 + tok) * H + kvh * G + g) * kD;
 #pragma unroll
       for (int c = 0; c < 4; ++c) {
@@ -639,12 +641,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int j = 0; j < 32; ++j)
             w[j] = __float_as_uint(__uint_as_float(w[j]) * f0 + __uint_as_float(v[j]) * f1);
         }
-        if (SH && row_valid) {
-          float4* dst = reinterpret_cast<float4*>(a.own_o + row * kD + 32 * c);
+        if (SH && part) {
+          if (row_valid) {
+            float* dst = a.own_o + row * kD + 32 * c;
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            dst[j] = make_float4(__uint_as_float(w[4 * j]), __uint_as_float(w[4 * j + 1]),
-                                 __uint_as_float(w[4 * j + 2]), __uint_as_float(w[4 * j + 3]));
+            for (int j = 0; j < 4; ++j) st_global_32(dst + 8 * j, w + 8 * j);
+          }
         } else if (row_valid) {
           uint32_t pk[16];
 #pragma unroll
@@ -724,5 +726,9 @@ cudaError_t launch_prefill(const PrefillArgs& a, const CUtensorMap& qmap, const 
 }
 
 int prefill_tokens_per_tile(int group) { return kBM / group; }
+
+int prefill_shared_tokens(int tokens_per_tile, int num_qtiles) {
+  return num_qtiles <= 1 ? tokens_per_tile : 2 * tokens_per_tile;
+}
 
 }  // namespace pa

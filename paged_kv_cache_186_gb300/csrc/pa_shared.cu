@@ -145,6 +145,53 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedA
   }
   __syncthreads();
 
+  // ---- prefill: does sharing pay? Unshared, CTA after CTA of the prefill kernel
+  // walks the prefix: waves of them, each as long as its key tiles; shared, the
+  // same products are spread evenly and full, but the call has a fixed cost, one
+  // for each wave of the CTAs over the sequences' own keys, and one for each row
+  // merged. In us, fitted on one GB300 over 2-64 sequences of 4-256 new tokens
+  // behind 512-16384 keys (shared / unshared measured): 64 drafts of 4-8 tokens
+  // behind 4096 98 / 219, 32 questions of 1-64 behind 8000 164 / 222, 32 of 128
+  // behind 8192 567 / 505, 8 of 32 behind 2048 53 / 31, 2 of 128 behind 8192 80 /
+  // 129. (A decode step is chosen for on the host: its kernel's own cost is small.)
+  if (!decode && !a.always) {
+    auto add = [](long long x, long long y) { return x + y; };
+    auto total = [&](long long v) {
+      block_scan<long long>(v, part, add);
+      const long long t = part[31];
+      __syncthreads();
+      return t;
+    };
+    const int span = a.own_tokens;  // new tokens of a sequence that one CTA takes
+    long long ctas = 0, walked = 0, units = 0, rows = 0;
+    for (int g = warp; g < G; g += kPlanThreads / 32) {
+      const int KT = (keys[g] + kBN - 1) / kBN, b0 = cu[g], b1 = cu[g + 1];
+      if (KT == 0) continue;
+      for (int b = b0 + lane; b < b1; b += 32) {
+        const int n = (max(a.cu_q[b + 1] - a.cu_q[b], 0) + span - 1) / span;
+        ctas += n;
+        walked += static_cast<long long>(n) * KT;
+      }
+      if (lane == 0) {
+        const int t = p.tok[2 * g + 1] - p.tok[2 * g], per = a.tokens_per_tile * a.row_tiles;
+        units += static_cast<long long>((t + per - 1) / per) * KT;
+        rows += t;
+      }
+    }
+    const float n = static_cast<float>(total(ctas)) * a.num_kv_heads;
+    const float tiles = static_cast<float>(total(walked)) * a.num_kv_heads / fmaxf(n, 1.f);
+    const float u = static_cast<float>(total(units)) * a.num_kv_heads;
+    const float r = static_cast<float>(total(rows)) * a.num_heads;
+    const float waves = ceilf(n / a.ctas);
+    const float unshared = waves * tiles * 1.8f;
+    const float shared = ceilf(u / a.ctas) * (a.row_tiles == 2 ? 2.f : 1.6f) + 14.f + 6.f * waves +
+                         r * 4e-4f;
+    if (shared >= unshared) {  // (the same in every thread)
+      for (int g = tid; g < G; g += kPlanThreads) keys[g] = p.keys[g] = 0;
+      __syncthreads();
+    }
+  }
+
   // ---- segments and units before each group
   const int per_seg = a.tokens_per_tile * a.row_tiles;
   long long segs = 0, units = 0;
@@ -952,7 +999,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       tc::fence_after_sync();
       const long long row = p.slot * (kBM * a.row_tiles) + (PAIR ? hf * kBM : 0) + r;
-      float4* const dst = reinterpret_cast<float4*>(a.part_o + row * D);
+      float* const dst = a.part_o + row * D;
 #pragma unroll
       for (int c = 0; c < kCols; ++c) {
         uint32_t w[32];
@@ -968,9 +1015,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (valid) {
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            dst[8 * c + j] = make_float4(__uint_as_float(w[4 * j]), __uint_as_float(w[4 * j + 1]),
-                                         __uint_as_float(w[4 * j + 2]), __uint_as_float(w[4 * j + 3]));
+          for (int j = 0; j < 4; ++j) st_global_32(dst + 32 * c + 8 * j, w + 8 * j);
         }
       }
       if (valid) a.part_ml[row] = make_float2(m_used, l);
@@ -1019,7 +1064,8 @@ __global__ void __launch_bounds__(kMergeWarps * 32, WIDE ? 4 : 8)
   // (no own keys: what is left here from another call is not used)
   int2 mine = make_int2(-1, 1);
   if (a.own_parts != nullptr) mine = a.own_parts[w];
-  if (vis < 0) return;
+  // (a row that shares nothing is written by the prefill kernel)
+  if (vis < 0 || (a.own_parts == nullptr && g < 0)) return;
   const bool own = vis > start;
 
   // ---- the row's parts of the shared keys, then those of its own
@@ -1205,12 +1251,14 @@ SharedLayout shared_layout(size_t base, int rows, int num_heads, int num_kv_head
   l.own_parts = up(l.part_o + part_rows * head_dim * sizeof(float));
   l.own_ml = up(l.own_parts + static_cast<size_t>(rows) * num_kv_heads * sizeof(int2));
   l.own_o = up(l.own_ml + rh * sizeof(float2));
-  l.bytes = l.own_o + rh * head_dim * sizeof(float);
+  l.bytes = l.own_o + rh * head_dim * sizeof(float) + 256;  // (to align the address)
   return l;
 }
 
 void shared_pointers(SharedArgs& a, const SharedLayout& l, void* workspace) {
-  char* const ws = static_cast<char*>(workspace);
+  // the parts are at multiples of 256 bytes of the address (stores of 32)
+  char* const ws = reinterpret_cast<char*>(
+      (reinterpret_cast<uintptr_t>(workspace) + 255) & ~static_cast<uintptr_t>(255));
   const int g1 = a.num_groups + 1;
   a.plan.unit = reinterpret_cast<long long*>(ws + l.plan);
   a.plan.parts = reinterpret_cast<int2*>(a.plan.unit + g1);

@@ -54,6 +54,8 @@ struct SharedArgs {
   int max_segments;     // segments the workspace has room for
   int ctas;             // grid of the launch over the shared keys
   int kv;               // kKvBf16, kKvE4m3 or kKvInt8
+  int always;           // prefill: share whether or not it pays
+  int own_tokens;       // prefill: new tokens a CTA of the launch over own keys takes
   float scale_log2;
 };
 

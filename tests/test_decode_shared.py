@@ -13,7 +13,7 @@ pytestmark = pytest.mark.gpu
 
 def run(s, **kw):
     out = pa.decode_shared(s.q, s.k_cache, s.v_cache, s.bt, s.context_lens, s.cu_groups,
-                           s.prefix_lens, s.scale, k_scale=s.k_scale, v_scale=s.v_scale, **kw)
+                           s.prefix_lens, s.scale, always=True, k_scale=s.k_scale, v_scale=s.v_scale, **kw)
     torch.cuda.synchronize()
     assert pa.get_device_error() == 0
     return out
@@ -162,13 +162,13 @@ def test_repeats_other_streams_outputs_and_strided_inputs():
     side.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(side):
         c = pa.decode_shared(s.q, s.k_cache, s.v_cache, s.bt, s.context_lens, s.cu_groups,
-                             s.prefix_lens, s.scale)
+                             s.prefix_lens, s.scale, always=True)
     side.synchronize()
     assert torch.equal(a, c)
     wide = torch.cat([s.bt, s.bt], dim=1)[:, :s.bt.shape[1]]
     q = s.q.transpose(0, 1).contiguous().transpose(0, 1)
     lens = torch.stack([s.context_lens] * 2, dim=1)[:, 0]
-    d = pa.decode_shared(q, s.k_cache, s.v_cache, wide, lens, s.cu_groups, s.prefix_lens, s.scale)
+    d = pa.decode_shared(q, s.k_cache, s.v_cache, wide, lens, s.cu_groups, s.prefix_lens, s.scale, always=True)
     assert torch.equal(a, d)
 
 
@@ -199,7 +199,7 @@ def test_graph_replays_with_lengths_and_groups_rewritten(kv):
     for k in range(2):  # two graphs that share the workspace
         with torch.cuda.graph(graphs[k]):
             pa.decode_shared(s.q, s.k_cache, s.v_cache, s.bt, s.context_lens, s.cu_groups,
-                             s.prefix_lens, s.scale, out=outs[k], workspace=ws, k_scale=s.k_scale,
+                             s.prefix_lens, s.scale, always=True, out=outs[k], workspace=ws, k_scale=s.k_scale,
                              v_scale=s.v_scale)
     gen = torch.Generator().manual_seed(1)
     for step in range(4):
@@ -228,7 +228,7 @@ def test_bad_block_ids_are_flagged_and_spoil_their_group_only():
     for bad in (-1, 1 << 30):
         s.bt[0, 3] = bad
         out = pa.decode_shared(s.q, s.k_cache, s.v_cache, s.bt, s.context_lens, s.cu_groups,
-                               s.prefix_lens, s.scale)
+                               s.prefix_lens, s.scale, always=True)
         assert pa.get_device_error() == pa.PA_DEVERR_BLOCK_RANGE
         assert_attention_close(out[2:], want[2:], "other group")
 
@@ -296,7 +296,7 @@ def test_many_groups_of_a_few_key_tiles_over_and_over(kv, D, bs, seqs):
     assert_attention_close(first, plain(s).double().cpu().numpy(), "against decode")
     for _ in range(60):
         out = pa.decode_shared(s.q, s.k_cache, s.v_cache, s.bt, s.context_lens, s.cu_groups,
-                               s.prefix_lens, s.scale, k_scale=s.k_scale, v_scale=s.v_scale)
+                               s.prefix_lens, s.scale, always=True, k_scale=s.k_scale, v_scale=s.v_scale)
     torch.cuda.synchronize()
     assert pa.get_device_error() == 0
     assert torch.equal(out, first)
@@ -345,6 +345,19 @@ def test_blocks_beyond_2_to_the_32_elements():
                     for _ in range(2))
     big_k[nb - need:], big_v[nb - need:] = s.k_cache, s.v_cache
     bt = torch.where(s.bt >= 0, s.bt + (nb - need), s.bt)
-    out = pa.decode_shared(s.q, big_k, big_v, bt, s.context_lens, s.cu_groups, s.prefix_lens, s.scale)
+    out = pa.decode_shared(s.q, big_k, big_v, bt, s.context_lens, s.cu_groups, s.prefix_lens, s.scale, always=True)
     torch.cuda.synchronize()
     assert torch.equal(out, small)
+
+
+@pytest.mark.parametrize("kv, batch, prefix, shares", [("bf16", 4, 1000, False), ("bf16", 40, 8000, True),
+                                                       ("int8", 2, 400, False), ("int8", 20, 2000, True)])
+def test_without_always_small_calls_are_decode(kv, batch, prefix, shares):
+    s = make([(prefix, [prefix + 5 + i for i in range(batch)])], 32, 8, 128, 16, kv, seed=580)
+    out = pa.decode_shared(s.q, s.k_cache, s.v_cache, s.bt, s.context_lens, s.cu_groups,
+                           s.prefix_lens, s.scale, k_scale=s.k_scale, v_scale=s.v_scale)
+    always, ref = run(s), plain(s)
+    torch.cuda.synchronize()
+    assert torch.equal(out, always if shares else ref)
+    assert not torch.equal(always, ref)
+    assert_attention_close(out, ref.double().cpu().numpy(), "decode")

@@ -14,7 +14,7 @@ pytestmark = pytest.mark.gpu
 def run(s, **kw):
     kw.setdefault("max_q_len", max(s.new, default=0))
     out = pa.prefill_shared(s.q, s.k_cache, s.v_cache, s.bt, s.cu_q, s.cu_k, s.cu_groups,
-                            s.prefix_lens, s.scale, **kw)
+                            s.prefix_lens, s.scale, **{"always": True, **kw})
     torch.cuda.synchronize()
     assert pa.get_device_error() == 0
     return out
@@ -60,7 +60,7 @@ def test_sequences_without_new_tokens_short_ones_and_rows_behind_the_last():
     q = torch.cat([s.q, s.q[:7]])  # rows behind the last sequence
     out = torch.full_like(q, 3.0)
     pa.prefill_shared(q, s.k_cache, s.v_cache, s.bt, s.cu_q, s.cu_k, s.cu_groups, s.prefix_lens,
-                      s.scale, max_q_len=40, out=out)
+                      s.scale, max_q_len=40, out=out, always=True)
     torch.cuda.synchronize()
     assert_attention_close(out[:T], want, "short")
     assert (out[T:] == 3.0).all()
@@ -117,7 +117,7 @@ def test_repeats_streams_workspaces_and_graphs():
     side.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(side):
         c = pa.prefill_shared(s.q, s.k_cache, s.v_cache, s.bt, s.cu_q, s.cu_k, s.cu_groups,
-                              s.prefix_lens, s.scale, max_q_len=150)
+                              s.prefix_lens, s.scale, max_q_len=150, always=True)
     side.synchronize()
     assert torch.equal(a, c)
     ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
@@ -126,7 +126,8 @@ def test_repeats_streams_workspaces_and_graphs():
     for k in range(2):
         with torch.cuda.graph(graphs[k]):
             pa.prefill_shared(s.q, s.k_cache, s.v_cache, s.bt, s.cu_q, s.cu_k, s.cu_groups,
-                              s.prefix_lens, s.scale, max_q_len=150, out=outs[k], workspace=ws)
+                              s.prefix_lens, s.scale, max_q_len=150, out=outs[k], workspace=ws,
+                              always=True)
     for _ in range(3):
         graphs[0].replay()
         graphs[1].replay()
@@ -140,7 +141,7 @@ def test_bad_block_ids_are_flagged_and_spoil_their_group_only():
     for bad in (-1, 1 << 30):
         s.bt[0, 3] = bad
         out = pa.prefill_shared(s.q, s.k_cache, s.v_cache, s.bt, s.cu_q, s.cu_k, s.cu_groups,
-                                s.prefix_lens, s.scale, max_q_len=30)
+                                s.prefix_lens, s.scale, max_q_len=30, always=True)
         assert pa.get_device_error() == pa.PA_DEVERR_BLOCK_RANGE
         assert_attention_close(out[13:], want[13:], "other group")
 
@@ -148,7 +149,7 @@ def test_bad_block_ids_are_flagged_and_spoil_their_group_only():
 def test_a_decode_step_is_a_prefill_of_one_token_each():
     s = make([(500, [501 + 17 * i for i in range(20)])], 8, 2, 128, 16, seed=749, new=[1] * 20)
     dec = pa.decode_shared(s.q, s.k_cache, s.v_cache, s.bt, s.context_lens, s.cu_groups,
-                           s.prefix_lens, s.scale)
+                           s.prefix_lens, s.scale, always=True)
     want = prefill64(s)
     assert_attention_close(run(s), want, "prefill")
     assert_attention_close(dec, want, "decode")
@@ -171,3 +172,29 @@ def test_seeded_random_batches():
         s = make(groups, G * Hkv, Hkv, 128, bs, seed=800 + i, new=new)
         assert_attention_close(run(s, max_q_len=max(new) if i % 2 else 0), prefill64(s),
                                f"case {i}: {groups} {new}")
+
+
+@pytest.mark.parametrize("new, prefix, shares", [([200, 256, 130], 600, False), ([3] * 40, 6000, True)])
+def test_without_always_calls_that_would_not_gain_are_prefill(new, prefix, shares):
+    s = make([(prefix, [prefix + n + 9 for n in new])], 32, 8, 128, 16, seed=760, new=new)
+    ref = pa.prefill_varlen(s.q, s.k_cache, s.v_cache, s.bt, s.cu_q, s.cu_k, s.scale,
+                            max_q_len=max(new))
+    always, out = run(s), run(s, always=False)
+    assert torch.equal(out, always) == shares
+    assert_attention_close(out, ref.double().cpu().numpy(), "prefill_varlen")
+    if not shares:  # as the windowed prefill computes it, whose window keeps every key
+        win = pa.prefill_window(s.q, s.k_cache, s.v_cache, s.bt, s.cu_q, s.cu_k, s.scale, 1 << 30,
+                                max_q_len=max(new))
+        assert torch.equal(out, win)
+
+
+def test_the_choice_follows_the_lengths_and_mixes_with_sequences_outside():
+    # every small case of above again without `always`: the rows are written by one kernel or
+    # the other, those without any key by either
+    for case in CASES:
+        groups, new, H, Hkv, bs = case
+        s = make(groups, H, Hkv, 128, bs, seed=770 + H + bs, new=new)
+        assert_attention_close(run(s, always=False), prefill64(s), str(case))
+    s = make([(64, [80, 81, 0]), (100, [120])], 8, 2, 128, 16, seed=771,
+             new=[5, 7, 10, 2, 3, 20, 12], outside=((50, 7), (300,)))
+    assert_attention_close(run(s, always=False), prefill64(s), "outside")

@@ -82,7 +82,7 @@ def test_questions_about_one_video(kv):
     cu = lambda x: torch.tensor(np.concatenate([[0], np.cumsum(x)]), dtype=torch.int32).cuda()
     if kv == "bf16":
         out = pa.prefill_shared(q, kc, vc, bt, cu(questions), cu(lens), cu_groups, prefix, scale,
-                                max_q_len=max(questions))
+                                max_q_len=max(questions), always=True)
         want = ops64.prefill_window(n64(q), *values(), tables, cu(questions).cpu().numpy(),
                                     cu(lens).cpu().numpy(), scale, 1 << 30, 0)
         assert_attention_close(out, want, "questions")
@@ -90,7 +90,7 @@ def test_questions_about_one_video(kv):
         q = store([(b, lens[b]) for b in range(B)], [(9 + questions[b] + step,) * 3 for b in range(B)])
         lens = [n + 1 for n in lens]
         out = pa.decode_shared(q, kc, vc, bt, torch.tensor(lens, dtype=torch.int32).cuda(), cu_groups,
-                               prefix, scale, k_scale=ks, v_scale=vs)
+                               prefix, scale, always=True, k_scale=ks, v_scale=vs)
         k64, v64 = values()
         want = np.zeros(q.shape)
         for b, n in enumerate(lens):

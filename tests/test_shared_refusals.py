@@ -56,8 +56,8 @@ def test_norm_rope_axes_arguments(L, kw, want):
 def decode(L, cache=None, q=P(0x10), bt=P(0x20), mb=4, cl=P(0x30), cu=P(0x40), pl=P(0x50), G=1,
            B=2, H=4, scale=0.1, out=P(0x60)):
     c = cache or _cache()
-    return L.pa_decode_shared(q, ctypes.byref(c), bt, mb, cl, 0, cu, pl, G, B, H, scale, out, None,
-                              0, None)
+    return L.pa_decode_shared(q, ctypes.byref(c), bt, mb, cl, 0, cu, pl, G, 0, B, H, scale, out,
+                              None, 0, None)
 
 
 @pytest.mark.parametrize("kw, want", [
@@ -75,7 +75,7 @@ def test_decode_shared_arguments(L, kw, want):
 def prefill(L, cache=None, q=P(0x10), bt=P(0x20), mb=4, cq=P(0x30), ck=P(0x40), cu=P(0x50),
             pl=P(0x60), G=1, B=2, H=4, T=8, scale=0.1, out=P(0x70)):
     c = cache or _cache()
-    return L.pa_prefill_shared(q, ctypes.byref(c), bt, mb, cq, ck, cu, pl, G, B, H, T, 0, scale,
+    return L.pa_prefill_shared(q, ctypes.byref(c), bt, mb, cq, ck, cu, pl, G, 0, B, H, T, 0, scale,
                                out, None, 0, None)
 
 

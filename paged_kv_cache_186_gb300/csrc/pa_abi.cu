@@ -139,13 +139,14 @@ pa_status encode_cache_map(CUtensorMap* map, void* base, const pa_kv_cache* c, i
 }
 
 // Recently encoded cache tensor maps: encoding is pure host work but costs a
-// few microseconds, and a decode loop passes the same cache every step.
+// few microseconds, and a decode loop passes the same caches every step (four
+// maps a layer where shared keys are attended to beside each sequence's own).
 struct MapEntry {
   void* base;
   int num_blocks, block_size, num_kv_heads, head_dim, dtype, device, kind;
   CUtensorMap map;
 };
-constexpr int kMapCache = 16;
+constexpr int kMapCache = 256;
 MapEntry g_maps[kMapCache];
 int g_map_count = 0, g_map_next = 0;
 std::mutex g_map_mu;

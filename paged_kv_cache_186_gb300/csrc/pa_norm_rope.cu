@@ -11,7 +11,9 @@
 // sc = max|x| / 448 (E4M3) or / 127 (INT8) taken from the unrounded row.
 // norm_rope_axes_store (AXES): a token has a position on each of up to four axes
 // (time, height, width of an image or a video), and pair i takes its row of the
-// table from the position on its own axis, positions[pair_axis[i]][t].
+// table from the position on its own axis, positions[pair_axis[i]][t]. 16383 tokens
+// of 32 + 8 + 8 rows of 128, all dims rotated, three axes: 92 us on one GB300, 4.5
+// TB/s (70 % of the issue slots); 7, 6 or 10 CTAs an SM instead of 8: 96, 105, 112.
 //
 // How: a row of head_dim elements belongs to head_dim/8 lanes with one 16-byte
 // chunk each, so every load and store is a 16-byte vector and a warp holds 2

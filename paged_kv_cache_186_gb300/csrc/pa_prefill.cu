@@ -60,9 +60,12 @@
 //     the weight lies on few keys: the sinks' tile, and every tile of a window
 //     below 128 keys. The sinks' second term: 105.1 -> 108.9 us and 3.63 -> 3.68
 //     ms below, 39.8 -> 41.1 on 32 short sequences. One GB300, 8 sequences of the
-//     benchmark's lengths, window 1000 + 4 sinks: 109 us, 0.30 of the bf16 rate; 2
-//     prompts of 9001-16384 new tokens, window 4096: 3.68 ms, 0.52 of it (the
+//     benchmark's lengths, window 1000 + 4 sinks: 99 us, 0.32 of the bf16 rate; 2
+//     prompts of 9001-16384 new tokens, window 4096: 3.31 ms, 0.57 of it (the
 //     chain S, softmax, P.V, next S of each key tile).
+//   * Copies and MMAs are issued by one elected lane, not by lane 0: their operands
+//     then come from uniform registers without a detour (benchmark 144 -> 131 us
+//     with a cold L2, the windowed cases above 109 -> 99 us and 3.68 -> 3.31 ms).
 //   * The variant of pa_prefill_shared (SH) is a window whose first key is where
 //     the group's shared keys end, for all rows alike; it leaves (max, sum,
 //     unnormalised O) in fp32 for the merge (pa_shared.cu).

@@ -21,15 +21,38 @@
 // tiles of 128 rows (128/G tokens x the G query heads of the kv head); a unit is
 // one 128-key tile of it. Every CTA takes an equal run of units, so one long
 // prefix is spread over all SMs and short ones are not, and leaves one partial
-// per segment it meets. The CTA is organised as the prefill kernel: K, V and Q
-// arrive by TMA through their own rings (warps 8, 10, 11), warp 9 issues the
-// tcgen05 MMAs, two softmax warpgroups own one TMEM lane (row) a thread. With
-// two row tiles each warpgroup has its own (a K/V tile serves 256 rows); with
-// one, both take its key tiles in turn and merge at the end of the segment.
-// P goes into P.V as two bf16 terms, bf16(p) and bf16(p - bf16(p)): rounded
-// once, a row whose weight lies on few keys misses the library's tolerance
-// (1.28e-2 measured on rows with four dominant keys), and shared prompts begin
-// with such keys.
+// per segment it meets. Sixteen warps:
+//   * warp 8 brings Q and K, warp 10 V, by TMA (one box per physical block and 64
+//     dims), each through its own ring, block ids read 32 ahead. One elected lane
+//     issues all copies of a tile: behind elect.sync their operands are taken from
+//     uniform registers, behind a comparison of the lane number a 16-copy tile took
+//     1300-1600 clocks instead of 400-480.
+//   * warps 12-15 turn V into f16 times a power of two (moved when a tile's largest
+//     value leaves its range, O being rescaled with it), and widen 8-bit codes, K
+//     to bf16 and V to f16, exactly; their scales go to the scores and the weights.
+//     P then goes into P.V as one f16 term (11 bits, at most 2^-11 of a weight off).
+//     In bf16 a row whose weight lies on few keys misses the library's tolerance
+//     (1.28e-2 measured on rows with four dominant keys, and shared prompts begin
+//     with such keys), and a second bf16 term costs as much tensor time again.
+//   * warps 9 and 11 issue the MMAs of one half each, one thread of each from end
+//     to end. A half is one of two row tiles (PAIR: a K/V tile serves 256 rows), or
+//     one of the two takers of a single row tile's key tiles, in turn, whose
+//     results meet at the end of a segment.
+//   * warps 0-7: a softmax warpgroup a half, one TMEM lane (row) a thread, 64 keys a
+//     step. S is read into registers at once and its columns given back, so that
+//     the next S is made during the step; P has two buffers of its own. TMEM, 512
+//     columns: per half S 64, P 2 x 32, O 128.
+// What it measured, per 128-key tile of a CTA with two row tiles (questions of 16-256
+// tokens over four documents, 32/8 heads of 128, one GB300):
+// S of 128 keys with P stored over it 6000 clocks; two S buffers of 64 keys, MMAs
+// issued by lane 0 8900, by one elected thread 4900; f16 P 4800; S given back once
+// read, an MMA warp a half 3850; fewer waits in a step 3600. 2.0 us a tile now, 0.66
+// of the measured bf16 rate. The bound is the softmax step (about 1400 clocks, of
+// which 440 are the exponentials) next to shared memory, busy 3250 clocks of a tile
+// at 128 bytes a clock (192 KB of operands of Q.K, 64 of P.V, 64 of copies, 64-96 of
+// conversion): a satisfied wait on an mbarrier takes 200 clocks there. With one row
+// tile a call is bound by reading the keys: 32 sequences behind 131067 keys take 82
+// us in the CTAs, 6.5 TB/s. 8-bit codes 4700 clocks a tile (scales and widening).
 #include <algorithm>
 #include <type_traits>
 
@@ -320,7 +343,7 @@ struct PieceWalk {
   }
 };
 
-constexpr int kThreads = 512;  // 2 x 4 softmax warps, Q and K, 2 MMA and V warps, 4 converting warps
+constexpr int kThreads = 512;  // 8 softmax warps, Q and K, MMA, V, MMA, 4 converting warps
 // Register split (setmaxnreg) of the launch's 512 x 128.
 constexpr int kSoftmaxRegs = 160;
 constexpr int kControlRegs = 96;
@@ -495,16 +518,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int tid = threadIdx.x - 384;  // and, of 8-bit codes, the thread's key of the tile
     uint32_t c = 0;  // key tiles so far
     int k = 0;       // log2 of V's factor, or of the V scales'
+    uint32_t xc = 0;  // maxima taken so far
     bool ok = true;
     // the largest of the four warps' values
     auto all_max = [&](uint32_t v) {
       v = __reduce_max_sync(kFull, v);
+      const uint32_t b = xc++ & 1;
       if (lane == 0) {
-        cmax[(c & 1) * 4 + (warp - 12)] = v;
+        cmax[b * 4 + (warp - 12)] = v;
         mbar_arrive(bar(BAR_X));
       }
-      ok = wait(BAR_X, c & 1);
-      const uint4 m = *reinterpret_cast<const uint4*>(cmax + (c & 1) * 4);
+      ok = wait(BAR_X, b);
+      const uint4 m = *reinterpret_cast<const uint4*>(cmax + b * 4);
       return max(max(m.x, m.y), max(m.z, m.w));
     };
     // keep the factor while it puts the tile's largest value (bits of a positive
@@ -555,8 +580,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             m = __vmaxu2(m, __vmaxu2(__vmaxu2(x[i].x & 0x7fff7fffu, x[i].y & 0x7fff7fffu),
                                      __vmaxu2(x[i].z & 0x7fff7fffu, x[i].w & 0x7fff7fffu)));
           }
-          m = min(max(m >> 16, m & 0xffffu), 0x7f7fu);
-          m = all_max(m);
+          m = all_max(max(m >> 16, m & 0xffffu));
+          if (ok && m >= 0x7f80u) {  // some V is not finite: the largest of the others
+            m = 0;
+#pragma unroll 1
+            for (int i = 0; i < N; ++i) {
+              const uint4 y = tile[128 * i];
+              const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                const uint32_t a0 = w[j] & 0x7fffu, a1 = (w[j] >> 16) & 0x7fffu;
+                m = max(m, max(a0 < 0x7f80u ? a0 : 0u, a1 < 0x7f80u ? a1 : 0u));
+              }
+            }
+            m = all_max(m);
+          }
           if (!ok) break;
           move_factor(m << 16, 6, 14, 11);
           const uint64_t f2 = tc::f32x2(pow2i(k), pow2i(k));

@@ -501,7 +501,7 @@ pa_status pa_prefill_window(const void* q, const pa_kv_cache* cache, const int32
  *   other arguments, support (bf16 caches, head_dim 128) and arithmetic as
  *   pa_prefill_varlen. Batches and num_groups above 16384 return
  *   PA_ERR_UNSUPPORTED. max_q_len also chooses the kernel of a sequence's own keys,
- *   as for pa_prefill_window.
+ *   as for pa_prefill_window; rows of out past that bound hold nothing of meaning.
  */
 size_t pa_prefill_shared_workspace_size(const pa_kv_cache* cache, int32_t num_heads,
                                         int32_t total_q, int32_t num_groups);

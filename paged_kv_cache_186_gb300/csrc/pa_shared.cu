@@ -400,7 +400,7 @@ enum {
   BAR_DRAIN,                     // + half
   NBAR = BAR_DRAIN + 2
 };
-static_assert(NBAR * 8 + kMaxStages * 4 + 8 * 4 + 8 <= 640, "barriers and small arrays");
+static_assert(NBAR * 8 + kMaxStages * 4 + 8 * 4 + 12 <= 640, "barriers and small arrays");
 
 // Bounded waits that also give up when another role of the CTA has aborted: by
 // one thread, and by a warp. (The timer is read and the flag looked at every 64
@@ -479,6 +479,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int* const fac = reinterpret_cast<int*>(bars + NBAR);  // (kV) V's factor is 2^fac
   uint32_t* const tmem_slot = reinterpret_cast<uint32_t*>(fac + kMaxStages);
   volatile int* const abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  int* const half_k = reinterpret_cast<int*>(tmem_slot + 2);  // the second half's factor
   const uint32_t bar0 = smem_addr(bars);
   auto bar = [&](int i) { return bar0 + 8u * i; };
   if (threadIdx.x == 0) {
@@ -533,11 +534,19 @@ __global__ void __launch_bounds__(kThreads, 1)
       return max(max(m.x, m.y), max(m.z, m.w));
     };
     // keep the factor while it puts the tile's largest value (bits of a positive
-    // float) at 2^lo .. 2^(hi + 1), else move the value to 2^mid
+    // float) at 2^lo .. 2^(hi + 1), else move the value to 2^mid. Within a piece it
+    // rises to no more than 2^70 times its smallest: O, below 2^47 in f16 products of
+    // at most 2^30, is multiplied by that and stays finite. (What is then lost is
+    // below 2^-90 of the piece's largest value.)
+    constexpr int kRise = 70;
+    int k_min = 1 << 20;
     auto move_factor = [&](uint32_t bits, int lo, int hi, int mid) {
-      if (bits == 0) return;
-      const int e = static_cast<int>(bits >> 23) - 127;
-      if (e + k < lo || e + k > hi) k = min(max(mid - e, -120), 90);
+      if (bits != 0) {
+        const int e = static_cast<int>(bits >> 23) - 127;
+        if (e + k < lo || e + k > hi) k = min(max(mid - e, -120), 80);
+      }
+      k = min(k, k_min + kRise);
+      k_min = min(k_min, k);
     };
     auto publish = [&](int b) {  // this warp's writes to a stage, to the MMAs
       fence_proxy_async_smem();
@@ -545,6 +554,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (lane == 0) mbar_arrive(bar(b));
     };
     while (ok && walk.next(a, p)) {
+      k_min = 1 << 20;
       float ks = 0.f, vs = 0.f;  // Q8: scales of this thread's key
       int phys1 = -1;            // its block in the next tile
       const long long bt_row = static_cast<long long>(p.owner) * a.max_blocks;
@@ -1000,11 +1010,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(bar(BAR_P + 2 * hf + (x & 1)));
       }
       if (!ok) break;
-      // ---- the piece's partial: (max, sum) and O, unnormalised. O's factor 2^k
-      // goes into them: O 2^(m - k) stays what it is, and so does l 2^m.
-      m_used -= kLift + static_cast<float>(k);
-      l *= pow2i(k);
-      float f0 = 1.f, f1 = 0.f;
+      // ---- the piece's partial: (max, sum) and O, unnormalised, without P's lift
+      // and V's factor (powers of two)
+      const int lift = static_cast<int>(kLift);
+      l *= pow2i(-lift);
+      float f0 = pow2i(-k - lift), f1 = 0.f;
       const bool both = !PAIR && T > 1;
       if constexpr (!PAIR) {
         if (both) {
@@ -1013,6 +1023,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = merged == 0 || wait(BAR_E + 1, (merged - 1) & 1);
             if (!ok) break;
             half_ml[r] = make_float2(m_used, l);
+            if (r == 0) *half_k = k;
             __syncwarp();
             if (lane == 0) mbar_arrive(bar(BAR_ML));
             ++merged;
@@ -1025,9 +1036,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float2 o = half_ml[r];
           ++merged;
           const float m = fmaxf(m_used, o.x);
-          f0 = m_used == -INFINITY ? 0.f : fast_exp2(m_used - m);
-          f1 = o.x == -INFINITY ? 0.f : fast_exp2(o.x - m);
-          l = l * f0 + o.y * f1;
+          const float e0 = m_used == -INFINITY ? 0.f : fast_exp2(m_used - m);
+          const float e1 = o.x == -INFINITY ? 0.f : fast_exp2(o.x - m);
+          f0 *= e0;
+          f1 = e1 * pow2i(-*half_k - lift);
+          l = l * e0 + o.y * e1;
           m_used = m;
         } else if (hf == 1) {
           continue;
@@ -1050,6 +1063,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int j = 0; j < 32; ++j)
             w[j] = __float_as_uint(__uint_as_float(w[j]) * f0 + __uint_as_float(v[j]) * f1);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(__uint_as_float(w[j]) * f0);
         }
         if (valid) {
 #pragma unroll

@@ -310,7 +310,8 @@ def test_values_of_any_magnitude(kv):
     blocks = s.bt[0, :75].long()
     t = s.v_cache if kv == "bf16" else s.v_scale
     ref = t.clone()
-    for shifts in ([0, -30, 40, 5], [40, 0, -30, 12], [-30, -30, -30, -30]):
+    for shifts in ([0, -30, 40, 5], [40, 0, -30, 12], [-30, -30, -30, -30], [100, -20, -90, 3],
+                   [-90, 3, 100, -20], [-75, -60, -75, -75]):
         t.copy_(ref)
         for i, e in enumerate(shifts):
             part = blocks[i * 19:(i + 1) * 19]
@@ -362,3 +363,31 @@ def test_without_always_small_calls_are_decode(kv, batch, prefix, shares):
     assert torch.equal(out, always if shares else ref)
     assert not torch.equal(always, ref)
     assert_attention_close(out, ref.double().cpu().numpy(), "decode")
+
+
+@pytest.mark.parametrize("kv, D", [("bf16", 128), ("bf16", 64), ("fp8", 128)])
+def test_long_own_contexts(kv, D):
+    # own segments of more parts than the merge takes (merged before it), next to short ones
+    s = make([(64, [21000, 70, 5003, 64]), (33, [30, 9000])], 8, 2, D, 16, kv, seed=590,
+             outside=((15000,), (3,)))
+    for bound in (0, 21000):
+        assert_attention_close(run(s, max_context_len=bound), decode64(s), "long own")
+
+
+def test_two_calls_at_once_on_two_streams():
+    cases = [make([(3000, [3010 + i for i in range(40)])], 8, 2, 128, 16, seed=591),
+             make([(700, [720, 705, 800]), (64, [65] * 9)], 16, 2, 128, 32, "fp8", seed=592)]
+    want = [run(s) for s in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    outs = [[], []]
+    torch.cuda.synchronize()
+    for _ in range(25):
+        for s, stream, out in zip(cases, streams, outs):
+            with torch.cuda.stream(stream):
+                out.append(pa.decode_shared(s.q, s.k_cache, s.v_cache, s.bt, s.context_lens,
+                                            s.cu_groups, s.prefix_lens, s.scale, always=True,
+                                            k_scale=s.k_scale, v_scale=s.v_scale))
+    torch.cuda.synchronize()
+    assert pa.get_device_error() == 0
+    for w, out in zip(want, outs):
+        assert all(torch.equal(w, o) for o in out)

@@ -198,3 +198,31 @@ def test_the_choice_follows_the_lengths_and_mixes_with_sequences_outside():
     s = make([(64, [80, 81, 0]), (100, [120])], 8, 2, 128, 16, seed=771,
              new=[5, 7, 10, 2, 3, 20, 12], outside=((50, 7), (300,)))
     assert_attention_close(run(s, always=False), prefill64(s), "outside")
+
+
+def test_a_bound_below_the_longest_sequence_keeps_the_others_right():
+    s = make([(200, [230, 300, 215])], 8, 2, 128, 16, seed=780, new=[20, 64, 5])
+    want = prefill64(s)
+    out = run(s, max_q_len=32)  # rows of the second sequence past the grid hold anything
+    rows = [*range(20), *range(84, 89)]
+    assert_attention_close(out[rows], want[rows], "the others")
+
+
+def test_two_calls_at_once_on_two_streams():
+    cases = [make([(2000, [2010 + 3 * i for i in range(12)])], 8, 2, 128, 16, seed=781,
+                  new=[1 + i % 9 for i in range(12)]),
+             make([(700, [800, 705, 1000])], 16, 2, 128, 32, seed=782, new=[90, 5, 250])]
+    want = [run(s) for s in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    outs = [[], []]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for s, stream, out in zip(cases, streams, outs):
+            with torch.cuda.stream(stream):
+                out.append(pa.prefill_shared(s.q, s.k_cache, s.v_cache, s.bt, s.cu_q, s.cu_k,
+                                             s.cu_groups, s.prefix_lens, s.scale, always=True,
+                                             max_q_len=max(s.new)))
+    torch.cuda.synchronize()
+    assert pa.get_device_error() == 0
+    for w, out in zip(want, outs):
+        assert all(torch.equal(w, o) for o in out)

@@ -114,6 +114,7 @@ constexpr int kPlanGroups = 512;
 __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedArgs a) {
   __shared__ long long part[32];
   __shared__ int s_cu[kPlanGroups + 1], s_keys[kPlanGroups];
+  __shared__ float sums[4][kPlanThreads / 32];
   const SharedPlan& p = a.plan;
   const int G = a.num_groups, B = a.batch, tid = threadIdx.x;
   const int warp = tid >> 5, lane = tid & 31;
@@ -178,33 +179,38 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedA
   // behind 8192 567 / 505, 8 of 32 behind 2048 53 / 31, 2 of 128 behind 8192 80 /
   // 129. (A decode step is chosen for on the host: its kernel's own cost is small.)
   if (!decode && !a.always) {
-    auto add = [](long long x, long long y) { return x + y; };
-    auto total = [&](long long v) {
-      block_scan<long long>(v, part, add);
-      const long long t = part[31];
-      __syncthreads();
-      return t;
-    };
     const int span = a.own_tokens;  // new tokens of a sequence that one CTA takes
-    long long ctas = 0, walked = 0, units = 0, rows = 0;
+    float v[4] = {0.f, 0.f, 0.f, 0.f};  // CTAs, their key tiles, shared units, rows
     for (int g = warp; g < G; g += kPlanThreads / 32) {
       const int KT = (keys[g] + kBN - 1) / kBN, b0 = cu[g], b1 = cu[g + 1];
       if (KT == 0) continue;
       for (int b = b0 + lane; b < b1; b += 32) {
         const int n = (max(a.cu_q[b + 1] - a.cu_q[b], 0) + span - 1) / span;
-        ctas += n;
-        walked += static_cast<long long>(n) * KT;
+        v[0] += n;
+        v[1] += static_cast<float>(n) * KT;
       }
       if (lane == 0) {
         const int t = p.tok[2 * g + 1] - p.tok[2 * g], per = a.tokens_per_tile * a.row_tiles;
-        units += static_cast<long long>((t + per - 1) / per) * KT;
-        rows += t;
+        v[2] += static_cast<float>((t + per - 1) / per) * KT;
+        v[3] += t;
       }
     }
-    const float n = static_cast<float>(total(ctas)) * a.num_kv_heads;
-    const float tiles = static_cast<float>(total(walked)) * a.num_kv_heads / fmaxf(n, 1.f);
-    const float u = static_cast<float>(total(units)) * a.num_kv_heads;
-    const float r = static_cast<float>(total(rows)) * a.num_heads;
+    // the CTA's sums, the same bits in every thread
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) v[i] += __shfl_xor_sync(kFull, v[i], o);
+      if (lane == 0) sums[i][warp] = v[i];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i] = sums[i][lane];
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) v[i] += __shfl_xor_sync(kFull, v[i], o);
+    }
+    const float n = v[0] * a.num_kv_heads, tiles = v[1] / fmaxf(v[0], 1.f);
+    const float u = v[2] * a.num_kv_heads, r = v[3] * a.num_heads;
     const float waves = ceilf(n / a.ctas);
     const float unshared = waves * tiles * 1.8f;
     const float shared = ceilf(u / a.ctas) * (a.row_tiles == 2 ? 2.f : 1.6f) + 14.f + 6.f * waves +
@@ -902,19 +908,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint32_t ct = c0 + (st >> 1);
         const int sv = ct % R::kV;
         ok = wait(BAR_S + hf, x & 1);
-        // the tile's V is converted: its factor and scales are there (asked for only
-        // after S: V of the tiles before is then known to be)
-        if ((st & 1) == 0) ok = ok && wait(BAR_VF + sv, (ct / R::kV) & 1);
         if (!ok) break;
         tc::fence_after_sync();
         uint32_t u[2][32];
 #pragma unroll
         for (int c = 0; c < 2; ++c) tc::tmem_ld32(S + 32 * c, u[c]);
+        // (S on its way) the tile's V is converted: its factor and scales are there
+        // (asked for only after S: V of the tiles before is then known to be)
+        if ((st & 1) == 0) ok = wait(BAR_VF + sv, (ct / R::kV) & 1);
         const int k_new = fac[sv];
         const float* const sc = scales + (2 * sv) * kBN + (st & 1) * kSN;
         tc::tmem_wait_ld();
         tc::fence_before_sync();
         __syncwarp();
+        if (!ok) break;
         if (lane == 0) mbar_arrive(bar(BAR_SR + hf));
         if constexpr (Q8) {  // K scales
 #pragma unroll

@@ -279,6 +279,12 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedA
     return fits && cu[lo] <= b && b < cu[lo + 1] && keys[lo] > 0 ? lo : -1;
   };
   if (decode) {
+    // (-1, 0): no own parts, until the decode kernel has finished the segment that
+    // leaves some. One whose wait runs out names none: the merge must not take what
+    // another call left here for slots and counts. (128 coalesced stores a thread at
+    // 16384 sequences of 8 kv heads.)
+    for (long long i = tid; i < static_cast<long long>(B) * a.num_kv_heads; i += kPlanThreads)
+      a.own_parts[i] = make_int2(-1, 0);
     for (int b = tid; b < B; b += kPlanThreads) {
       const int g = group_of(b);
       p.row_vis[b] = kv_len(b);

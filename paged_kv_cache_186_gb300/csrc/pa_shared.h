@@ -41,7 +41,8 @@ struct SharedArgs {
   float* own_o;     // (rows, H, D) fp32, of each row's own keys
   float2* own_ml;   // (rows, H)
   // decode: where a sequence and kv head's own result is: (-1, 1) in own_o, else
-  // (first warp, parts) in the decode kernel's partial slots
+  // (first warp, parts) in the decode kernel's partial slots; the plan sets (-1, 0),
+  // nowhere
   int2* own_parts;         // (rows, Hkv), NULL for prefill
   const float* slot_o;     // (slots, slot_rows, D)
   const float2* slot_ml;   // (slots, slot_rows)

@@ -330,7 +330,9 @@ pa_status pa_decode_scored(const void* q, const pa_kv_cache* cache, const int32_
  *                (by the batch, the groups and the length bound), else the call is
  *                pa_decode; other values: whether or not it pays.
  *   workspace    at least pa_decode_shared_workspace_size() bytes (0: the shape is
- *                not supported), contract as for pa_decode.
+ *                not supported), contract as for pa_decode. The size never falls as
+ *                batch, num_groups or the length bound grow: a workspace for a
+ *                program's largest serves its smaller calls (same heads and cache).
  *   scale        > 0 (PA_ERR_SHAPE).
  *   other arguments as pa_decode. Batches and num_groups above 16384 return
  *   PA_ERR_UNSUPPORTED. K and V of shared keys past the context_len of a shorter
@@ -497,7 +499,8 @@ pa_status pa_prefill_window(const void* q, const pa_kv_cache* cache, const int32
  *                from the lengths.
  *   workspace    at least pa_prefill_shared_workspace_size() bytes (0: the shape is
  *                not supported): about 8 * head_dim bytes per query row. Contents on
- *                entry are ignored; calls sharing one workspace must not overlap.
+ *                entry are ignored; calls sharing one workspace must not overlap. The
+ *                size never falls as total_q or num_groups grow.
  *   other arguments, support (bf16 caches, head_dim 128) and arithmetic as
  *   pa_prefill_varlen. Batches and num_groups above 16384 return
  *   PA_ERR_UNSUPPORTED. max_q_len also chooses the kernel of a sequence's own keys,

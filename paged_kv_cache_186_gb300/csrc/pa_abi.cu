@@ -443,6 +443,17 @@ pa::SharedArgs shared_args(const SharedCall& call, const pa::SharedLayout& layou
   return a;
 }
 
+// The workspace of pa_decode_shared: enough for every smaller batch and number of
+// groups too.
+size_t decode_shared_bytes(const pa_kv_cache* cache, int32_t batch, int32_t num_heads, int cap,
+                           int32_t num_groups, int num_sms) {
+  const size_t decode_bytes = pa::decode_workspace_upto(
+      batch, num_heads, cache->num_kv_heads, cache->head_dim, cache->block_size,
+      static_cast<int>(cache->dtype), cap, num_sms);
+  return pa::shared_workspace_bytes(decode_bytes, batch, num_heads, cache->num_kv_heads,
+                                    cache->head_dim, num_groups, num_sms);
+}
+
 // The workspace of pa_decode_scored: pa_decode's, then (from ml on) the final
 // (max, 1 / sum) of every query head, then the scores of every key.
 struct ScoredWorkspace {
@@ -494,12 +505,12 @@ pa_status decode_common(const void* q, const pa_kv_cache* cache, const int32_t* 
   const ScoredWorkspace sw =
       scored_workspace(plan.workspace_bytes, batch, num_heads, cap, cache->block_size);
   pa::SharedLayout layout{};
-  if (shared != nullptr)
+  size_t need = scores != nullptr ? sw.bytes : plan.workspace_bytes;
+  if (shared != nullptr) {
     layout = pa::shared_layout(plan.workspace_bytes, batch, num_heads, cache->num_kv_heads,
                                cache->head_dim, shared->num_groups, dev->num_sms);
-  const size_t need = scores != nullptr   ? sw.bytes
-                      : shared != nullptr ? layout.bytes
-                                          : plan.workspace_bytes;
+    need = decode_shared_bytes(cache, batch, num_heads, cap, shared->num_groups, dev->num_sms);
+  }
   if (need > 0 && (workspace == nullptr || workspace_bytes < need || !aligned16(workspace)))
     return PA_ERR_WORKSPACE;
   if (window > 0 && plan.persistent_ctas == 0) return PA_ERR_UNSUPPORTED;
@@ -772,7 +783,9 @@ pa_status prefill_common(const void* q, const pa_kv_cache* cache, const int32_t*
   if (shared != nullptr) {
     layout = pa::shared_layout(0, total_q, num_heads, cache->num_kv_heads, 128, shared->num_groups,
                                dev->num_sms);
-    if (shared->workspace == nullptr || shared->workspace_bytes < layout.bytes ||
+    const size_t need = pa::shared_workspace_bytes(0, total_q, num_heads, cache->num_kv_heads, 128,
+                                                   shared->num_groups, dev->num_sms);
+    if (shared->workspace == nullptr || shared->workspace_bytes < need ||
         !aligned16(shared->workspace))
       return PA_ERR_WORKSPACE;
   }
@@ -853,17 +866,14 @@ pa_status pa_prefill_window(const void* q, const pa_kv_cache* cache, const int32
 size_t pa_decode_shared_workspace_size(const pa_kv_cache* cache, int32_t batch, int32_t num_heads,
                                        int32_t max_blocks_per_seq, int32_t num_groups,
                                        int32_t max_context_len) {
-  const size_t decode_bytes =
-      pa_decode_workspace_size(cache, batch, num_heads, max_blocks_per_seq, max_context_len);
-  if (decode_bytes == 0 || batch > pa::kMaxPersistentBatch || num_groups < 0 ||
-      num_groups > pa::kMaxPersistentBatch || num_heads % cache->num_kv_heads != 0 ||
-      num_heads / cache->num_kv_heads > 8)
+  if (check_cache(cache) != PA_OK || batch <= 0 || batch > pa::kMaxPersistentBatch ||
+      max_blocks_per_seq <= 0 || num_groups < 0 || num_groups > pa::kMaxPersistentBatch ||
+      num_heads <= 0 || num_heads % cache->num_kv_heads != 0 || num_heads / cache->num_kv_heads > 8)
     return 0;
   DeviceInfo* dev = nullptr;
   if (device_info(&dev) != PA_OK) return 0;
-  return pa::shared_layout(decode_bytes, batch, num_heads, cache->num_kv_heads, cache->head_dim,
-                           num_groups, dev->num_sms)
-      .bytes;
+  const int cap = decode_len_cap(cache, max_blocks_per_seq, max_context_len);
+  return decode_shared_bytes(cache, batch, num_heads, cap, num_groups, dev->num_sms);
 }
 
 pa_status pa_decode_shared(const void* q, const pa_kv_cache* cache, const int32_t* block_tables,
@@ -907,8 +917,8 @@ size_t pa_prefill_shared_workspace_size(const pa_kv_cache* cache, int32_t num_he
     return 0;
   DeviceInfo* dev = nullptr;
   if (device_info(&dev) != PA_OK) return 0;
-  return pa::shared_layout(0, total_q, num_heads, cache->num_kv_heads, 128, num_groups, dev->num_sms)
-      .bytes;
+  return pa::shared_workspace_bytes(0, total_q, num_heads, cache->num_kv_heads, 128, num_groups,
+                                    dev->num_sms);
 }
 
 pa_status pa_prefill_shared(const void* q, const pa_kv_cache* cache, const int32_t* block_tables,

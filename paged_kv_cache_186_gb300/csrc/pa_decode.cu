@@ -1684,6 +1684,20 @@ DecodePlan plan_decode(int batch, int num_heads, int num_kv_heads, int head_dim,
   return p;
 }
 
+// Within a bucket of batches the partial slots grow with the batch; the next one may
+// have fewer CTAs an SM.
+size_t decode_workspace_upto(int batch, int num_heads, int num_kv_heads, int head_dim,
+                             int block_size, int kv, int len_cap, int num_sms) {
+  auto bytes = [&](int b) {
+    return plan_decode(b, num_heads, num_kv_heads, head_dim, block_size, kv, len_cap, num_sms)
+        .workspace_bytes;
+  };
+  size_t most = bytes(batch);
+  constexpr int kBucket = Inst<128, 16, kKvBf16>::kBucket;
+  for (int b = kBucket; b < batch; b += kBucket) most = std::max(most, bytes(b));
+  return most;
+}
+
 cudaError_t launch_decode(const DecodeArgs& a, const CUtensorMap& kmap, const CUtensorMap& vmap,
                           cudaStream_t stream) {
   if (a.kv != kKvBf16 && a.head_dim != 128) return cudaErrorInvalidValue;

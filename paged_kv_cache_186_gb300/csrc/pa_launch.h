@@ -106,6 +106,9 @@ struct DecodePlan {
 
 DecodePlan plan_decode(int batch, int num_heads, int num_kv_heads, int head_dim, int block_size,
                        int kv, int len_cap, int num_sms);
+// The most workspace_bytes that plan_decode has for any batch up to this one.
+size_t decode_workspace_upto(int batch, int num_heads, int num_kv_heads, int head_dim,
+                             int block_size, int kv, int len_cap, int num_sms);
 
 // Second launch of pa_decode_scored: adds the softmax weight of every key,
 // summed over the query heads of its kv head, to scores (NB, Hkv, bs).

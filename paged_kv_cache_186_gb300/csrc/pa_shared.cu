@@ -1289,18 +1289,17 @@ cudaError_t launch_keys(const SharedArgs& a, const CUtensorMap& qmap, const CUte
               : launch_keys_inst<D, 32, KV, false>(a, qmap, kmap, vmap, stream);
 }
 
-}  // namespace
+long long query_tiles(int rows, int tokens_per_tile) {
+  return (rows + static_cast<long long>(tokens_per_tile) - 1) / tokens_per_tile;
+}
 
-SharedLayout shared_layout(size_t base, int rows, int num_heads, int num_kv_heads, int head_dim,
-                           int num_groups, int num_sms) {
+// The layout of a call with `row_tiles` tiles a segment.
+SharedLayout layout_of(size_t base, int rows, int num_heads, int num_kv_heads, int head_dim,
+                       int num_groups, int num_sms, int row_tiles) {
   auto up = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
   SharedLayout l{};
   l.tokens_per_tile = kBM / (num_heads / num_kv_heads);
-  // Two row tiles a segment where the groups have the rows for them on average:
-  // a K/V tile then serves twice the rows. Smaller groups leave the second tile
-  // empty, and are bound by reading the keys.
-  const long long tiles = (rows + static_cast<long long>(l.tokens_per_tile) - 1) / l.tokens_per_tile;
-  l.row_tiles = tiles > std::max(num_groups, 1) ? 2 : 1;
+  l.row_tiles = row_tiles;
   const long long per_seg = static_cast<long long>(l.tokens_per_tile) * l.row_tiles;
   // every group may end in a segment that is not full
   const long long segs = (rows / per_seg + std::min(num_groups, rows)) * num_kv_heads;
@@ -1320,6 +1319,31 @@ SharedLayout shared_layout(size_t base, int rows, int num_heads, int num_kv_head
   l.own_o = up(l.own_ml + rh * sizeof(float2));
   l.bytes = l.own_o + rh * head_dim * sizeof(float) + 256;  // (to align the address)
   return l;
+}
+
+}  // namespace
+
+SharedLayout shared_layout(size_t base, int rows, int num_heads, int num_kv_heads, int head_dim,
+                           int num_groups, int num_sms) {
+  // Two row tiles a segment where the groups have the rows for them on average:
+  // a K/V tile then serves twice the rows. Smaller groups leave the second tile
+  // empty, and are bound by reading the keys.
+  const bool two = query_tiles(rows, kBM / (num_heads / num_kv_heads)) > std::max(num_groups, 1);
+  return layout_of(base, rows, num_heads, num_kv_heads, head_dim, num_groups, num_sms, two ? 2 : 1);
+}
+
+// Either form takes more with more rows and with more groups, but a call of fewer
+// groups may have two row tiles where one of more has one, and then twice the rows
+// a partial: the larger of the two, with as many groups as each can have.
+size_t shared_workspace_bytes(size_t base, int rows, int num_heads, int num_kv_heads, int head_dim,
+                              int num_groups, int num_sms) {
+  auto bytes = [&](int groups, int row_tiles) {
+    return layout_of(base, rows, num_heads, num_kv_heads, head_dim, groups, num_sms, row_tiles).bytes;
+  };
+  const long long tiles = query_tiles(rows, kBM / (num_heads / num_kv_heads));
+  const size_t one = bytes(num_groups, 1);
+  if (tiles <= 1) return one;
+  return std::max(one, bytes(static_cast<int>(std::min<long long>(num_groups, tiles - 1)), 2));
 }
 
 void shared_pointers(SharedArgs& a, const SharedLayout& l, void* workspace) {

@@ -67,6 +67,10 @@ struct SharedLayout {
 };
 SharedLayout shared_layout(size_t base, int rows, int num_heads, int num_kv_heads, int head_dim,
                            int num_groups, int num_sms);
+// Bytes that serve this call and every one of fewer rows or groups (base: what those
+// need in front of it).
+size_t shared_workspace_bytes(size_t base, int rows, int num_heads, int num_kv_heads, int head_dim,
+                              int num_groups, int num_sms);
 // Fill the workspace pointers of `a` (rows, num_groups set) from a layout.
 void shared_pointers(SharedArgs& a, const SharedLayout& l, void* workspace);
 

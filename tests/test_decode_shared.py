@@ -391,3 +391,34 @@ def test_two_calls_at_once_on_two_streams():
     assert pa.get_device_error() == 0
     for w, out in zip(want, outs):
         assert all(torch.equal(w, o) for o in out)
+
+
+def test_a_workspace_for_the_most_sequences_and_groups_serves_fewer():
+    # fewer groups may have two row tiles a segment, whose partials are twice as large; larger
+    # batches fewer partial slots
+    kc = torch.zeros((4, 16, 8, 128), dtype=torch.bfloat16, device="cuda")
+    small = torch.zeros((4, 16, 1, 64), dtype=torch.bfloat16, device="cuda")
+    for cache, H, batches in ((kc, 32, [1, 7, 31, 32, 33, 64, 65, 200, 256, 257, 960]),
+                              (small, 1, [1, 128, 129, 300, 5000, 9999, 16384]),
+                              (small, 3, [42, 43, 84, 86])):
+        groups = [0, 1, 2, 3, 8, 30, 31, 64, 1000, 16384]
+        for bound in (0, 40):
+            need = torch.tensor([[pa.decode_shared_workspace_size(cache, b, H, 64, g, bound)
+                                  for g in groups] for b in batches])
+            assert (need > 0).all()
+            assert (need.diff(dim=0) >= 0).all() and (need.diff(dim=1) >= 0).all(), need
+            if bound:
+                assert (need <= wide).all()
+            wide = need
+    s = make([(200, [201 + i for i in range(64)])], 32, 8, 128, 16, seed=593)
+    want = decode64(s)
+    ws = torch.full((pa.decode_shared_workspace_size(s.k_cache, 64, 32, s.bt.shape[1], 2),), 255,
+                    dtype=torch.uint8, device="cuda")
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    for cu in ([0, 30, 64], [0, 64], [3, 50]):
+        s.cu_groups, s.prefix_lens = i32(cu), i32([200] * (len(cu) - 1))
+        assert_attention_close(run(s, workspace=ws), want, f"groups {cu}")
+    s.q, s.bt, s.context_lens, s.lens = s.q[:9], s.bt[:9], s.context_lens[:9], s.lens[:9]
+    s.cu_groups = i32([0, 9])
+    s.prefix_lens = s.prefix_lens[:1]
+    assert_attention_close(run(s, workspace=ws), want[:9], "9 sequences")

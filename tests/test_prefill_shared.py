@@ -226,3 +226,21 @@ def test_two_calls_at_once_on_two_streams():
     assert pa.get_device_error() == 0
     for w, out in zip(want, outs):
         assert all(torch.equal(w, o) for o in out)
+
+
+def test_a_workspace_for_the_most_rows_and_groups_serves_fewer():
+    kc = torch.zeros((4, 16, 8, 128), dtype=torch.bfloat16, device="cuda")
+    for H, rows in ((32, [1, 32, 33, 64, 65, 960, 961, 100000]), (128, [8, 9, 16, 17, 4000]),
+                    (8, [1, 128, 129, 257])):
+        need = torch.tensor([[pa.prefill_shared_workspace_size(kc, t, H, g)
+                              for g in (0, 1, 2, 3, 16, 30, 31, 500, 16384)] for t in rows])
+        assert (need > 0).all()
+        assert (need.diff(dim=0) >= 0).all() and (need.diff(dim=1) >= 0).all(), need
+    s = make([(200, [230 + i for i in range(32)])], 32, 8, 128, 16, seed=783, new=[30] * 32)
+    want = prefill64(s)
+    ws = torch.full((pa.prefill_shared_workspace_size(s.k_cache, 960, 32, 30),), 255,
+                    dtype=torch.uint8, device="cuda")
+    i32 = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+    for cu in ([*range(0, 60, 2)][:16] + [32], [0, 32], [*range(30)] + [32]):
+        s.cu_groups, s.prefix_lens = i32(cu), i32([200] * (len(cu) - 1))
+        assert_attention_close(run(s, workspace=ws), want, f"groups {cu}")

@@ -333,6 +333,10 @@ pa_status pa_decode_scored(const void* q, const pa_kv_cache* cache, const int32_
  *                not supported), contract as for pa_decode. The size never falls as
  *                batch, num_groups or the length bound grow: a workspace for a
  *                program's largest serves its smaller calls (same heads and cache).
+ *                Beside pa_decode's it holds fp32 results, head_dim + 2 floats each:
+ *                at most about 2 * num_heads a sequence, 256 a group and kv head
+ *                and 256 an SM (32/8 heads of 128: 23 MB for 64 sequences in one
+ *                group, 181 MB for 1024 in 256).
  *   scale        > 0 (PA_ERR_SHAPE).
  *   other arguments as pa_decode. Batches and num_groups above 16384 return
  *   PA_ERR_UNSUPPORTED. K and V of shared keys past the context_len of a shorter
@@ -498,9 +502,11 @@ pa_status pa_prefill_window(const void* q, const pa_kv_cache* cache, const int32
  *   always       as pa_decode_shared; whether sharing pays is seen on the device,
  *                from the lengths.
  *   workspace    at least pa_prefill_shared_workspace_size() bytes (0: the shape is
- *                not supported): about 8 * head_dim bytes per query row. Contents on
- *                entry are ignored; calls sharing one workspace must not overlap. The
- *                size never falls as total_q or num_groups grow.
+ *                not supported). Contents on entry are ignored; calls sharing one
+ *                workspace must not overlap. The size never falls as total_q or
+ *                num_groups grow. It holds fp32 results, head_dim + 2 floats each: at
+ *                most about 2 * num_heads a query row, 256 a group and kv head and 256
+ *                an SM (32/8 heads: 33 KB a row, 53 MB for 960 rows in one group).
  *   other arguments, support (bf16 caches, head_dim 128) and arithmetic as
  *   pa_prefill_varlen. Batches and num_groups above 16384 return
  *   PA_ERR_UNSUPPORTED. max_q_len also chooses the kernel of a sequence's own keys,

@@ -665,8 +665,8 @@ def prefill_shared(q, k_cache, v_cache, block_tables, cu_seqlens_q, cu_seqlens_k
     """pa_prefill_shared: prefill_varlen of sequences that share their first keys in groups
     (cu_groups, prefix_lens, always: as decode_shared). bf16 caches of head_dim 128. max_q_len (a bound of
     every sequence's new tokens) sizes the grid and lets short questions take their own variant. A
-    workspace (uint8 tensor of prefill_shared_workspace_size bytes, about 8 * head_dim per query
-    row) is allocated in every call that gives none."""
+    workspace (uint8 tensor of prefill_shared_workspace_size bytes: about 8 * head_dim a query row and
+    head, and some MB for the groups and the SMs) is allocated in every call that gives none."""
     if q.dim() != 3:
         raise ValueError("q must be (total_q, num_heads, head_dim)")
     max_q_len = int(max_q_len)

@@ -422,3 +422,20 @@ def test_a_workspace_for_the_most_sequences_and_groups_serves_fewer():
     s.cu_groups = i32([0, 9])
     s.prefix_lens = s.prefix_lens[:1]
     assert_attention_close(run(s, workspace=ws), want[:9], "9 sequences")
+
+
+def test_the_workspace_is_no_larger_than_documented():
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    for D, Hkv, H in ((128, 8, 32), (64, 8, 64), (128, 1, 3), (64, 4, 20), (128, 8, 8)):
+        kc = torch.zeros((4, 16, Hkv, D), dtype=torch.bfloat16, device="cuda")
+        for rows in (1, 7, 64, 960, 1024, 16384):
+            for g in (1, 2, 30, 256, 8192):
+                if g > rows:
+                    continue
+                floats = (D + 2) * (2 * H * rows + 256 * Hkv * g + 256 * sms)
+                decode = pa.decode_workspace_size(kc, min(rows, 256), H, 64)
+                need = pa.decode_shared_workspace_size(kc, rows, H, 64, g)
+                assert need - decode <= 1.1 * 4 * floats, (D, Hkv, H, rows, g)
+                if D == 128 and H // Hkv in (1, 2, 4, 8, 16):
+                    need = pa.prefill_shared_workspace_size(kc, rows, H, g)
+                    assert need <= 1.1 * 4 * floats, (D, Hkv, H, rows, g)

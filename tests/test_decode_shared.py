@@ -439,3 +439,46 @@ def test_the_workspace_is_no_larger_than_documented():
                 if D == 128 and H // Hkv in (1, 2, 4, 8, 16):
                     need = pa.prefill_shared_workspace_size(kc, rows, H, g)
                     assert need <= 1.1 * 4 * floats, (D, Hkv, H, rows, g)
+
+
+@pytest.mark.parametrize("D, seqs", [(64, 700), (128, 400), (64, 500)])
+def test_a_team_of_lanes_for_each_row(D, seqs):
+    # above 16 warps of rows an SM the merge gives a row to a team of lanes, below it to a CTA: with 8
+    # kv heads on 152 SMs from 608 rows of head_dim 64, 304 of 128
+    lens = [[33 + (7 * i + j) % 60 for j in range(seqs // 4)] for i in range(4)]
+    lens[2][5] = lens[3][0] = 0
+    s = make([(32 + 16 * i, [n + 16 * i if n else 0 for n in ls]) for i, ls in enumerate(lens)], 16, 8,
+             D, 16, seed=594)
+    out = run(s)
+    assert_attention_close(out, decode64(s), "teams")
+    assert (out[s.context_lens == 0] == 0).all()
+
+
+@pytest.mark.parametrize("groups", [512, 513, 1023, 1024, 1025, 2049])
+@pytest.mark.parametrize("order", ["ascending", "mixed"])
+def test_more_groups_than_fit_the_plan_or_one_of_its_passes(groups, order):
+    # one prefix for all sequences, so that any partition of them is one of groups that share it:
+    # bounds of empty groups, and such that fall back or lie outside
+    r = np.random.default_rng(groups)
+    n = 1300
+    s = make([(50, [49 + int(x) for x in r.integers(0, 40, n)])], 2, 1, 64, 16, seed=595)
+    cu = np.sort(r.integers(0, n + 1, groups + 1))
+    if order == "mixed":
+        at = r.integers(0, groups + 1, groups // 5)
+        cu[at] = r.integers(-50, n, len(at))
+        cu[-3:] = n, n + 9, 5
+    i32 = lambda x: torch.tensor(np.asarray(x), dtype=torch.int32, device="cuda")
+    s.cu_groups, s.prefix_lens = i32(cu), i32(r.integers(-5, 51, groups))
+    assert_attention_close(run(s), decode64(s), f"{groups} groups")
+
+
+@pytest.mark.parametrize("kv, prefix, own, width", [("bf16", 16, 2000, 0), ("bf16", 30, 100, 2048),
+                                                    ("fp8", 40, 700, 0), ("int8", 5, 400, 0)])
+def test_without_always_a_short_prefix_of_long_contexts(kv, prefix, own, width):
+    # the host's bound takes the whole contexts for shared
+    s = make([(prefix, [prefix + own - 3 * i for i in range(33)])], 32, 8, 128, 16, kv, seed=596)
+    if width:
+        s.bt = torch.cat([s.bt, s.bt.new_full((33, width // 16 - s.bt.shape[1]), -1)], dim=1)
+    out = pa.decode_shared(s.q, s.k_cache, s.v_cache, s.bt, s.context_lens, s.cu_groups,
+                           s.prefix_lens, s.scale, k_scale=s.k_scale, v_scale=s.v_scale)
+    assert_attention_close(out, decode64(s), "short prefix")

@@ -244,3 +244,31 @@ def test_a_workspace_for_the_most_rows_and_groups_serves_fewer():
     for cu in ([*range(0, 60, 2)][:16] + [32], [0, 32], [*range(30)] + [32]):
         s.cu_groups, s.prefix_lens = i32(cu), i32([200] * (len(cu) - 1))
         assert_attention_close(run(s, workspace=ws), want, f"groups {cu}")
+
+
+@pytest.mark.parametrize("new, prefix", [([200, 256, 130], 600), ([3] * 40, 6000)])
+def test_always_where_the_choice_is_measured(new, prefix):
+    # the rows of test_without_always_calls_that_would_not_gain_are_prefill against 64 bits; the first
+    # form has a team of lanes for each row in its merge
+    s = make([(prefix, [prefix + n + 9 for n in new])], 32, 8, 128, 16, seed=760, new=new)
+    want = prefill64(s)
+    assert_attention_close(run(s), want, "always")
+    assert_attention_close(run(s, always=False), want, "chosen")
+
+
+@pytest.mark.parametrize("groups", [513, 1025])
+def test_more_groups_than_fit_the_plan_or_one_of_its_passes(groups):
+    # one prefix for all sequences: any partition of them is one of groups that share it
+    r = np.random.default_rng(groups)
+    n = 700
+    new = [int(x) for x in r.integers(0, 4, n)]
+    s = make([(50, [max(k, 49 + int(x)) for k, x in zip(new, r.integers(0, 40, n))])], 2, 1, 128, 16,
+             seed=784, new=new)
+    cu = np.sort(r.integers(0, n + 1, groups + 1))
+    at = r.integers(0, groups + 1, groups // 5)
+    cu[at] = r.integers(-50, n, len(at))
+    i32 = lambda x: torch.tensor(np.asarray(x), dtype=torch.int32, device="cuda")
+    s.cu_groups, s.prefix_lens = i32(cu), i32(r.integers(-5, 51, groups))
+    want = prefill64(s)
+    assert_attention_close(run(s), want, f"{groups} groups")
+    assert_attention_close(run(s, always=False), want, f"{groups} groups, chosen")

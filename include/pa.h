@@ -339,7 +339,10 @@ pa_status pa_decode_scored(const void* q, const pa_kv_cache* cache, const int32_
  *                group, 181 MB for 1024 in 256).
  *   scale        > 0 (PA_ERR_SHAPE).
  *   other arguments as pa_decode. Batches and num_groups above 16384 return
- *   PA_ERR_UNSUPPORTED. K and V of shared keys past the context_len of a shorter
+ *   PA_ERR_UNSUPPORTED. Arithmetic as pa_decode, but for the shared keys' weights
+ *   in P.V, which are rounded to f16 (11 bits), and their V, which are f16 times a
+ *   power of two: exact down to 2^-20 of the largest of 128 keys, then off by at
+ *   most 2^-31 of it (or 2^-90 of the largest of all, if that is more). K and V of shared keys past the context_len of a shorter
  *   sequence of the group must be finite: it gives them the weight 0.
  */
 size_t pa_decode_shared_workspace_size(const pa_kv_cache* cache, int32_t batch, int32_t num_heads,
@@ -507,9 +510,11 @@ pa_status pa_prefill_window(const void* q, const pa_kv_cache* cache, const int32
  *                num_groups grow. It holds fp32 results, head_dim + 2 floats each: at
  *                most about 2 * num_heads a query row, 256 a group and kv head and 256
  *                an SM (32/8 heads: 33 KB a row, 53 MB for 960 rows in one group).
- *   other arguments, support (bf16 caches, head_dim 128) and arithmetic as
- *   pa_prefill_varlen. Batches and num_groups above 16384 return
- *   PA_ERR_UNSUPPORTED. max_q_len also chooses the kernel of a sequence's own keys,
+ *   other arguments and support (bf16 caches, head_dim 128) as
+ *   pa_prefill_varlen, arithmetic too where a sequence's group shares nothing
+ *   (whether it has no shared block or sharing would not pay). Where it shares:
+ *   weights of shared keys as pa_decode_shared, of its own keys as two bf16 terms.
+ *   Batches and num_groups above 16384 return PA_ERR_UNSUPPORTED. max_q_len also chooses the kernel of a sequence's own keys,
  *   as for pa_prefill_window; rows of out past that bound hold nothing of meaning.
  */
 size_t pa_prefill_shared_workspace_size(const pa_kv_cache* cache, int32_t num_heads,

@@ -241,8 +241,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   // row sees fewer than kBN keys (every key of such a row lies in tile 0), and
   // with a window where there are sinks (they lie in tile 0, and draw most of
   // a row's weight onto a few keys, whose roundings do not average out) and on
-  // every tile of a window of fewer than kBN keys
-  const bool narrow = WIN && min(a.window, kBN) + min(a.sinks, kBN) < kBN;
+  // every tile of a window of fewer than kBN keys. SH, rows that share keys: on every
+  // tile, as the shared keys' weights have more bits than bf16 for the same reason
+  // (the own keys of such a call are few: drafts_b64 97 -> 99 us)
+  const bool narrow = (SH && part) || (WIN && min(a.window, kBN) + min(a.sinks, kBN) < kBN);
   auto two_term = [&](int i, int n) {
     return (n == 0 && (cached + t00 + i * TPT - own < kBN || (WIN && a.sinks > 0))) || narrow;
   };

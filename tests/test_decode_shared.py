@@ -7,6 +7,7 @@ import torch
 import paged_kv_cache_186_gb300 as pa
 from gpu_util import assert_attention_close
 from shared_util import decode64, make, n64
+from test_prefill_shared import weights_of_few_keys_hold
 
 pytestmark = pytest.mark.gpu
 
@@ -482,3 +483,9 @@ def test_without_always_a_short_prefix_of_long_contexts(kv, prefix, own, width):
     out = pa.decode_shared(s.q, s.k_cache, s.v_cache, s.bt, s.context_lens, s.cu_groups,
                            s.prefix_lens, s.scale, k_scale=s.k_scale, v_scale=s.v_scale)
     assert_attention_close(out, decode64(s), "short prefix")
+
+
+@pytest.mark.parametrize("where", ["own", "shared", "both"])
+def test_weights_of_few_dominant_keys_keep_more_bits_than_bf16(where):
+    # (bounds: beside the prefill's test; the own keys' weights are two bf16 terms here too)
+    weights_of_few_keys_hold(where, [1] * 200, run, decode64)

@@ -6,7 +6,7 @@ import torch
 
 import paged_kv_cache_186_gb300 as pa
 from gpu_util import assert_attention_close
-from shared_util import make, prefill64
+from shared_util import make, n64, prefill64
 
 pytestmark = pytest.mark.gpu
 
@@ -272,3 +272,37 @@ def test_more_groups_than_fit_the_plan_or_one_of_its_passes(groups):
     want = prefill64(s)
     assert_attention_close(run(s), want, f"{groups} groups")
     assert_attention_close(run(s, always=False), want, f"{groups} groups, chosen")
+
+
+@pytest.mark.parametrize("where", ["own", "shared", "both"])
+@pytest.mark.parametrize("new", [[1 + i % 5 for i in range(40)], [70, 33, 64, 130, 1, 90]])
+def test_weights_of_few_dominant_keys_keep_more_bits_than_bf16(where, new):
+    # q of a kv head's heads is one direction and a little noise, three keys of the prefix or of each
+    # sequence's own lie along it: their scores are near 11, those of the 600 others N(0, 1), so they
+    # hold 98 % of the weight. An output is then off by at most
+    #   own keys: the scores' fp32 error (below 2^-12 of a weight in all) and 2^-17 of a weight,
+    #             P being two bf16 terms; with 2 % of the weight on keys of the other kind
+    #   shared keys: 2^-11 of a weight (f16) instead
+    # of the largest |V|, and twice that beyond the rounding of the exact result where the output
+    # rounds to the other side of it. One bf16 term would be off by 2^-9 of a weight.
+    weights_of_few_keys_hold(where, new, run, prefill64)
+
+
+def weights_of_few_keys_hold(where, new, call, definition):
+    n = len(new)
+    s = make([(200, [600 + x + 7 * (i % 9) for i, x in enumerate(new)])], 8, 2, 128, 16, seed=785, new=new)
+    g = torch.Generator().manual_seed(786)
+    base = torch.randn((2, 128), generator=g)
+    q = base.repeat_interleave(4, dim=0) + 0.25 * torch.randn(s.q.shape, generator=g)
+    s.q.copy_(q.to(torch.bfloat16))
+    bt = s.bt.cpu()
+    spots = {(bt[b, p // 16].item(), p % 16) for b in range(n)
+             for p in {"own": (195, 340, 530), "shared": (3, 100, 188), "both": (3, 195, 530)}[where]}
+    for block, at in sorted(spots):
+        s.k_cache[block, at] = (base + 0.15 * torch.randn((2, 128), generator=g)).to(torch.bfloat16).cuda()
+    want = definition(s)
+    got = n64(call(s))
+    bits = 2.0 ** -12 + (2.0 ** -17 + 0.02 * 2.0 ** -11 if where == "own" else 2.0 ** -11)
+    top = np.abs(n64(s.v_cache)).max()
+    rounding = np.abs(n64(torch.from_numpy(want).float().to(torch.bfloat16)) - want)
+    assert (np.abs(got - want) - rounding).max() <= 2 * bits * top

@@ -613,9 +613,10 @@ def decode_shared(q, k_cache, v_cache, block_tables, context_lens, cu_groups, pr
     """pa_decode_shared: decode where the sequences cu_groups[g] .. cu_groups[g+1]-1 (int32
     (groups + 1,)) share their first prefix_lens[g] keys (int32 (groups,)): their block table rows
     begin with the same prefix_lens[g] // block_size blocks, which are read and attended to once
-    for the whole group (where that is expected to pay, by the batch, the groups and
-    max_context_len; always: in any case). A workspace (uint8 tensor of
-    decode_shared_workspace_size bytes) is allocated in every call that gives none."""
+    for the whole group (if that would pay were all of max_context_len, or of the table's width,
+    shared; always: in any case). Where prefixes are not most of the contexts decode is faster. A
+    workspace (uint8 tensor of decode_shared_workspace_size bytes) is allocated in every call that
+    gives none."""
     if q.dim() != 3:
         raise ValueError("q must be (batch, num_heads, head_dim)")
     max_context_len = int(max_context_len)

@@ -889,13 +889,19 @@ pa_status pa_decode_shared(const void* q, const pa_kv_cache* cache, const int32_
     return PA_ERR_NULL;
   if (batch > pa::kMaxPersistentBatch || num_groups > pa::kMaxPersistentBatch)
     return PA_ERR_UNSUPPORTED;
-  // Sharing costs two more launches and a merge (about 6 us) and spares at most
-  // this many bytes of K and V (by the host's bound of the lengths). Measured on
-  // one GB300, shared / unshared us: bf16, 8 kv heads of 128, 4 sequences behind
-  // 16384 keys (201 MB) 36 / 35, 8 behind 8192 (235 MB) 30 / 34, 16 behind 2048 (126
-  // MB) 27 / 23 and 4096 (252 MB) 29 / 31, 64 behind 1024 (264 MB) 32 / 30 and 2048
-  // (529 MB) 35 / 46. The decode of 8-bit codes is slower a byte: 8 sequences
-  // behind 2048 keys (29 MB) 31 / 33, 64 behind 2048 (264 MB) 42 / 59.
+  // Sharing costs three more launches and spares at most this many bytes of K and V:
+  // the host has a bound of the lengths, not the prefixes, and takes the whole of it
+  // for shared. Where that is about so (64 own keys), shared / unshared us on one
+  // GB300, from graphs, 8 kv heads of 128: bf16, 4 query heads each, 8 sequences
+  // behind 8192 keys (237 MB) 33 / 32 and 12288 (354 MB) 35 / 40, 16 behind 4096 (256
+  // MB) 31 / 28 and 6144 (381 MB) 32 / 36, 64 behind 1024 (281 MB) 33 / 28 and 1536
+  // (413 MB) 34 / 36; 8 query heads each, 8 behind 8192 37 / 43, 64 behind 1024 37 / 32;
+  // kv heads of 64, 8 behind 16384 (236 MB) 30 / 39. 8-bit codes, 8 query heads: 8 behind
+  // 2048 (30 MB) 32 / 35, 16 behind 1024 (33 MB) 29 / 30, 64 behind 512 (74 MB) 36 / 32; 4
+  // query heads: 26 / 23, 25 / 21, 24 / 25. So the sides cross at 200-400 MB (bf16) and 30-80
+  // MB (8 bits) by shape, and the thresholds miss by up to 5 us there. Short prefixes of
+  // long contexts are taken for shared: 64 sequences, bf16, 16 keys shared and 4096 own
+  // 173 / 161, 2048 and 2048 110 / 88.
   const double saved = static_cast<double>(std::max(0, batch - num_groups)) * 2.0 *
                        decode_len_cap(cache, std::max(max_blocks_per_seq, 0), max_context_len) *
                        cache->num_kv_heads * cache->head_dim * elem_bytes(cache);

@@ -447,7 +447,8 @@ def norm_rope_axes_store(q, k, v, positions, slot_mapping, k_cache, v_cache, pai
     if positions.dim() != 2:
         raise ValueError("positions must be (axes, tokens)")
     if not isinstance(pair_axis, bytes):
-        pair_axis = bytes(pair_axis)  # refuses what is not 0 .. 255
+        # (a list: bytes() takes a number for a length and an array for its memory)
+        pair_axis = bytes(list(pair_axis))  # refuses what is not 0 .. 255
     return _norm_rope(q, k, v, positions, slot_mapping, k_cache, v_cache, pair_axis, q_weight,
                       k_weight, eps, cos_sin, interleaved, q_out, k_scale, v_scale, scores)
 

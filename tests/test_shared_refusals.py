@@ -2,6 +2,7 @@
 a CUDA call, so these run on the CPU."""
 import ctypes
 
+import numpy as np
 import pytest
 import torch
 
@@ -183,3 +184,28 @@ def test_shared_bindings_refuse_numbers_that_do_not_fit_32_bits(big):
     for fn, args, kw, name in calls:
         with pytest.raises(ValueError, match=f"{name} must fit 32 bits"):
             fn(*args, **kw)
+
+
+@pytest.mark.parametrize("pair_axis", [64, torch.tensor(64), np.int64(64), "axes", None,
+                                       np.arange(8), np.zeros(64), torch.zeros(64)])
+def test_axes_that_are_not_integers_one_a_pair_are_refused(pair_axis):
+    # (64 is no list of 64 zeros, and 8 numbers of 8 bytes are not 64 axes)
+    with pytest.raises((TypeError, ValueError)) as e:
+        _axes_call(pair_axis)
+    assert "caches' device" not in str(e.value) and "CUDA" not in str(e.value)
+
+
+@pytest.mark.parametrize("pair_axis", [[0, 1] * 32, (0, 1) * 32, bytes([0, 1] * 32),
+                                       bytearray([0, 1] * 32), np.arange(64) % 2,
+                                       (np.arange(64) % 2).astype(np.int32), torch.arange(64) % 2])
+def test_axes_of_any_integers_reach_the_call(pair_axis, monkeypatch):
+    seen = []
+    monkeypatch.setattr(pa, "_norm_rope", lambda *a: seen.append(a[7]))
+    _axes_call(pair_axis)
+    assert seen == [bytes([0, 1] * 32)]
+
+
+def _axes_call(pair_axis):
+    pa.norm_rope_axes_store(_t((3, 4, 128)), _t((3, 2, 128)), _t((3, 2, 128)),
+                            _t((2, 3), torch.int64), _t(3, torch.int64), _t((8, 16, 2, 128)),
+                            _t((8, 16, 2, 128)), pair_axis, _t((10, 128), torch.float32))

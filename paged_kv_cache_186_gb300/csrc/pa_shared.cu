@@ -962,8 +962,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (begin) {
           m_used = m_step;
           k = k_new;
-        } else if (k_new != k || __any_sync(kFull, m_step > m_used + kRescaleThreshold)) {
+        } else if (k_new != k || __any_sync(kFull, valid && m_step > m_used + kRescaleThreshold)) {
           // raise the maximum, or follow V's factor: rescale O once its last product is done
+          // (for rows of the group only: where 128 is no multiple of G, the tile's last rows
+          // of Q hold what another CTA left there, which must not decide how these round)
           ok = wait(BAR_O + 2 * hf + ((x - 1) & 1), ((x - 1) >> 1) & 1);
           if (!ok) break;
           tc::fence_after_sync();

@@ -489,3 +489,20 @@ def test_without_always_a_short_prefix_of_long_contexts(kv, prefix, own, width):
 def test_weights_of_few_dominant_keys_keep_more_bits_than_bf16(where):
     # (bounds: beside the prefill's test; the own keys' weights are two bf16 terms here too)
     weights_of_few_keys_hold(where, [1] * 200, run, decode64)
+
+
+@pytest.mark.parametrize("group", [3, 5, 6, 7, 4])
+@pytest.mark.parametrize("kv, D, seqs", [("bf16", 128, 24), ("bf16", 64, 150), ("fp8", 128, 60),
+                                         ("int8", 128, 9)])
+def test_repeats_do_not_depend_on_what_shared_memory_holds(group, kv, D, seqs):
+    # 128 / group tokens leave rows of a tile's Q unwritten for these groups: calls of four heads in
+    # between fill all rows with other magnitudes
+    s = make([(2700, [2701 + 3 * i for i in range(seqs)])], group * 2, 2, D, 16, kv, seed=597, spread=2.0)
+    t = make([(1500, [1510 + i for i in range(seqs + 40)])], 8, 2, D, 16, kv, seed=598)
+    first = run(s)
+    assert_attention_close(first, decode64(s), "first")
+    q = t.q.clone()
+    for f in (0.0, 1.0, 30.0, -7.0, 0.1, 100.0, 3.0, 10.0):
+        t.q.copy_(q * f)
+        run(t)
+        assert torch.equal(run(s), first), f

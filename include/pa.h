@@ -464,7 +464,10 @@ pa_status pa_decode_window_append(const void* q, const void* k_new, const void* 
  * Arithmetic: bf16 operands on the tensor cores, fp32 scores and
  * accumulation, probabilities rounded to bf16 for P.V (as two bf16 terms,
  * bf16(p) + bf16(p - bf16(p)), on the first 128 keys of the query tiles that
- * hold rows seeing fewer than 128 keys), bf16 output. V of every key of a
+ * hold rows seeing fewer than 128 keys), bf16 output. One term is off by up to
+ * 2^-8 of a weight. The roundings of many weights average out; where a few of many
+ * keys hold a row's weight, its output may be off by up to 2^-8 of the largest |V|
+ * before its own rounding (1.6e-2 seen beyond that with V up to 5). V of every key of a
  * sequence must be finite: a row that does not see a key may give it the weight
  * 0.
  */

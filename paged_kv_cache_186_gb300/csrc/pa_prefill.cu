@@ -68,7 +68,8 @@
 //     with a cold L2, the windowed cases above 109 -> 99 us and 3.68 -> 3.31 ms).
 //   * The variant of pa_prefill_shared (SH) is a window whose first key is where
 //     the group's shared keys end, for all rows alike; it leaves (max, sum,
-//     unnormalised O) in fp32 for the merge (pa_shared.cu).
+//     unnormalised O) in fp32 for the merge (pa_shared.cu), and takes P as two terms
+//     on every tile where there are shared keys.
 //   * TMEM: 512 columns (S0, S1, O0, O1, 128 each); shared memory: Q0, Q1,
 //     two K and two V stages (192 KB).
 #include <algorithm>

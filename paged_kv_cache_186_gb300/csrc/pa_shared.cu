@@ -174,9 +174,9 @@ __global__ void __launch_bounds__(kPlanThreads) shared_plan_kernel(const SharedA
   // same products are spread evenly and full, but the call has a fixed cost, one
   // for each wave of the CTAs over the sequences' own keys, and one for each row
   // merged. In us, fitted on one GB300 over 2-64 sequences of 4-256 new tokens
-  // behind 512-16384 keys (shared / unshared measured): 64 drafts of 4-8 tokens
-  // behind 4096 98 / 219, 32 questions of 1-64 behind 8000 164 / 222, 32 of 128
-  // behind 8192 567 / 505, 8 of 32 behind 2048 53 / 31, 2 of 128 behind 8192 80 /
+  // behind 512-16384 keys (always shared / pa_prefill_varlen measured: 64 drafts of 4-8
+  // tokens behind 4096 91 / 216, 32 questions of 1-64 behind 8000 147 / 219, 32 of 128
+  // behind 8192 568 / 502, 8 of 32 behind 2048 48 / 30, 2 of 128 behind 8192 72 /
   // 129. (A decode step is chosen for on the host: its kernel's own cost is small.)
   if (!decode && !a.always) {
     const int span = a.own_tokens;  // new tokens of a sequence that one CTA takes

@@ -280,11 +280,12 @@ def test_weights_of_few_dominant_keys_keep_more_bits_than_bf16(where, new):
     # q of a kv head's heads is one direction and a little noise, three keys of the prefix or of each
     # sequence's own lie along it: their scores are near 11, those of the 600 others N(0, 1), so they
     # hold 98 % of the weight. An output is then off by at most
-    #   own keys: the scores' fp32 error (below 2^-12 of a weight in all) and 2^-17 of a weight,
-    #             P being two bf16 terms; with 2 % of the weight on keys of the other kind
+    #   own keys: the scores' fp32 error (below 2^-12 of a weight in all) and 2^-16 of a weight, the
+    #             second of P's two bf16 terms rounding what the first left, both by 2^-8; with 2 % of
+    #             the weight on keys of the other kind
     #   shared keys: 2^-11 of a weight (f16) instead
     # of the largest |V|, and twice that beyond the rounding of the exact result where the output
-    # rounds to the other side of it. One bf16 term would be off by 2^-9 of a weight.
+    # rounds to the other side of it. One bf16 term would be off by 2^-8 of a weight.
     weights_of_few_keys_hold(where, new, run, prefill64)
 
 
@@ -302,7 +303,7 @@ def weights_of_few_keys_hold(where, new, call, definition):
         s.k_cache[block, at] = (base + 0.15 * torch.randn((2, 128), generator=g)).to(torch.bfloat16).cuda()
     want = definition(s)
     got = n64(call(s))
-    bits = 2.0 ** -12 + (2.0 ** -17 + 0.02 * 2.0 ** -11 if where == "own" else 2.0 ** -11)
+    bits = 2.0 ** -12 + (2.0 ** -16 + 0.02 * 2.0 ** -11 if where == "own" else 2.0 ** -11)
     top = np.abs(n64(s.v_cache)).max()
     rounding = np.abs(n64(torch.from_numpy(want).float().to(torch.bfloat16)) - want)
     assert (np.abs(got - want) - rounding).max() <= 2 * bits * top

@@ -346,8 +346,9 @@ pa_status pa_decode_scored(const void* q, const pa_kv_cache* cache, const int32_
  *   PA_ERR_UNSUPPORTED. Arithmetic as pa_decode, but for the shared keys' weights
  *   in P.V, which are rounded to f16 (11 bits), and their V, which are f16 times a
  *   power of two: exact down to 2^-20 of the largest of 128 keys, then off by at
- *   most 2^-31 of it (or 2^-90 of the largest of all, if that is more). K and V of shared keys past the context_len of a shorter
- *   sequence of the group must be finite: it gives them the weight 0.
+ *   most 2^-31 of it (or 2^-90 of the largest of all, if that is more). K and V of
+ *   shared keys past the context_len of a shorter sequence of the group must be
+ *   finite: it gives them the weight 0. Repeats of a call give the same bits.
  */
 size_t pa_decode_shared_workspace_size(const pa_kv_cache* cache, int32_t batch, int32_t num_heads,
                                        int32_t max_blocks_per_seq, int32_t num_groups,

@@ -468,9 +468,9 @@ pa_status pa_decode_window_append(const void* q, const void* k_new, const void* 
  * hold rows seeing fewer than 128 keys), bf16 output. One term is off by up to
  * 2^-8 of a weight. The roundings of many weights average out; where a few of many
  * keys hold a row's weight, its output may be off by up to 2^-8 of the largest |V|
- * before its own rounding (1.6e-2 seen beyond that with V up to 5). V of every key of a
- * sequence must be finite: a row that does not see a key may give it the weight
- * 0.
+ * before its own rounding (2.4e-2 seen beyond that with V up to 5). V of every key
+ * of a sequence must be finite: a row that does not see a key may give it the
+ * weight 0.
  */
 pa_status pa_prefill_varlen(const void* q, const pa_kv_cache* cache, const int32_t* block_tables,
                             int32_t max_blocks_per_seq, const int32_t* cu_seqlens_q,
